@@ -910,6 +910,8 @@ dv_status layer_decode_impl(const dv_layer_desc *desc, const dv_layer_weights *w
 
 namespace dv {
 
+bool cuda_failed(cudaError_t e) { return failed(e); }
+
 bool ws_layout(const dv_layer_desc &D, int B, WsLayout *L)
 {
     if (check_desc(&D) != DV_OK || B < 1 || B > DV_MAX_BATCH)

@@ -55,6 +55,9 @@ private:
     std::mutex mu_;
 };
 
+// True if e is an error; it is kept for dv_cuda_error (dv_abi.cu).
+bool cuda_failed(cudaError_t e);
+
 enum RowKind { RK_PRED1 = 0, RK_PRED2 = 1, RK_QKV = 2, RK_FC1 = 3 };
 enum ColKind { CK_OPROJ = 0, CK_FC2 = 1 };
 

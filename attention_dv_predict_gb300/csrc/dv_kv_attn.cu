@@ -1,0 +1,223 @@
+// dv_kv_attn.cu -- attention over a KV cache for drafted trees and selected
+// blocks on CUDA cores: every storage type and head size (sm_103a).
+//
+// o_r = sum_p softmax_p(scale q_r . k_p) v_p over the positions that row r
+// sees, with the running max and sum of an online softmax in binary32.  A
+// group of D esize / 16 lanes covers one cached row with 16-byte loads and
+// serves four query rows with it; the groups of a warp, then the four warps
+// (16 positions of a 64-position tile each) are merged when a unit ends
+// (dv_kv_sched.cuh).  It serves binary32 caches and head sizes the
+// tensor-core kernel does not tile.
+#include "dv_kv_sched.cuh"
+
+namespace dv {
+namespace {
+
+constexpr int kGenThreads = 128;
+constexpr int kGenWarps = kGenThreads / 32;
+constexpr int RM = kKvGenRows;
+
+template <typename T>
+struct Cached;
+template <>
+struct Cached<float> {
+    static constexpr int EPC = 4;
+    DV_DEV static void unpack(const uint4 &v, float (&f)[4]) { Elem<float>::unpack(v, f); }
+};
+template <>
+struct Cached<__half> {
+    static constexpr int EPC = 8;
+    DV_DEV static void unpack(const uint4 &v, float (&f)[8]) { Elem<__half>::unpack(v, f); }
+};
+template <>
+struct Cached<int8_t> {
+    static constexpr int EPC = 16;
+    DV_DEV static void unpack(const uint4 &v, float (&f)[16])
+    {
+        const unsigned u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            f[i] = (float)(int8_t)(u[i / 4] >> (8 * (i % 4)));
+    }
+};
+
+DV_DEV float safe(float m) { return m == -INFINITY ? 0.f : m; }
+
+template <typename T, bool BLOCK>
+__global__ void __launch_bounds__(kGenThreads) k_kv_attn(const KvAttnArgs a)
+{
+    constexpr int EPC = Cached<T>::EPC;
+    __shared__ SchedSmem sm;
+    __shared__ __align__(16) float qs[RM][256];
+    __shared__ __align__(16) float wo[kGenWarps][RM][256];
+    __shared__ float wm[kGenWarps][RM], wl[kGenWarps][RM], um[RM], ul[RM];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int D = a.c.D, lpk = D / EPC, dc = lane % lpk, ks = lane / lpk, kpw = 32 / lpk;
+    const T *K = static_cast<const T *>(a.c.k);
+    const T *V = static_cast<const T *>(a.c.v);
+    const int G = a.H / a.c.Hkv;
+    const Run run = sched_init<BLOCK>(a, RM, sm);
+
+    for (long long w = run.lo; w < run.hi;) {
+        const Unit x = sched_unit<BLOCK>(a, RM, sm, run, w);
+        const long long wend = min(run.hi, x.w1);
+        const long long t0 = w - x.w0, t1 = wend - x.w0;
+        w = wend;
+        if (x.h < 0)
+            continue;
+        for (int i = threadIdx.x; i < RM * D; i += kGenThreads) {
+            const int r = i / D, d = i - r * D;
+            qs[r][d] = r < x.nrows ? ld_row(a.q, q_at<BLOCK>(a, x, r) + d) * a.scale : 0.f;
+        }
+        unsigned long long bits[RM];
+#pragma unroll
+        for (int r = 0; r < RM; ++r)
+            bits[r] = !BLOCK && r < x.nrows ? seen_bits(a, x, (x.row0 + r) / G) : 0ull;
+        __syncthreads();
+        const size_t base =
+            ((size_t)x.b * a.c.Hkv + (BLOCK ? x.h / G : x.h)) * (size_t)a.c.cap;
+        float m[RM], l[RM], o[RM][EPC];
+#pragma unroll
+        for (int r = 0; r < RM; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+#pragma unroll
+            for (int e = 0; e < EPC; ++e)
+                o[r][e] = 0.f;
+        }
+        for (long long t = t0; t < t1; ++t) {
+            constexpr int PW = kKvTile / kGenWarps;  // positions of a warp's share
+            for (int s = 0; s < PW; s += kpw) {
+                const int i = s + ks;
+                const long long at = t * kKvTile + warp * PW + i;
+                int p = -1;
+                if (i < PW) {
+                    if (BLOCK)
+                        p = block_pos(a, x, at);
+                    else
+                        p = at < x.len + x.ntok ? (int)at : -1;
+                }
+                uint4 kv = make_uint4(0u, 0u, 0u, 0u), vv = kv;
+                float ksc = 1.f, vsc = 1.f;
+                if (p >= 0) {
+                    kv = __ldcg(reinterpret_cast<const uint4 *>(K + (base + p) * D) + dc);
+                    vv = __ldcg(reinterpret_cast<const uint4 *>(V + (base + p) * D) + dc);
+                    if (a.c.dtype == DV_I8) {
+                        ksc = __ldcg(a.c.ks + base + p);
+                        vsc = __ldcg(a.c.vs + base + p);
+                    }
+                }
+                float kf[EPC], vf[EPC];
+                Cached<T>::unpack(kv, kf);
+                Cached<T>::unpack(vv, vf);
+#pragma unroll
+                for (int r = 0; r < RM; ++r) {
+                    float dot = 0.f;
+                    const float4 *qp = reinterpret_cast<const float4 *>(&qs[r][dc * EPC]);
+#pragma unroll
+                    for (int e = 0; e < EPC; e += 4) {
+                        const float4 q = qp[e / 4];
+                        dot = fmaf(q.x, kf[e], dot);
+                        dot = fmaf(q.y, kf[e + 1], dot);
+                        dot = fmaf(q.z, kf[e + 2], dot);
+                        dot = fmaf(q.w, kf[e + 3], dot);
+                    }
+                    for (int off = lpk / 2; off > 0; off >>= 1)
+                        dot += __shfl_xor_sync(0xffffffffu, dot, off);
+                    const int j = p - x.len;
+                    if (p >= 0 && (j < 0 || ((bits[r] >> j) & 1))) {
+                        dot *= ksc;
+                        const float mn = fmaxf(m[r], dot), ms = safe(mn);
+                        const float sc = exp2f(m[r] - ms);
+                        const float pe = exp2f(dot - ms);
+                        l[r] = fmaf(l[r], sc, pe);
+                        const float pv = pe * vsc;
+#pragma unroll
+                        for (int e = 0; e < EPC; ++e)
+                            o[r][e] = fmaf(o[r][e], sc, pv * vf[e]);
+                        m[r] = mn;
+                    }
+                }
+            }
+        }
+        // the key groups of the warp, then the warps
+#pragma unroll
+        for (int r = 0; r < RM; ++r) {
+            for (int off = lpk; off < 32; off <<= 1) {
+                const float m2 = __shfl_xor_sync(0xffffffffu, m[r], off);
+                const float l2 = __shfl_xor_sync(0xffffffffu, l[r], off);
+                const float mn = fmaxf(m[r], m2), ms = safe(mn);
+                const float s1 = exp2f(m[r] - ms), s2 = exp2f(m2 - ms);
+                l[r] = l[r] * s1 + l2 * s2;
+#pragma unroll
+                for (int e = 0; e < EPC; ++e)
+                    o[r][e] = o[r][e] * s1 + __shfl_xor_sync(0xffffffffu, o[r][e], off) * s2;
+                m[r] = mn;
+            }
+            if (ks == 0) {
+#pragma unroll
+                for (int e = 0; e < EPC; ++e)
+                    wo[warp][r][dc * EPC + e] = o[r][e];
+            }
+            if (lane == 0) {
+                wm[warp][r] = m[r];
+                wl[warp][r] = l[r];
+            }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < RM * D; i += kGenThreads) {
+            const int r = i / D, d = i - r * D;
+            float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+            for (int v = 0; v < kGenWarps; ++v)
+                M = fmaxf(M, wm[v][r]);
+            const float ms = safe(M);
+#pragma unroll
+            for (int v = 0; v < kGenWarps; ++v) {
+                const float s = exp2f(wm[v][r] - ms);
+                L += wl[v][r] * s;
+                O += wo[v][r][d] * s;
+            }
+            wo[0][r][d] = O;  // (this thread alone reads and writes column d of row r)
+            if (d == 0) {
+                um[r] = M;
+                ul[r] = L;
+            }
+        }
+        __syncthreads();
+        finish_unit<BLOCK>(a, RM, run, x, sm, &wo[0][0][0], 256, um, ul);
+    }
+}
+
+template <typename T>
+cudaError_t launch_gen(const KvAttnArgs &a, int grid, cudaStream_t st)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kGenThreads);
+    cfg.stream = st;
+    return a.idx ? cudaLaunchKernelEx(&cfg, k_kv_attn<T, true>, a)
+                 : cudaLaunchKernelEx(&cfg, k_kv_attn<T, false>, a);
+}
+
+}  // namespace
+
+KvPlan kv_plan(int, int, int)
+{
+    KvPlan p;
+    p.rows = kKvGenRows;
+    p.mma = false;
+    return p;
+}
+
+cudaError_t launch_kv_attn(const KvAttnArgs &a, const KvPlan &, int nsm, cudaStream_t st)
+{
+    const int grid = nsm * 4 < kKvMaxCtas ? nsm * 4 : kKvMaxCtas;
+    if (a.c.dtype == DV_I8)
+        return launch_gen<int8_t>(a, grid, st);
+    if (a.c.dtype == DV_F16)
+        return launch_gen<__half>(a, grid, st);
+    return launch_gen<float>(a, grid, st);
+}
+
+}  // namespace dv

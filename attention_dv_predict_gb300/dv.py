@@ -26,10 +26,12 @@ _lib = C.CDLL(LIB_PATH)
 
 DV_OK, DV_ERR_INVALID_ARG, DV_ERR_UNSUPPORTED, DV_ERR_CUDA = 0, 1, 2, 3
 DV_ERR_TIMEOUT, DV_ERR_WORKSPACE, DV_ERR_DEVICE_INDEX, DV_ERR_SCRATCH_LIMIT = 4, 5, 6, 7
-DV_F32, DV_F16 = 0, 1
+DV_F32, DV_F16, DV_I8 = 0, 1, 2
 DV_LAYERNORM, DV_RMSNORM = 0, 1
 DV_MLP_RELU, DV_MLP_SWIGLU = 0, 1
 DV_MAX_BATCH = 32
+DV_KV_MAX_BATCH = 256
+DV_TREE_MAX_TOKENS = 64
 
 WEIGHT_FIELDS = ("ln1_g", "ln1_b", "w_qkv", "b_qkv", "w_oT", "b_o", "ln2_g", "ln2_b",
                  "w1", "b1", "w2T", "b2", "pred_h", "pred_a", "pred_b")
@@ -50,12 +52,30 @@ class Selection(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("idx_h", "idx_n", "u_h", "n_u_h", "u_n", "n_u_n")]
 
 
+class KvDesc(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("n_heads", "n_kv_heads", "head_dim", "kv_cap", "dtype",
+                                         "block")]
+
+
+class KvCachePointers(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "k_mean",
+                                          "k_mean_scale")]
+
+
+class KvRows(C.Structure):
+    _fields_ = [("p", C.c_void_p), ("dtype", C.c_int32), ("stride_b", C.c_int64),
+                ("stride_t", C.c_int64), ("stride_h", C.c_int64)]
+
+
 _P = C.c_void_p
 _I = C.c_int
 _SZ = C.c_size_t
 _D = C.POINTER(LayerDesc)
 _W = C.POINTER(LayerWeights)
 _S = C.POINTER(Selection)
+_KD = C.POINTER(KvDesc)
+_KC = C.POINTER(KvCachePointers)
+_KR = C.POINTER(KvRows)
 
 _SIGS = {
     "dv_status_string": ([_I], C.c_char_p),
@@ -86,6 +106,14 @@ _SIGS = {
     "dv_layer_decode_host": ([_D, _W, _P, _P, _I, _I, _I, _P, _P, _I, _S, _P, _P, _SZ, _P], _I),
     "dv_hbm_copy": ([_P, _P, _SZ, _P], _I),
     "dv_test_hold_wait": ([_P, _SZ, _I, _I, _P], _I),
+    "dv_kv_workspace_size": ([_KD, _I, _I], _SZ),
+    "dv_kv_append": ([_KD, _KC, _KR, _KR, _I, _I, _P, _P, _P, _SZ, _P], _I),
+    "dv_kv_read": ([_KD, _KC, _I, _I, _P, _I, _P, _P, _P, _SZ, _P], _I),
+    "dv_kv_keep": ([_KD, _KC, _I, _I, _P, _P, _P, _P, _SZ, _P], _I),
+    "dv_tree_attn": ([_KD, _KC, _KR, _I, _I, _P, _P, _P, C.c_float, _P, _P, _I, _P, _P, _SZ, _P],
+                     _I),
+    "dv_block_topk": ([_KD, _KC, _KR, _I, _P, _I, _I, _I, _P, _P, _SZ, _P], _I),
+    "dv_block_attn": ([_KD, _KC, _KR, _I, _P, _P, _I, C.c_float, _P, _P, _SZ, _P], _I),
 }
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -380,3 +408,202 @@ def dv_test_hold_wait(ws: Workspace, wait_id: int, budget_us: int, stream=None):
 def dv_hbm_copy(dst: torch.Tensor, src: torch.Tensor, nbytes: Optional[int] = None, stream=None):
     n = src.numel() * src.element_size() if nbytes is None else nbytes
     _check("dv_hbm_copy", _lib.dv_hbm_copy(_ptr(dst), _ptr(src), n, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# KV-cache operators.
+
+
+_TORCH_DTYPE = {DV_F32: torch.float32, DV_F16: torch.float16, DV_I8: torch.int8}
+_ROW_DTYPE = {torch.float32: DV_F32, torch.float16: DV_F16}
+
+
+def make_kv_desc(n_heads, n_kv_heads, head_dim, kv_cap, dtype, block=0) -> KvDesc:
+    return KvDesc(n_heads, n_kv_heads, head_dim, kv_cap, dtype, block)
+
+
+def kv_workspace_size(desc: KvDesc, batch: int, tokens: int = 1) -> int:
+    return int(_lib.dv_kv_workspace_size(C.byref(desc), int(batch), int(tokens)))
+
+
+def _kv_tensors(desc: KvDesc, batch: int):
+    """Shape and type of each of a cache's tensors."""
+    B, H, cap, D = batch, desc.n_kv_heads, desc.kv_cap, desc.head_dim
+    t = {n: ((B, H, cap, D), _TORCH_DTYPE[desc.dtype]) for n in ("k", "v")}
+    if desc.dtype == DV_I8:
+        t.update({n: ((B, H, cap), torch.float32) for n in ("k_scale", "v_scale")})
+    if desc.block:
+        nb = cap // desc.block
+        t["k_mean"] = ((B, H, nb, D), torch.int8)
+        t["k_mean_scale"] = ((B, H, nb), torch.float32)
+    return t
+
+
+class KvCache:
+    """The tensors of one KV cache (attributes ``k``, ``v``, and where the
+    descriptor has them ``k_scale``, ``v_scale``, ``k_mean``,
+    ``k_mean_scale``) plus the C struct pointing at them.  ``tensors``: use
+    these instead of allocating (zeroed) ones."""
+
+    def __init__(self, desc: KvDesc, batch: int, device=None,
+                 tensors: Optional[Dict[str, torch.Tensor]] = None):
+        if kv_workspace_size(desc, batch) == 0:
+            raise DvError("dv_kv_workspace_size", DV_ERR_INVALID_ARG)
+        self.desc, self.batch = desc, batch
+        want = _kv_tensors(desc, batch)
+        if tensors is None:
+            dev = device or "cuda"
+            tensors = {n: torch.zeros(shape, dtype=dt, device=dev)
+                       for n, (shape, dt) in want.items()}
+        if set(tensors) != set(want):
+            raise ValueError(f"this cache has the tensors {sorted(want)}, got {sorted(tensors)}")
+        self.device = tensors["k"].device
+        for n, (shape, dt) in want.items():
+            t = tensors[n]
+            if (tuple(t.shape) != shape or t.dtype != dt or not t.is_cuda
+                    or not t.is_contiguous() or t.device != self.device):
+                raise ValueError(f"cache tensor {n} must be a contiguous CUDA tensor {shape} of "
+                                 f"{dt} on one device")
+            setattr(self, n, t)
+        self.c = KvCachePointers(*[_ptr(getattr(self, n, None)) if n in want else None
+                                   for n, _ in KvCachePointers._fields_])
+        self._refs = (C.byref(self.desc), C.byref(self.c))
+
+
+class KvWorkspace(Workspace):
+    """Device workspace of the KV-cache operators, zeroed once: for caches of
+    ``desc`` with up to ``tokens`` query tokens a row."""
+
+    def __init__(self, desc: KvDesc, batch: int, tokens: int = 1, device=None, stream=None):
+        n = kv_workspace_size(desc, batch, tokens)
+        if n == 0:
+            raise DvError("dv_kv_workspace_size", DV_ERR_INVALID_ARG)
+        self.buf = torch.empty(n + 256, dtype=torch.uint8, device=device or "cuda")
+        self.device = self.buf.device
+        off = (-self.buf.data_ptr()) % 256
+        self.ptr = self.buf.data_ptr() + off
+        self.nbytes = n
+        with torch.cuda.device(self.device):
+            _check("dv_workspace_init", _lib.dv_workspace_init(C.c_void_p(self.ptr), n,
+                                                                _stream(stream)))
+
+
+def _kv_dev(cache: KvCache, ws: KvWorkspace, stream):
+    """The stream of a call; its device must be the cache's and the current one."""
+    if ws.device != cache.device:
+        raise ValueError("the workspace is not on the cache's device")
+    if torch.cuda.current_device() != cache.device.index:
+        raise ValueError("the cache is not on the current device (torch.cuda.device)")
+    if stream is not None and stream.device != cache.device:
+        raise ValueError("the stream is not of the cache's device")
+    return _stream(stream)
+
+
+def _kv_tensor(name: str, t: Optional[torch.Tensor], cache: KvCache, shape, dtype):
+    if t is None:
+        return None
+    if (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()
+            or t.device != cache.device):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on the "
+                         "cache's device")
+    return t.data_ptr()
+
+
+def _kv_rows(name: str, t: torch.Tensor, cache: KvCache, shape) -> KvRows:
+    if (t.dtype not in _ROW_DTYPE or tuple(t.shape) != tuple(shape) or t.device != cache.device
+            or (t.stride(-1) != 1 and t.shape[-1] != 1)):
+        raise ValueError(f"{name} must be a float32 or float16 tensor {tuple(shape)} on the "
+                         "cache's device, contiguous in its last dimension")
+    # (a dimension of one row is never stepped over: its stride says nothing)
+    s = [0 if n == 1 else st for n, st in zip(t.shape, t.stride())]
+    if t.dim() == 3:  # (b, h): one query per row
+        s.insert(1, 0)
+    return KvRows(t.data_ptr(), _ROW_DTYPE[t.dtype], s[0], s[1], s[2])
+
+
+def dv_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, lens: torch.Tensor,
+                 ws: KvWorkspace, n_tok: Optional[torch.Tensor] = None, stream=None):
+    """Write k, v [B, T, Hkv, D] (any strides over the first three) at positions lens[b] + t."""
+    d, B, T = cache.desc, cache.batch, k.shape[1]
+    st = _kv_dev(cache, ws, stream)
+    shape = (B, T, d.n_kv_heads, d.head_dim)
+    _check("dv_kv_append", _lib.dv_kv_append(
+        *cache._refs, C.byref(_kv_rows("k", k, cache, shape)),
+        C.byref(_kv_rows("v", v, cache, shape)), B, T,
+        _kv_tensor("lens", lens, cache, (B,), torch.int32),
+        _kv_tensor("n_tok", n_tok, cache, (B,), torch.int32), ws.ptr, ws.nbytes, st))
+
+
+def dv_kv_read(cache: KvCache, start: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor,
+               ws: KvWorkspace, stream=None):
+    """Positions start[b] .. start[b] + T - 1 into k_out, v_out [B, Hkv, T, D] (float32/float16)."""
+    d, B, T = cache.desc, cache.batch, k_out.shape[2]
+    st = _kv_dev(cache, ws, stream)
+    if k_out.dtype not in _ROW_DTYPE:
+        raise ValueError("k_out must be float32 or float16")
+    shape = (B, d.n_kv_heads, T, d.head_dim)
+    _check("dv_kv_read", _lib.dv_kv_read(
+        *cache._refs, B, T, _kv_tensor("start", start, cache, (B,), torch.int32),
+        _ROW_DTYPE[k_out.dtype], _kv_tensor("k_out", k_out, cache, shape, k_out.dtype),
+        _kv_tensor("v_out", v_out, cache, shape, k_out.dtype), ws.ptr, ws.nbytes, st))
+
+
+def dv_kv_keep(cache: KvCache, lens: torch.Tensor, path: torch.Tensor, n_keep: torch.Tensor,
+               ws: KvWorkspace, stream=None):
+    """Move position lens[b] + path[b, i] to lens[b] + i for i < n_keep[b] (path [B, T] ascending)."""
+    B, T = cache.batch, path.shape[1]
+    st = _kv_dev(cache, ws, stream)
+    _check("dv_kv_keep", _lib.dv_kv_keep(
+        *cache._refs, B, T, _kv_tensor("lens", lens, cache, (B,), torch.int32),
+        _kv_tensor("path", path, cache, (B, T), torch.int32),
+        _kv_tensor("n_keep", n_keep, cache, (B,), torch.int32), ws.ptr, ws.nbytes, st))
+
+
+def dv_tree_attn(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, out: torch.Tensor,
+                 ws: KvWorkspace, mask: Optional[torch.Tensor] = None,
+                 n_tok: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                 u_h: Optional[torch.Tensor] = None, n_u_h: Optional[torch.Tensor] = None,
+                 stream=None):
+    """Attention of q [B, T, H, D] over the cache; mask [B, T] int64 (bit j: sees drafted token j).
+
+    scale: head_dim ** -0.5 by default.  u_h, n_u_h: a device list of KV heads and its length."""
+    d, B, T = cache.desc, cache.batch, q.shape[1]
+    st = _kv_dev(cache, ws, stream)
+    shape = (B, T, d.n_heads, d.head_dim)
+    if (u_h is None) != (n_u_h is None):
+        raise ValueError("u_h and n_u_h go together")
+    m = 0 if u_h is None else u_h.numel()
+    _check("dv_tree_attn", _lib.dv_tree_attn(
+        *cache._refs, C.byref(_kv_rows("q", q, cache, shape)), B, T,
+        _kv_tensor("lens", lens, cache, (B,), torch.int32),
+        _kv_tensor("n_tok", n_tok, cache, (B,), torch.int32),
+        _kv_tensor("mask", mask, cache, (B, T), torch.int64),
+        d.head_dim ** -0.5 if scale is None else scale,
+        _kv_tensor("u_h", u_h, cache, (m,), torch.int32),
+        _kv_tensor("n_u_h", n_u_h, cache, (1,), torch.int32), m,
+        _kv_tensor("out", out, cache, shape, torch.float32), ws.ptr, ws.nbytes, st))
+
+
+def dv_block_topk(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, idx: torch.Tensor,
+                  ws: KvWorkspace, n_first: int = 1, n_last: int = 1, stream=None):
+    """The idx.shape[2] blocks each query of q [B, H, D] attends to, into idx [B, H, k] (-1 behind)."""
+    d, B, k = cache.desc, cache.batch, idx.shape[2]
+    st = _kv_dev(cache, ws, stream)
+    _check("dv_block_topk", _lib.dv_block_topk(
+        *cache._refs, C.byref(_kv_rows("q", q, cache, (B, d.n_heads, d.head_dim))), B,
+        _kv_tensor("lens", lens, cache, (B,), torch.int32), k, n_first, n_last,
+        _kv_tensor("idx", idx, cache, (B, d.n_heads, k), torch.int32), ws.ptr, ws.nbytes, st))
+
+
+def dv_block_attn(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, idx: torch.Tensor,
+                  out: torch.Tensor, ws: KvWorkspace, scale: Optional[float] = None, stream=None):
+    """Attention of q [B, H, D] over the blocks listed in idx [B, H, k], into out [B, H, D]."""
+    d, B, k = cache.desc, cache.batch, idx.shape[2]
+    st = _kv_dev(cache, ws, stream)
+    shape = (B, d.n_heads, d.head_dim)
+    _check("dv_block_attn", _lib.dv_block_attn(
+        *cache._refs, C.byref(_kv_rows("q", q, cache, shape)), B,
+        _kv_tensor("lens", lens, cache, (B,), torch.int32),
+        _kv_tensor("idx", idx, cache, (B, d.n_heads, k), torch.int32), k,
+        d.head_dim ** -0.5 if scale is None else scale,
+        _kv_tensor("out", out, cache, shape, torch.float32), ws.ptr, ws.nbytes, st))

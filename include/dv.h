@@ -73,7 +73,8 @@ typedef enum {
     DV_ERR_SCRATCH_LIMIT = 7 /* dv_predict_topk_noalloc: shape needs more than its scratch */
 } dv_status;
 
-typedef enum { DV_F32 = 0, DV_F16 = 1 } dv_dtype;
+/* DV_I8 is a storage type of the KV-cache operators (dv_kv_desc) alone. */
+typedef enum { DV_F32 = 0, DV_F16 = 1, DV_I8 = 2 } dv_dtype;
 typedef enum { DV_LAYERNORM = 0, DV_RMSNORM = 1 } dv_norm;
 /* MLP of the layer: OPT's fc1, ReLU, fc2 (w1 [N, d], w2T [N, d]) or the
  * LLaMA-style SwiGLU (gate and up rows of neuron j interleaved in w1
@@ -424,6 +425,166 @@ int dv_predict_topk_noalloc(const dv_layer_desc *desc, const dv_layer_weights *w
                             const float *x_pred, int batch, int k_heads, int k_neurons,
                             const dv_selection *sel, float *scores_h, float *scores_n,
                             void *stream);
+
+/*
+ * KV-cache operators: a cache that is written quantised and read back,
+ * attention for a tree of drafted tokens over it, and attention over the
+ * blocks of positions that a cheap score selects -- contextual sparsity along
+ * the cached positions, beside the heads and neurons above.  They are an
+ * addition of this library; the DejaVu pages have no counterpart.
+ *
+ * They serve caches of their own: every batch row has its own length (device
+ * memory), query heads may share KV heads in groups of n_heads / n_kv_heads
+ * (query head h reads KV head h / group), and rows may be held in 8 bits.
+ * The conventions at the top of this file hold; the workspace is one of
+ * dv_kv_workspace_size() bytes (not one of the layer calls'), zeroed once
+ * with dv_workspace_init() and read by dv_check().  It may be shared by calls
+ * of any shapes that fit it, one after another.
+ *
+ * Device-side checks: a batch row whose length, token count, path or list of
+ * blocks is out of range is skipped, its outputs and cache rows are left as
+ * they were (a bad entry of a list of heads or blocks alone is skipped), and
+ * DV_ERR_DEVICE_INDEX is recorded in the status word.
+ *
+ * Cache: k, v [B, Hkv, kv_cap, D] in desc.dtype.  DV_I8 holds a row of D
+ * values as codes c in [-127, 127] (int8) and one scale s (k_scale, v_scale
+ * [B, Hkv, kv_cap], binary32): value = c s, with s = max(amax |x| / 127,
+ * 2^-126) and c = x / s rounded to the nearest whole number, ties to even
+ * (both quotients in binary32).  A row that holds a NaN or an infinity is
+ * stored with s = NaN and codes 0.
+ * Block means (desc.block = n > 0): k_mean [B, Hkv, kv_cap / n, D] (int8) and
+ * k_mean_scale [B, Hkv, kv_cap / n] hold the mean of the n keys of every
+ * complete aligned block of positions, quantised like a row.  dv_kv_append
+ * and dv_kv_keep write a block's mean when they write its last position (the
+ * other n - 1 must be in the cache by then).  The mean's sum is taken over
+ * the keys as stored, each rounded to a multiple of n 2^(e - 24) with 2^e the
+ * power of two above the block's largest magnitude (e >= -100), so that it is
+ * exact in any order.  A block with a NaN or an infinity has codes 0 and
+ * scale +infinity.
+ */
+#define DV_KV_MAX_BATCH 256
+#define DV_TREE_MAX_TOKENS 64
+
+typedef struct {
+    int32_t n_heads;    /* query heads: a multiple of n_kv_heads, at most 256 */
+    int32_t n_kv_heads;
+    int32_t head_dim;   /* power of two, at most 256; head_dim * sizeof(dtype) in [16, 512] */
+    int32_t kv_cap;     /* positions per (batch row, KV head), at most 2^28 */
+    int32_t dtype;      /* DV_F32, DV_F16 or DV_I8 */
+    int32_t block;      /* 0 (no block means), or 16, 32, 64 or 128 <= kv_cap (head_dim >= 16,
+                         * fewer than 16384 blocks) */
+} dv_kv_desc;
+
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale; /* DV_I8 only */
+    int8_t *k_mean;           /* block > 0 only */
+    float *k_mean_scale;
+} dv_kv_cache;
+
+/* Rows of head_dim contiguous values (DV_F32 or DV_F16): row (b, t, h) at
+ * p + b stride_b + t stride_t + h stride_h, strides in elements, each a
+ * non-negative multiple of 16 bytes (p 16-byte aligned); any slice of a
+ * projection's output. */
+typedef struct {
+    const void *p;
+    int32_t dtype;
+    int64_t stride_b, stride_t, stride_h;
+} dv_kv_rows;
+
+/* Bytes of workspace the calls below need for this cache with up to `tokens`
+ * query tokens a row (dv_tree_attn; 1 serves the others).  0 if invalid. */
+size_t dv_kv_workspace_size(const dv_kv_desc *desc, int batch, int tokens);
+
+/*
+ * dv_kv_append -- write new keys and values, quantised for a DV_I8 cache.
+ *   k, v: rows (b, t, h), t < tokens, h < n_kv_heads; token t of row b goes
+ *   to position lens[b] + t, for t < n_tok[b] (n_tok [B], NULL: tokens).
+ *   lens [B] device, lens[b] + n_tok[b] <= kv_cap; it is not advanced.
+ * Rounding to binary16 is to nearest (a value above 65504 becomes infinite).
+ */
+int dv_kv_append(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_rows *k,
+                 const dv_kv_rows *v, int batch, int tokens, const int32_t *lens,
+                 const int32_t *n_tok, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * dv_kv_read -- read cached rows back as numbers: positions start[b] ..
+ * start[b] + tokens - 1 of every head into k_out, v_out [B, Hkv, tokens, D]
+ * in out_dtype (DV_F32, or DV_F16 rounded to nearest: the layout of a layer's
+ * KV cache with kv_cap = tokens).  start[b] + tokens <= kv_cap.
+ */
+int dv_kv_read(const dv_kv_desc *desc, const dv_kv_cache *cache, int batch, int tokens,
+               const int32_t *start, int out_dtype, void *k_out, void *v_out, void *ws,
+               size_t ws_bytes, void *stream);
+
+/*
+ * dv_kv_keep -- after a draft has been verified: the cached rows of the
+ * accepted path move together.  For i < n_keep[b], position lens[b] +
+ * path[b][i] moves to lens[b] + i (codes and scales as they are).
+ *   path [B, tokens] device, strictly ascending over its first n_keep[b]
+ *   entries, each in [0, tokens); tokens <= DV_TREE_MAX_TOKENS.
+ * Positions from lens[b] + n_keep[b] on keep what they held.
+ */
+int dv_kv_keep(const dv_kv_desc *desc, const dv_kv_cache *cache, int batch, int tokens,
+               const int32_t *lens, const int32_t *path, const int32_t *n_keep, void *ws,
+               size_t ws_bytes, void *stream);
+
+/*
+ * dv_tree_attn -- attention of the drafted tokens of every row over its
+ * cached prefix and over each other.
+ *   q: rows (b, t, h), t < tokens <= DV_TREE_MAX_TOKENS, h < n_heads.  The
+ *   drafted tokens' own keys and values are in the cache at positions lens[b]
+ *   + t (dv_kv_append), t < n_tok[b] (NULL: tokens).
+ *   mask [B, tokens] device: bit j of mask[b][t]: token t sees drafted token
+ *   j (itself included only if bit t is set; bits from n_tok[b] on are
+ *   ignored).  NULL: token t sees drafted tokens 0 .. t.
+ *   out [B, tokens, n_heads, D] binary32:
+ *     out[b, t, h] = sum_p softmax_p(scale q . k_p) v_p
+ *   over positions p < lens[b] and the drafted ones it sees; zeros where it
+ *   sees none.  Tokens t >= n_tok[b] and heads that are not listed are left
+ *   as they were.  A position that a token does not see cannot change its
+ *   result, whatever it holds; one that it sees and that holds a NaN or an
+ *   infinity makes the result non-finite.
+ *   u_h, n_u_h, max_u_h: device list of KV heads to compute, as
+ *   dv_sparse_attn's (NULL, NULL, 0: every head; max_u_h <= n_kv_heads).
+ * tokens = 1 is decode attention with one length a row.  Scores, weights and
+ * sums are binary32 to its last bits for every cache type: on tensor cores
+ * queries and weights are split into two binary16 parts.  One launch; the
+ * order of every sum is fixed by the shapes and lengths.
+ */
+int dv_tree_attn(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_rows *q, int batch,
+                 int tokens, const int32_t *lens, const int32_t *n_tok, const uint64_t *mask,
+                 float scale, const int32_t *u_h, const int32_t *n_u_h, int max_u_h, float *out,
+                 void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * dv_block_topk -- the blocks of cached positions each query attends to.
+ * desc.block = n > 0; row b has nb = ceil(lens[b] / n) blocks.
+ *   q: rows (b, 0, h) (stride_t is not used), one query per row and head.
+ *   Score of block j: the query is quantised like a cached row to codes qc;
+ *   score = float(sum_d qc_d k_mean[j]_d) k_mean_scale[j] (the sum is a whole
+ *   number below 2^24), +infinity where the scale is.
+ *   The first n_first and the last n_last >= 1 blocks are taken, and of the
+ *   others the k_blocks - n_first - n_last with the largest scores (ties to
+ *   the lower block).
+ *   idx [B, n_heads, k_blocks]: ascending; -1 behind the last of nb blocks.
+ * The workspace holds its status word only.
+ */
+int dv_block_topk(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_rows *q, int batch,
+                  const int32_t *lens, int k_blocks, int n_first, int n_last, int32_t *idx,
+                  void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * dv_block_attn -- attention of one query per row and head over its listed
+ * blocks (positions p < lens[b] of them).
+ *   idx [B, n_heads, k_blocks]: distinct blocks in any order, -1 for none;
+ *   only the first min(k_blocks, ceil(lens[b] / n)) entries are read.
+ *   out [B, n_heads, D] binary32; zeros where no position is left.
+ * Arithmetic as dv_tree_attn's.
+ */
+int dv_block_attn(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_rows *q, int batch,
+                  const int32_t *lens, const int32_t *idx, int k_blocks, float scale, float *out,
+                  void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }
