@@ -98,6 +98,7 @@ cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t st);
 cudaError_t launch_kv_read(const KvReadArgs &a, cudaStream_t st);
 cudaError_t launch_kv_keep(const KvKeepArgs &a, cudaStream_t st);
 cudaError_t launch_kv_topk(const KvTopkArgs &a, cudaStream_t st);
+cudaError_t launch_kv_mma(const KvAttnArgs &a, int rows, int nsm, cudaStream_t st);
 cudaError_t launch_kv_attn(const KvAttnArgs &a, const KvPlan &p, int nsm, cudaStream_t st);
 
 }  // namespace dv

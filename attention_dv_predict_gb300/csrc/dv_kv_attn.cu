@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kGenThreads) k_kv_attn(const KvAttnArgs a)
             }
         }
         __syncthreads();
-        finish_unit<BLOCK>(a, RM, run, x, sm, &wo[0][0][0], 256, um, ul);
+        finish_unit<BLOCK>(a, RM, run, x, sm, [&](int r, int d) { return wo[0][r][d]; }, um, ul);
     }
 }
 
@@ -202,16 +202,20 @@ cudaError_t launch_gen(const KvAttnArgs &a, int grid, cudaStream_t st)
 
 }  // namespace
 
-KvPlan kv_plan(int, int, int)
+// The tensor-core kernel serves binary16 and 8-bit rows of 64 and 128 values;
+// units of 8, 16, 32 or 64 query rows, the smallest that holds a token set.
+KvPlan kv_plan(int dtype, int D, int rows)
 {
     KvPlan p;
-    p.rows = kKvGenRows;
-    p.mma = false;
+    p.mma = dtype != DV_F32 && (D == 64 || D == 128);
+    p.rows = !p.mma ? kKvGenRows : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     return p;
 }
 
-cudaError_t launch_kv_attn(const KvAttnArgs &a, const KvPlan &, int nsm, cudaStream_t st)
+cudaError_t launch_kv_attn(const KvAttnArgs &a, const KvPlan &p, int nsm, cudaStream_t st)
 {
+    if (p.mma)
+        return launch_kv_mma(a, p.rows, nsm, st);
     const int grid = nsm * 4 < kKvMaxCtas ? nsm * 4 : kKvMaxCtas;
     if (a.c.dtype == DV_I8)
         return launch_gen<int8_t>(a, grid, st);

@@ -190,20 +190,19 @@ DV_DEV int block_pos(const KvAttnArgs &a, const Unit &x, long long i)
 
 DV_DEV float row_result(float o, float l) { return l == 0.f ? 0.f : o / l; }
 
-// A run's part of a unit is done: so [rows][D] (stride ld), sm_m, sm_l [rows]
-// hold it merged over the CTA (visible to every thread; m in units of log2).
+// A run's part of a unit is done: so(row, d), sm_m, sm_l [rows] give it
+// merged over the CTA (visible to every thread; m in units of log2).
 // Writes the result, or a piece, and merges the pieces if it is the last.
 // Barriers inside; the buffers may be reused after it returns.
-template <bool BLOCK>
+template <bool BLOCK, class F>
 DV_DEV void finish_unit(const KvAttnArgs &a, int rows, const Run &r, const Unit &x,
-                        SchedSmem &sm, const float *so, int ld, const float *sm_m,
-                        const float *sm_l)
+                        SchedSmem &sm, F so, const float *sm_m, const float *sm_l)
 {
     const int D = a.c.D, n = x.nrows * D;
     if (r.lo <= x.w0 && x.w1 <= r.hi) {
         for (int i = threadIdx.x; i < n; i += blockDim.x) {
             const int row = i / D, d = i - row * D;
-            a.out[out_at<BLOCK>(a, x, row) + d] = row_result(so[row * ld + d], sm_l[row]);
+            a.out[out_at<BLOCK>(a, x, row) + d] = row_result(so(row, d), sm_l[row]);
         }
         __syncthreads();
         return;
@@ -212,7 +211,7 @@ DV_DEV void finish_unit(const KvAttnArgs &a, int rows, const Run &r, const Unit 
     float *rec = a.rec + (2 * (size_t)r.c + (x.w0 > r.lo)) * rsz;
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const int row = i / D, d = i - row * D;
-        __stcg(rec + i, so[row * ld + d]);
+        __stcg(rec + i, so(row, d));
     }
     for (int i = threadIdx.x; i < x.nrows; i += blockDim.x) {
         __stcg(rec + rows * D + i, sm_m[i]);
