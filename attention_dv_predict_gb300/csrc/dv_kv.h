@@ -78,6 +78,7 @@ struct KvAttnArgs {
     int max_u_h;
     const int32_t *idx;    // block mode: [B][H][k]
     int k;
+    int blog;              // log2(block)
     int B, H, T;
     float scale;           // softmax scale x log2(e)
     float *out;            // [B][T][H][D]

@@ -135,6 +135,8 @@ int dv_kv_append(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_r
     if ((s = check_cache(*desc, cache, batch, &a.c)) || (s = check_rows(k, &a.k)) ||
         (s = check_rows(v, &a.v)))
         return s;
+    if (a.k.f16 != a.v.f16)
+        return DV_ERR_INVALID_ARG;
     if (tokens < 1 || tokens > desc->kv_cap || !aligned(lens, 4) || (n_tok && !aligned(n_tok, 4)))
         return DV_ERR_INVALID_ARG;
     if ((s = check_ws(*desc, 1, ws, ws_bytes)))
@@ -288,6 +290,8 @@ int dv_block_attn(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_
     a.lens = lens;
     a.idx = idx;
     a.k = k_blocks;
+    while ((1 << a.blog) < desc->block)
+        ++a.blog;
     a.B = batch;
     a.H = desc->n_heads;
     a.T = 1;

@@ -51,6 +51,8 @@ __global__ void __launch_bounds__(kGenThreads) k_kv_attn(const KvAttnArgs a)
     __shared__ __align__(16) float qs[RM][256];
     __shared__ __align__(16) float wo[kGenWarps][RM][256];
     __shared__ float wm[kGenWarps][RM], wl[kGenWarps][RM], um[RM], ul[RM];
+    __shared__ float wgt[kMergePieces][RM];
+    __shared__ __align__(16) float so[RM * 256];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int D = a.c.D, lpk = D / EPC, dc = lane % lpk, ks = lane / lpk, kpw = 32 / lpk;
     const T *K = static_cast<const T *>(a.c.k);
@@ -61,7 +63,7 @@ __global__ void __launch_bounds__(kGenThreads) k_kv_attn(const KvAttnArgs a)
     for (long long w = run.lo; w < run.hi;) {
         const Unit x = sched_unit<BLOCK>(a, RM, sm, run, w);
         const long long wend = min(run.hi, x.w1);
-        const long long t0 = w - x.w0, t1 = wend - x.w0;
+        const int t0 = (int)(w - x.w0), t1 = (int)(wend - x.w0);
         w = wend;
         if (x.h < 0)
             continue;
@@ -85,17 +87,17 @@ __global__ void __launch_bounds__(kGenThreads) k_kv_attn(const KvAttnArgs a)
             for (int e = 0; e < EPC; ++e)
                 o[r][e] = 0.f;
         }
-        for (long long t = t0; t < t1; ++t) {
+        for (int t = t0; t < t1; ++t) {
             constexpr int PW = kKvTile / kGenWarps;  // positions of a warp's share
             for (int s = 0; s < PW; s += kpw) {
                 const int i = s + ks;
-                const long long at = t * kKvTile + warp * PW + i;
+                const int at = t * kKvTile + warp * PW + i;
                 int p = -1;
                 if (i < PW) {
                     if (BLOCK)
                         p = block_pos(a, x, at);
                     else
-                        p = at < x.len + x.ntok ? (int)at : -1;
+                        p = at < x.len + x.ntok ? at : -1;
                 }
                 uint4 kv = make_uint4(0u, 0u, 0u, 0u), vv = kv;
                 float ksc = 1.f, vsc = 1.f;
@@ -178,14 +180,16 @@ __global__ void __launch_bounds__(kGenThreads) k_kv_attn(const KvAttnArgs a)
                 L += wl[v][r] * s;
                 O += wo[v][r][d] * s;
             }
-            wo[0][r][d] = O;  // (this thread alone reads and writes column d of row r)
+            so[i] = O;
             if (d == 0) {
                 um[r] = M;
                 ul[r] = L;
             }
         }
         __syncthreads();
-        finish_unit<BLOCK>(a, RM, run, x, sm, [&](int r, int d) { return wo[0][r][d]; }, um, ul);
+        finish_unit<BLOCK, RM, kGenThreads>(
+            a, run, x, sm, so, um, ul, wgt, [&](int r, int d) { return r * D + d; },
+            [&](int i) { return i / D; });
     }
 }
 

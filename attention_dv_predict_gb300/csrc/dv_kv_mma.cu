@@ -80,21 +80,6 @@ DV_DEV unsigned h2_rest(float a, float b, unsigned hi)
     return h2(a - f.x, b - f.y);
 }
 
-// Pairs of codes to binary16: a code's byte with its sign bit flipped is
-// code + 128, which under the byte 0x64 reads 1024 + 128 + code.
-DV_DEV unsigned codes_lo(unsigned biased)  // bytes 0, 1
-{
-    unsigned u = __byte_perm(biased, 0x64646464u, 0x4140), r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x64806480u));
-    return r;
-}
-DV_DEV unsigned codes_hi(unsigned biased)  // bytes 2, 3
-{
-    unsigned u = __byte_perm(biased, 0x64646464u, 0x4342), r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x64806480u));
-    return r;
-}
-
 DV_DEV float ex2(float x)
 {
     float r;
@@ -143,8 +128,7 @@ DV_DEV int swz(int r, int c)
 
 // One tile of unit x into a stage; WM == 1: the calling warp's positions only.
 template <class C, bool BLOCK>
-DV_DEV void load_tile(const KvAttnArgs &a, const Unit &x, size_t base, long long tile,
-                      unsigned stage)
+DV_DEV void load_tile(const KvAttnArgs &a, const Unit &x, size_t base, int tile, unsigned stage)
 {
     constexpr bool OWN = C::WM == 1;
     constexpr int ROWS = OWN ? C::PW : kKvTile, N = OWN ? 32 : C::THREADS;
@@ -164,8 +148,8 @@ DV_DEV void load_tile(const KvAttnArgs &a, const Unit &x, size_t base, long long
         if (BLOCK) {
             p = block_pos(a, x, tile * kKvTile + r);
         } else {
-            const long long at = tile * kKvTile + r;
-            p = at < end ? (int)at : -1;
+            p = tile * kKvTile + r;
+            p = p < end ? p : -1;
         }
         const bool on = p >= 0;
         const size_t row = on ? base + p : base;
@@ -187,10 +171,12 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB) k_kv_mma(const KvAttnArgs
 {
     constexpr int D = C::D, KS = C::KS, NT = C::NT, CH = C::CH, RM = C::RM, WP = C::WP;
     constexpr int NR = C::PACK ? 1 : 2;  // query rows per thread
+    constexpr int PS = C::PW < 32 ? C::PW : 32, NTL = PS / 8, NV = 2 * NTL;  // positions a step
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ SchedSmem sm;
     __shared__ float s_m[WP][RM], s_l[WP][RM], u_m[RM], u_l[RM], s_al[RM], s_inv[RM];
     __shared__ unsigned long long s_bits[RM];
+    __shared__ float wgt[kMergePieces][RM];
     uint4 *qf = reinterpret_cast<uint4 *>(smem + (size_t)C::NST * C::STAGE);
     float *so = reinterpret_cast<float *>(smem + (size_t)C::NST * C::STAGE + C::QF);
     const unsigned ring = (unsigned)__cvta_generic_to_shared(smem);
@@ -208,14 +194,18 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB) k_kv_mma(const KvAttnArgs
         return ((size_t)u.b * a.c.Hkv + (BLOCK ? u.h / G : u.h)) * (size_t)a.c.cap;
     };
     long long wl = run.lo;
+    size_t bl = unit_base(xl);
+    unsigned sl = ring;  // stage of the next load
     auto issue = [&]() {
         if (wl < run.hi) {
-            if (wl >= xl.w1)
+            if (wl >= xl.w1) {
                 xl = sched_unit<BLOCK>(a, RM, sm, run, wl);
+                bl = unit_base(xl);
+            }
             if (xl.h >= 0)
-                load_tile<C, BLOCK>(a, xl, unit_base(xl), wl - xl.w0,
-                                    ring + (unsigned)((wl - run.lo) % C::NST) * C::STAGE);
+                load_tile<C, BLOCK>(a, xl, bl, (int)(wl - xl.w0), sl);
             ++wl;
+            sl = sl + C::STAGE == ring + C::NST * C::STAGE ? ring : sl + C::STAGE;
         }
         cp_commit();
     };
@@ -230,6 +220,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB) k_kv_mma(const KvAttnArgs
         else
             __syncwarp();
     };
+    unsigned st_next = ring;  // stage of the next tile
     const int pc0 = col_pos(2 * t), pc1 = col_pos(2 * t + 1);  // positions of this thread's columns
     const int kr = col_pos(g);                                 // key row of this thread
 
@@ -241,6 +232,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB) k_kv_mma(const KvAttnArgs
                 cp_wait<C::NST - 2>();
                 sync_tile();
                 issue();
+                st_next = st_next + C::STAGE == ring + C::NST * C::STAGE ? ring
+                                                                        : st_next + C::STAGE;
             }
             continue;
         }
@@ -316,75 +309,91 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB) k_kv_mma(const KvAttnArgs
             cp_wait<C::NST - 2>();
             sync_tile();
             issue();  // into the stage of the tile before this one
-            const unsigned st = ring + (unsigned)((w - run.lo) % C::NST) * C::STAGE;
-            const long long p0 = (w - x.w0) * kKvTile;
+            const unsigned st = st_next;
+            st_next = st_next + C::STAGE == ring + C::NST * C::STAGE ? ring : st_next + C::STAGE;
+            const int p0 = (int)(w - x.w0) * kKvTile;
             const bool edge = !BLOCK && p0 + kKvTile > x.len;  // some position may be unseen
-            // ---- 16 positions at a time
+            // ---- PS positions at a time
 #pragma unroll 1
-            for (int pb = wp * C::PW; pb < (wp + 1) * C::PW; pb += 16) {
-                float s[2][4];
+            for (int pb = wp * C::PW; pb < (wp + 1) * C::PW; pb += PS) {
+                float s[NTL][4], sl2[C::PACK ? 1 : NTL][4];
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int nt = 0; nt < NTL; ++nt) {
                     s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+                    if (!C::PACK)
+                        sl2[nt][0] = sl2[nt][1] = sl2[nt][2] = sl2[nt][3] = 0.f;
+                }
                 const uint4 *qw = qf + wm * KS * (C::PACK ? 1 : 2) * 32 + lane;
+                auto step = [&](int ks, const unsigned (&b0)[NTL], const unsigned (&b1)[NTL]) {
+                    const uint4 q = qw[ks * (C::PACK ? 1 : 2) * 32];
+#pragma unroll
+                    for (int nt = 0; nt < NTL; ++nt)
+                        mma(s[nt], q, b0[nt], b1[nt]);
+                    if (!C::PACK) {
+                        const uint4 ql = qw[(ks * 2 + 1) * 32];
+#pragma unroll
+                        for (int nt = 0; nt < NTL; ++nt)
+                            mma(sl2[nt], ql, b0[nt], b1[nt]);
+                    }
+                };
 #pragma unroll
                 for (int i = 0; i < C::CPR / 4; ++i) {
-                    uint4 kc[2];
+                    unsigned kc[NTL][4];
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
-                        kc[nt] = lds16(st + swz<C>(pb + 8 * nt + kr, t + 4 * i));
+                    for (int nt = 0; nt < NTL; ++nt) {
+                        const uint4 u = lds16(st + swz<C>(pb + 8 * nt + kr, t + 4 * i));
+                        kc[nt][0] = u.x;
+                        kc[nt][1] = u.y;
+                        kc[nt][2] = u.z;
+                        kc[nt][3] = u.w;
+                    }
+                    unsigned b0[NTL], b1[NTL];
                     if (C::I8) {
-                        const unsigned w0[4] = {kc[0].x, kc[0].y, kc[0].z, kc[0].w};
-                        const unsigned w1[4] = {kc[1].x, kc[1].y, kc[1].z, kc[1].w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const int ks = 4 * i + j;
-                            const unsigned u0 = w0[j] ^ 0x80808080u, u1 = w1[j] ^ 0x80808080u;
-                            const unsigned a0 = codes_lo(u0), a1 = codes_hi(u0);
-                            const unsigned b0 = codes_lo(u1), b1 = codes_hi(u1);
 #pragma unroll
-                            for (int part = 0; part < (C::PACK ? 1 : 2); ++part) {
-                                const uint4 q = qw[(ks * (C::PACK ? 1 : 2) + part) * 32];
-                                mma(s[0], q, a0, a1);
-                                mma(s[1], q, b0, b1);
+                            for (int nt = 0; nt < NTL; ++nt) {
+                                const unsigned u = kc[nt][j] ^ 0x80808080u;
+                                b0[nt] = codes_lo(u);
+                                b1[nt] = codes_hi(u);
                             }
+                            step(4 * i + j, b0, b1);
                         }
                     } else {
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            const int ks = 2 * i + j;
 #pragma unroll
-                            for (int part = 0; part < (C::PACK ? 1 : 2); ++part) {
-                                const uint4 q = qw[(ks * (C::PACK ? 1 : 2) + part) * 32];
-                                mma(s[0], q, j ? kc[0].z : kc[0].x, j ? kc[0].w : kc[0].y);
-                                mma(s[1], q, j ? kc[1].z : kc[1].x, j ? kc[1].w : kc[1].y);
+                            for (int nt = 0; nt < NTL; ++nt) {
+                                b0[nt] = kc[nt][2 * j];
+                                b1[nt] = kc[nt][2 * j + 1];
                             }
+                            step(2 * i + j, b0, b1);
                         }
                     }
                 }
-                // ---- scores of row g (and g + 8): columns 2t, 2t + 1 of both tiles
-                float v[NR][4];
+                // ---- scores of row g (and g + 8): columns 2t, 2t + 1 of each tile
+                float v[NR][NV];
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
+                for (int nt = 0; nt < NTL; ++nt) {
                     if (C::PACK) {
                         v[0][2 * nt] = s[nt][0] + s[nt][2];
                         v[0][2 * nt + 1] = s[nt][1] + s[nt][3];
                     } else {
-                        v[0][2 * nt] = s[nt][0];
-                        v[0][2 * nt + 1] = s[nt][1];
-                        v[NR - 1][2 * nt] = s[nt][2];
-                        v[NR - 1][2 * nt + 1] = s[nt][3];
+                        v[0][2 * nt] = s[nt][0] + sl2[nt][0];
+                        v[0][2 * nt + 1] = s[nt][1] + sl2[nt][1];
+                        v[NR - 1][2 * nt] = s[nt][2] + sl2[nt][2];
+                        v[NR - 1][2 * nt + 1] = s[nt][3] + sl2[nt][3];
                     }
                 }
-                const int pos[4] = {pb + pc0, pb + pc1, pb + 8 + pc0, pb + 8 + pc1};
                 const float *sc = reinterpret_cast<const float *>(
-                    smem + (st - ring) + 2 * C::TILE);
-                float vs[4];
+                    smem + (st - ring) + 2 * C::TILE) + pb;
+                float vs[NV];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float kscl = C::I8 ? sc[pos[e]] : 1.f;
-                    vs[e] = C::I8 ? sc[kKvTile + pos[e]] : 1.f;
-                    const float add = BLOCK ? sc[2 * kKvTile + pos[e]] : 0.f;
+                for (int e = 0; e < NV; ++e) {
+                    const int ps = 8 * (e >> 1) + ((e & 1) ? pc1 : pc0);
+                    const float kscl = C::I8 ? sc[ps] : 1.f;
+                    vs[e] = C::I8 ? sc[kKvTile + ps] : 1.f;
+                    const float add = BLOCK ? sc[2 * kKvTile + ps] : 0.f;
 #pragma unroll
                     for (int r = 0; r < NR; ++r) {
                         const float f = C::I8 ? inv[r] * kscl : inv[r];
@@ -394,14 +403,14 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB) k_kv_mma(const KvAttnArgs
                 unsigned seen[NR];
 #pragma unroll
                 for (int r = 0; r < NR; ++r)
-                    seen[r] = 15u;
+                    seen[r] = (1u << NV) - 1;
                 if (edge) {
 #pragma unroll
                     for (int r = 0; r < NR; ++r) {
                         const unsigned long long bits = s_bits[wm * C::RW + g + 8 * r];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const long long j = p0 + pos[e] - x.len;
+                        for (int e = 0; e < NV; ++e) {
+                            const int j = p0 + pb + 8 * (e >> 1) + ((e & 1) ? pc1 : pc0) - x.len;
                             const bool on = j < 0 || (j < 64 && ((bits >> j) & 1));
                             if (!on) {
                                 v[r][e] = -INFINITY;
@@ -412,31 +421,36 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB) k_kv_mma(const KvAttnArgs
                 }
                 // ---- running max, weights, their power of two
                 float f[NR];
-                uint4 ph, pl;  // weights, high and low parts, as A fragments
-                unsigned hh[2][2], ll[2][2];
+                unsigned hh[NR][NTL], ll[NR][NTL];  // weights, high and low parts
                 bool moved = false;
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
-                    const float mx =
-                        quad_max(fmaxf(fmaxf(v[r][0], v[r][1]), fmaxf(v[r][2], v[r][3])));
+                    float mx = v[r][0];
+#pragma unroll
+                    for (int e = 1; e < NV; ++e)
+                        mx = fmaxf(mx, v[r][e]);
+                    mx = quad_max(mx);
                     const float mn = fmaxf(m[r], mx), ms = mn == -INFINITY ? 0.f : mn;
                     f[r] = ex2(m[r] - ms);
                     m[r] = mn;
-                    float p[4];
+                    float p[NV], sum = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < NV; ++e) {
                         p[e] = ex2(v[r][e] - ms);
-                    l[r] = fmaf(l[r], f[r], (p[0] + p[1]) + (p[2] + p[3]));
+                        sum += p[e];
+                    }
+                    l[r] = fmaf(l[r], f[r], sum);
                     float up = 16384.f;
                     if (C::I8) {
+                        float big = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                        for (int e = 0; e < NV; ++e) {
                             p[e] = (seen[r] >> e) & 1 ? p[e] * vs[e] : 0.f;
+                            big = fmaxf(big, p[e]);
+                        }
                         // weights relative to the largest so far: the low part keeps
                         // its bits whatever the scales are
-                        const float big = fmaxf(
-                            sg[r] * f[r],
-                            quad_max(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]))));
+                        big = fmaxf(sg[r] * f[r], quad_max(big));
                         if (big >= 2.f * sg[r] || (big < sg[r] * 0x1p-10f && big > 0.f)) {
                             const float now = fmaxf(
                                 __uint_as_float(__float_as_uint(big) & 0x7f800000u), 0x1p-100f);
@@ -447,94 +461,105 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB) k_kv_mma(const KvAttnArgs
                     }
                     moved |= f[r] != 1.f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        p[e] *= up;
-                    hh[r][0] = h2(p[0], p[1]);
-                    hh[r][1] = h2(p[2], p[3]);
-                    ll[r][0] = h2_rest(p[0], p[1], hh[r][0]);
-                    ll[r][1] = h2_rest(p[2], p[3], hh[r][1]);
+                    for (int nt = 0; nt < NTL; ++nt) {
+                        const float w0 = p[2 * nt] * up, w1 = p[2 * nt + 1] * up;
+                        hh[r][nt] = h2(w0, w1);
+                        ll[r][nt] = h2_rest(w0, w1, hh[r][nt]);
+                    }
                 }
                 if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
                         o[i][0] *= f[0];
                         o[i][1] *= f[0];
+                        // (PACK: rows 8-15 are the low parts of the same rows)
                         o[i][2] *= f[NR - 1];
                         o[i][3] *= f[NR - 1];
                     }
                 }
-                if (C::PACK) {
-                    ph = make_uint4(hh[0][0], ll[0][0], hh[0][1], ll[0][1]);
-                } else {
-                    ph = make_uint4(hh[0][0], hh[NR - 1][0], hh[0][1], hh[NR - 1][1]);
-                    pl = make_uint4(ll[0][0], ll[NR - 1][0], ll[0][1], ll[NR - 1][1]);
-                }
-                // ---- values: rows at this thread's four positions
-                constexpr int VI = NT / CH;  // 16-byte (or half) chunks per row
-                unsigned bad = 0;            // edge tiles of binary16: positions not finite
+                // ---- values, 16 positions a product
+                unsigned bad = 0;  // edge tiles of binary16: positions not finite
 #pragma unroll
-                for (int i = 0; i < VI; ++i) {
-                    unsigned vw[4][4];
+                for (int kk = 0; kk < NTL / 2; ++kk) {
+                    uint4 ph, pl;
+                    if (C::PACK) {
+                        ph = make_uint4(hh[0][2 * kk], ll[0][2 * kk], hh[0][2 * kk + 1],
+                                        ll[0][2 * kk + 1]);
+                    } else {
+                        ph = make_uint4(hh[0][2 * kk], hh[NR - 1][2 * kk], hh[0][2 * kk + 1],
+                                        hh[NR - 1][2 * kk + 1]);
+                        pl = make_uint4(ll[0][2 * kk], ll[NR - 1][2 * kk], ll[0][2 * kk + 1],
+                                        ll[NR - 1][2 * kk + 1]);
+                    }
+                    const int pos[4] = {pb + 16 * kk + pc0, pb + 16 * kk + pc1,
+                                        pb + 16 * kk + 8 + pc0, pb + 16 * kk + 8 + pc1};
+                    constexpr int VI = NT / CH;  // 16-byte (or half) chunks per row
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (C::I8 && D == 64) {
-                            const uint2 u = lds8(st + C::TILE + swz<C>(pos[e], g >> 1) +
-                                                 8 * (g & 1));
-                            vw[e][0] = u.x;
-                            vw[e][1] = u.y;
-                            vw[e][2] = vw[e][3] = 0u;
-                        } else {
-                            const uint4 u = lds16(st + C::TILE + swz<C>(pos[e], g + 8 * i));
-                            vw[e][0] = u.x;
-                            vw[e][1] = u.y;
-                            vw[e][2] = u.z;
-                            vw[e][3] = u.w;
+                    for (int i = 0; i < VI; ++i) {
+                        unsigned vw[4][4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (C::I8 && D == 64) {
+                                const uint2 u = lds8(st + C::TILE + swz<C>(pos[e], g >> 1) +
+                                                     8 * (g & 1));
+                                vw[e][0] = u.x;
+                                vw[e][1] = u.y;
+                                vw[e][2] = vw[e][3] = 0u;
+                            } else {
+                                const uint4 u = lds16(st + C::TILE + swz<C>(pos[e], g + 8 * i));
+                                vw[e][0] = u.x;
+                                vw[e][1] = u.y;
+                                vw[e][2] = u.z;
+                                vw[e][3] = u.w;
+                            }
                         }
-                    }
-                    if (!C::I8 && !BLOCK && edge) {
-                        // a NaN or an infinity must not reach rows that do not see it:
-                        // taken out of the product here, given back below
+                        if (!C::I8 && !BLOCK && edge) {
+                            // a NaN or an infinity must not reach rows that do not see it:
+                            // taken out of the product here, given back below
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                            for (int e = 0; e < 4; ++e)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const unsigned u = vw[e][j] & 0x7c007c00u;
-                                if ((u & 0xffffu) == 0x7c00u || (u >> 16) == 0x7c00u) {
-                                    vw[e][j] = 0u;
-                                    bad |= 1u << e;
+                                for (int j = 0; j < 4; ++j) {
+                                    const unsigned u = vw[e][j] & 0x7c007c00u;
+                                    if ((u & 0xffffu) == 0x7c00u || (u >> 16) == 0x7c00u) {
+                                        vw[e][j] = 0u;
+                                        bad |= 1u << (4 * kk + e);
+                                    }
                                 }
-                            }
-                    }
-                    constexpr int WV = C::I8 ? CH / 4 : 4;  // words per chunk
+                        }
+                        constexpr int WV = C::I8 ? CH / 4 : 4;  // words per chunk
 #pragma unroll
-                    for (int j = 0; j < WV; ++j) {
-                        if (C::I8) {
-                            const unsigned x0 = vw[0][j] ^ 0x80808080u, x1 = vw[1][j] ^ 0x80808080u;
-                            const unsigned x2 = vw[2][j] ^ 0x80808080u, x3 = vw[3][j] ^ 0x80808080u;
-                            const unsigned a01 = __byte_perm(x0, x1, 0x5140);
-                            const unsigned a23 = __byte_perm(x0, x1, 0x7362);
-                            const unsigned b01 = __byte_perm(x2, x3, 0x5140);
-                            const unsigned b23 = __byte_perm(x2, x3, 0x7362);
-                            const unsigned b0[4] = {codes_lo(a01), codes_hi(a01), codes_lo(a23),
-                                                    codes_hi(a23)};
-                            const unsigned b1[4] = {codes_lo(b01), codes_hi(b01), codes_lo(b23),
-                                                    codes_hi(b23)};
+                        for (int j = 0; j < WV; ++j) {
+                            if (C::I8) {
+                                const unsigned x0 = vw[0][j] ^ 0x80808080u,
+                                               x1 = vw[1][j] ^ 0x80808080u,
+                                               x2 = vw[2][j] ^ 0x80808080u,
+                                               x3 = vw[3][j] ^ 0x80808080u;
+                                const unsigned a01 = __byte_perm(x0, x1, 0x5140);
+                                const unsigned a23 = __byte_perm(x0, x1, 0x7362);
+                                const unsigned b01 = __byte_perm(x2, x3, 0x5140);
+                                const unsigned b23 = __byte_perm(x2, x3, 0x7362);
+                                const unsigned b0[4] = {codes_lo(a01), codes_hi(a01),
+                                                        codes_lo(a23), codes_hi(a23)};
+                                const unsigned b1[4] = {codes_lo(b01), codes_hi(b01),
+                                                        codes_lo(b23), codes_hi(b23)};
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                mma(o[i * CH + 4 * j + k], ph, b0[k], b1[k]);
-                                if (!C::PACK)
-                                    mma(o[i * CH + 4 * j + k], pl, b0[k], b1[k]);
-                            }
-                        } else {
+                                for (int k = 0; k < 4; ++k) {
+                                    mma(o[i * CH + 4 * j + k], ph, b0[k], b1[k]);
+                                    if (!C::PACK)
+                                        mma(o[i * CH + 4 * j + k], pl, b0[k], b1[k]);
+                                }
+                            } else {
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const unsigned b0 =
-                                    __byte_perm(vw[0][j], vw[1][j], k ? 0x7632 : 0x5410);
-                                const unsigned b1 =
-                                    __byte_perm(vw[2][j], vw[3][j], k ? 0x7632 : 0x5410);
-                                mma(o[i * CH + 2 * j + k], ph, b0, b1);
-                                if (!C::PACK)
-                                    mma(o[i * CH + 2 * j + k], pl, b0, b1);
+                                for (int k = 0; k < 2; ++k) {
+                                    const unsigned b0 =
+                                        __byte_perm(vw[0][j], vw[1][j], k ? 0x7632 : 0x5410);
+                                    const unsigned b1 =
+                                        __byte_perm(vw[2][j], vw[3][j], k ? 0x7632 : 0x5410);
+                                    mma(o[i * CH + 2 * j + k], ph, b0, b1);
+                                    if (!C::PACK)
+                                        mma(o[i * CH + 2 * j + k], pl, b0, b1);
+                                }
                             }
                         }
                     }
@@ -599,11 +624,14 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB) k_kv_mma(const KvAttnArgs
             }
             __syncthreads();
         }
-        finish_unit<BLOCK>(a, RM, run, x, sm, [&](int row, int d) {
-            const int n = d / CH % 8, nt = d / (8 * CH) * CH + d % CH;
-            const int gr = row % 8, r = row / 8 % NR, wr = row / C::RW;
-            return so[(((wr * NT + nt) * NR + r) * 2 + (n & 1)) * 32 + gr * 4 + n / 2];
-        }, u_m, u_l);
+        finish_unit<BLOCK, RM, C::THREADS>(
+            a, run, x, sm, so, u_m, u_l, wgt,
+            [](int row, int d) {
+                const int n = d / CH % 8, nt = d / (8 * CH) * CH + d % CH;
+                const int gr = row % 8, r = row / 8 % NR, wr = row / C::RW;
+                return (((wr * NT + nt) * NR + r) * 2 + (n & 1)) * 32 + gr * 4 + n / 2;
+            },
+            [](int i) { return i / (NT * NR * 64) * C::RW + i / 64 % NR * 8 + i % 32 / 4; });
     }
     cp_wait<0>();
 }
@@ -642,16 +670,16 @@ cudaError_t launch_cfg(const KvAttnArgs &a, int nsm, cudaStream_t st)
 template <bool I8, int D>
 cudaError_t launch_d(const KvAttnArgs &a, int rows, int nsm, cudaStream_t st)
 {
-    // ring depth: about 64 KB of tiles per CTA
-    constexpr int NST = (I8 ? 4 : 2) * (128 / D);
-    constexpr int N2 = NST < 3 ? 3 : NST;
+    constexpr int NST = (I8 ? 3 : 2) * (128 / D) + (I8 ? 0 : 1);
+    constexpr int N2 = !I8 && D == 128 ? 2 : NST;  // two CTAs per SM
+    constexpr int MB = I8 || D == 64 ? 3 : 2;
     if (a.idx)
-        return launch_cfg<Cfg<I8, D, 1, 4, true, N2, 2>, true>(a, nsm, st);
+        return launch_cfg<Cfg<I8, D, 1, 4, true, NST, MB>, true>(a, nsm, st);
     switch (rows) {
-    case 8: return launch_cfg<Cfg<I8, D, 1, 4, true, N2, 2>, false>(a, nsm, st);
+    case 8: return launch_cfg<Cfg<I8, D, 1, 4, true, NST, MB>, false>(a, nsm, st);
     case 16: return launch_cfg<Cfg<I8, D, 1, 4, false, N2, 2>, false>(a, nsm, st);
-    case 32: return launch_cfg<Cfg<I8, D, 2, 4, false, N2, 1>, false>(a, nsm, st);
-    case 64: return launch_cfg<Cfg<I8, D, 4, 2, false, N2, 1>, false>(a, nsm, st);
+    case 32: return launch_cfg<Cfg<I8, D, 2, 2, false, N2, 2>, false>(a, nsm, st);
+    case 64: return launch_cfg<Cfg<I8, D, 4, 2, false, NST, 1>, false>(a, nsm, st);
     default: return cudaErrorInvalidValue;
     }
 }

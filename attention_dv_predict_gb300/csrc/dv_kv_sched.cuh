@@ -173,77 +173,111 @@ DV_DEV unsigned long long seen_bits(const KvAttnArgs &a, const Unit &x, int t)
 
 // Cached position of place i of a unit's tile sequence in block mode, -1
 // where there is none.
-DV_DEV int block_pos(const KvAttnArgs &a, const Unit &x, long long i)
+DV_DEV int block_pos(const KvAttnArgs &a, const Unit &x, int i)
 {
-    const int n = a.c.block, e = (int)(i / n);
+    const int lg = a.blog, e = i >> lg;
     if (e >= x.ent)
         return -1;
     const int j = __ldg(a.idx + ((size_t)x.b * a.H + x.h) * a.k + e);
-    if (j < 0 || j > (x.len - 1) / n) {
+    if (j < 0 || j > (x.len - 1) >> lg) {
         if (j != -1)
             set_status(a.status, DV_ERR_DEVICE_INDEX);
         return -1;
     }
-    const int p = j * n + (int)(i % n);
+    const int p = (j << lg) + (i & (a.c.block - 1));
     return p < x.len ? p : -1;
 }
 
 DV_DEV float row_result(float o, float l) { return l == 0.f ? 0.f : o / l; }
 
-// A run's part of a unit is done: so(row, d), sm_m, sm_l [rows] give it
-// merged over the CTA (visible to every thread; m in units of log2).
-// Writes the result, or a piece, and merges the pieces if it is the last.
-// Barriers inside; the buffers may be reused after it returns.
-template <bool BLOCK, class F>
-DV_DEV void finish_unit(const KvAttnArgs &a, int rows, const Run &r, const Unit &x,
-                        SchedSmem &sm, F so, const float *sm_m, const float *sm_l)
+constexpr int kMergePieces = 16;  // pieces whose weights are in shared memory at a time
+
+// A run's part of a unit is done: so[RM * D] (in the kernel's own order: at(row,
+// d) is the place of a value), u_m, u_l [RM] hold it merged over the CTA,
+// visible to every thread (m in units of log2).  Writes the result, or a
+// piece, and merges the pieces if it is the last.  Every thread of the CTA
+// (NTHR of them) calls it; the buffers may be reused after it returns.
+template <bool BLOCK, int RM, int NTHR, class F, class R>
+DV_DEV void finish_unit(const KvAttnArgs &a, const Run &r, const Unit &x, SchedSmem &sm,
+                        float *so, float *u_m, float *u_l, float (*wgt)[RM], F at, R rowof)
 {
-    const int D = a.c.D, n = x.nrows * D;
-    if (r.lo <= x.w0 && x.w1 <= r.hi) {
-        for (int i = threadIdx.x; i < n; i += blockDim.x) {
-            const int row = i / D, d = i - row * D;
-            a.out[out_at<BLOCK>(a, x, row) + d] = row_result(so(row, d), sm_l[row]);
+    const int D = a.c.D, n4 = RM * D / 4;
+    if (!(r.lo <= x.w0 && x.w1 <= r.hi)) {
+        const size_t rsz = (size_t)RM * (D + 2);
+        float *rec = a.rec + (2 * (size_t)r.c + (x.w0 > r.lo)) * rsz;
+        for (int i = threadIdx.x; i < n4; i += NTHR)
+            __stcg(reinterpret_cast<float4 *>(rec) + i, reinterpret_cast<const float4 *>(so)[i]);
+        for (int i = threadIdx.x; i < RM; i += NTHR) {
+            __stcg(rec + RM * D + i, u_m[i]);
+            __stcg(rec + RM * D + RM + i, u_l[i]);
+        }
+        __threadfence();
+        __syncthreads();
+        const int c0 = (int)(((x.w0 + 1) * r.C - 1) / r.W), c1 = (int)((x.w1 * r.C - 1) / r.W);
+        if (threadIdx.x == 0)
+            sm.last = atomicAdd(a.cnt + c0, 1) == c1 - c0;
+        __syncthreads();
+        if (!sm.last)
+            return;
+        __threadfence();
+        // record of piece c (the unit's first CTA has it after its run's start, or at it)
+        auto piece = [&](int c) {
+            const bool late = c == c0 && x.w0 > r.W * c / r.C;
+            return a.rec + (2 * (size_t)c + late) * rsz;
+        };
+        const int lane = threadIdx.x & 31;
+        for (int row = threadIdx.x >> 5; row < RM; row += NTHR / 32) {
+            float M = -INFINITY, L = 0.f;
+            for (int c = c0 + lane; c <= c1; c += 32)
+                M = fmaxf(M, __ldcg(piece(c) + RM * D + row));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            const float ms = M == -INFINITY ? 0.f : M;
+            for (int c = c0 + lane; c <= c1; c += 32) {
+                const float *p = piece(c) + RM * D;
+                L = fmaf(__ldcg(p + RM + row), exp2f(__ldcg(p + row) - ms), L);
+            }
+            L = warp_sum(L);
+            if (lane == 0) {
+                u_m[row] = ms;
+                u_l[row] = L;
+            }
         }
         __syncthreads();
-        return;
-    }
-    const size_t rsz = (size_t)rows * (D + 2);
-    float *rec = a.rec + (2 * (size_t)r.c + (x.w0 > r.lo)) * rsz;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int row = i / D, d = i - row * D;
-        __stcg(rec + i, so(row, d));
-    }
-    for (int i = threadIdx.x; i < x.nrows; i += blockDim.x) {
-        __stcg(rec + rows * D + i, sm_m[i]);
-        __stcg(rec + rows * D + rows + i, sm_l[i]);
-    }
-    __threadfence();
-    __syncthreads();
-    const int c0 = (int)(((x.w0 + 1) * r.C - 1) / r.W), c1 = (int)((x.w1 * r.C - 1) / r.W);
-    if (threadIdx.x == 0)
-        sm.last = atomicAdd(a.cnt + c0, 1) == c1 - c0;
-    __syncthreads();
-    if (sm.last) {
-        __threadfence();
-        for (int i = threadIdx.x; i < n; i += blockDim.x) {
-            const int row = i / D, d = i - row * D;
-            float M = -INFINITY, L = 0.f, O = 0.f;
-            for (int c = c0; c <= c1; ++c) {
-                // the unit's first CTA has it after its run's start, or at it
-                const bool late = c == c0 && x.w0 > r.W * c / r.C;
-                const float *p = a.rec + (2 * (size_t)c + late) * rsz;
-                const float m = __ldcg(p + rows * D + row), l = __ldcg(p + rows * D + rows + row);
-                const float o = __ldcg(p + i);
-                const float mn = fmaxf(M, m), ms = mn == -INFINITY ? 0.f : mn;
-                const float s0 = exp2f(M - ms), s1 = exp2f(m - ms);
-                L = L * s0 + l * s1;
-                O = O * s0 + o * s1;
-                M = mn;
+        for (int i = threadIdx.x; i < n4; i += NTHR)
+            reinterpret_cast<float4 *>(so)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int cb = c0; cb <= c1; cb += kMergePieces) {
+            const int nc = min(kMergePieces, c1 - cb + 1);
+            for (int i = threadIdx.x; i < nc * RM; i += NTHR) {
+                const int k = i / RM, row = i - k * RM;
+                wgt[k][row] = exp2f(__ldcg(piece(cb + k) + RM * D + row) - u_m[row]);
             }
-            a.out[out_at<BLOCK>(a, x, row) + d] = row_result(O, L);
+            __syncthreads();
+            for (int i = threadIdx.x; i < n4; i += NTHR) {
+                float4 acc = reinterpret_cast<float4 *>(so)[i];
+                const int row = rowof(4 * i);
+#pragma unroll 8
+                for (int k = 0; k < nc; ++k) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(piece(cb + k)) + i);
+                    const float wt = wgt[k][row];
+                    // (a piece without a seen position has zeros, whatever else is NaN)
+                    acc.x = fmaf(v.x, wt, acc.x);
+                    acc.y = fmaf(v.y, wt, acc.y);
+                    acc.z = fmaf(v.z, wt, acc.z);
+                    acc.w = fmaf(v.w, wt, acc.w);
+                }
+                reinterpret_cast<float4 *>(so)[i] = acc;
+            }
+            __syncthreads();
         }
         if (threadIdx.x == 0)
             a.cnt[c0] = 0;  // ready for the next call
+    }
+    const int lg = __ffs(D) - 1;
+    for (int i = threadIdx.x; i < x.nrows * D; i += NTHR) {
+        const int row = i >> lg, d = i & (D - 1);
+        a.out[out_at<BLOCK>(a, x, row) + d] = row_result(so[at(row, d)], u_l[row]);
     }
     __syncthreads();
 }

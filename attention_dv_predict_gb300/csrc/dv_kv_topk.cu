@@ -48,8 +48,10 @@ __global__ void __launch_bounds__(kTopkThreads) k_kv_topk(const KvTopkArgs a)
     // the query's codes
     const float x = tid < D ? ld_row(a.q, b * a.q.sb + h * a.q.sh + tid) : 0.f;
     const float s = quant_scale(block_amax(fabsf(x), red));
-    if (tid < D)
-        qc[tid] = s == s ? (int8_t)quant_code(x, s) : (int8_t)0;
+    if (tid < D) {
+        float v[4] = {x, 0.f, 0.f, 0.f};
+        qc[tid] = s == s ? (int8_t)quant4<false>(v, s, quant_inv(s)) : (int8_t)0;
+    }
     __syncthreads();
     // scores of the blocks that are not taken anyway (complete ones: the
     // last block, the only one that may not be, is among the n_last)
@@ -58,18 +60,26 @@ __global__ void __launch_bounds__(kTopkThreads) k_kv_topk(const KvTopkArgs a)
     const size_t row0 = ((size_t)b * c.Hkv + h / (a.H / c.Hkv)) * (size_t)(c.cap / n) + a.n_first;
     const int part = tid % cpr;
     const int4 q4 = reinterpret_cast<const int4 *>(qc)[part];
-    for (int j0 = 0; j0 < m; j0 += per) {
-        const int j = j0 + tid / cpr;
-        int dot = 0;
-        if (j < m) {
-            const int4 v = __ldg(reinterpret_cast<const int4 *>(c.mean + (row0 + j) * D) + part);
-            dot = __dp4a(v.x, q4.x, __dp4a(v.y, q4.y, __dp4a(v.z, q4.z, __dp4a(v.w, q4.w, 0))));
+    constexpr int UN = 8;  // rows in flight per lane group
+    for (int j0 = tid / cpr; j0 < m + tid / cpr; j0 += UN * per) {
+        int4 v[UN];
+        float ms[UN];
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int j = j0 + i * per;
+            v[i] = j < m ? __ldg(reinterpret_cast<const int4 *>(c.mean + (row0 + j) * D) + part)
+                         : make_int4(0, 0, 0, 0);
+            ms[i] = j < m ? __ldg(c.mean_scale + row0 + j) : 0.f;
         }
-        for (int o = cpr / 2; o > 0; o >>= 1)
-            dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (j < m && part == 0) {
-            const float ms = __ldg(c.mean_scale + row0 + j);
-            keys[j] = score_key(ms == INFINITY ? INFINITY : (float)dot * ms);
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int j = j0 + i * per;
+            int dot = __dp4a(v[i].x, q4.x,
+                             __dp4a(v[i].y, q4.y, __dp4a(v[i].z, q4.z, __dp4a(v[i].w, q4.w, 0))));
+            for (int o = cpr / 2; o > 0; o >>= 1)
+                dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            if (j < m && part == 0)
+                keys[j] = score_key(ms[i] == INFINITY ? INFINITY : (float)dot * ms[i]);
         }
     }
     __syncthreads();

@@ -7,6 +7,7 @@ namespace dv {
 namespace {
 
 constexpr int kWriteThreads = 256;
+constexpr int kReadRows = 2;  // rows a thread of dv_kv_read has in flight
 
 // Count of new tokens of row b, 0 and a recorded fault where its position or
 // count is out of range.
@@ -23,49 +24,127 @@ DV_DEV int row_tokens(const int32_t *lens, const int32_t *n_tok, int b, int T, i
     return n;
 }
 
-// One warp writes one cached row from one given row.
-DV_DEV void write_row(const KvCacheArgs &c, const KvRowsArgs &src, long long at, void *dst,
-                      float *scale, size_t row, int lane)
+// VEC values of a given row (F16: binary16 ones), as binary32.
+template <int VEC, bool F16>
+DV_DEV void ld_rows(const void *p, float (&x)[VEC])
 {
-    float4 x[2];
-    float mx = 0.f;
-    const int D = c.D;
+    if (F16 && VEC >= 8) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int d = (lane + 32 * i) * 4;
-        x[i] = d < D ? ld_row4(src, at + d) : make_float4(0.f, 0.f, 0.f, 0.f);
-        mx = amax2(mx, amax2(amax2(x[i].x, x[i].y), amax2(x[i].z, x[i].w)));
-    }
-    if (c.dtype == DV_I8) {
+        for (int i = 0; i < VEC; i += 8) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __half *>(p) + i));
+            const unsigned w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            mx = amax2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float s = quant_scale(mx);
-        const bool fine = s == s;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int d = (lane + 32 * i) * 4;
-            if (d < D)
-                *reinterpret_cast<unsigned *>(static_cast<int8_t *>(dst) + row * D + d) =
-                    fine ? pack_codes(quant_code(x[i].x, s), quant_code(x[i].y, s),
-                                      quant_code(x[i].z, s), quant_code(x[i].w, s))
-                         : 0u;
+            for (int k = 0; k < 4; ++k) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+                x[i + 2 * k] = f.x;
+                x[i + 2 * k + 1] = f.y;
+            }
         }
-        if (lane == 0)
-            scale[row] = s;
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int d = (lane + 32 * i) * 4;
-        if (d >= D)
-            continue;
-        if (c.dtype == DV_F32) {
-            *reinterpret_cast<float4 *>(static_cast<float *>(dst) + row * D + d) = x[i];
+    for (int i = 0; i < VEC; i += 4) {
+        float4 v;
+        if (F16) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __half *>(p) + i));
+            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
+            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
+            v = make_float4(a.x, a.y, b.x, b.y);
         } else {
-            __half2 h[2] = {__floats2half2_rn(x[i].x, x[i].y), __floats2half2_rn(x[i].z, x[i].w)};
-            *reinterpret_cast<uint2 *>(static_cast<__half *>(dst) + row * D + d) =
-                *reinterpret_cast<uint2 *>(h);
+            v = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i));
+        }
+        x[i] = v.x;
+        x[i + 1] = v.y;
+        x[i + 2] = v.z;
+        x[i + 3] = v.w;
+    }
+}
+
+// VEC values of a row into the cache at p; a row is spread over lpr lanes
+// (all of them call it, `on` or not).  Returns the row's scale (DV_I8).
+// HELD: x becomes the values as stored.
+template <int VEC, int DT, bool HELD>
+DV_DEV float write_row(float (&x)[VEC], typename Store<DT>::T *p, int lpr, bool on)
+{
+    if constexpr (DT == DV_I8) {
+        float mx = amax_of(x);
+        for (int k = lpr / 2; k > 0; k >>= 1)
+            mx = amax2(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+        const float s = quant_scale(mx);
+        const float inv = quant_inv(s);
+        unsigned w[VEC / 4];
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+            w[i] = quant4<HELD>(x + 4 * i, s, inv);  // (NaN where the row is not finite)
+            w[i] = s == s ? w[i] : 0u;
+        }
+        if (on) {
+            if constexpr (VEC == 16)
+                *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+            else
+                *reinterpret_cast<unsigned *>(p) = w[0];
+        }
+        return s;
+    } else if constexpr (DT == DV_F16) {
+        unsigned w[VEC / 2];
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+            const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const unsigned *>(&h);
+            if (HELD) {
+                const float2 f = __half22float2(h);
+                x[2 * i] = f.x;
+                x[2 * i + 1] = f.y;
+            }
+        }
+        if (on) {
+            if constexpr (VEC == 16) {
+                reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            } else {
+                *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+            }
+        }
+    } else if (on) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4)
+            *reinterpret_cast<float4 *>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+    }
+    return 0.f;
+}
+
+// One side (0 keys, 1 values) of the `rows` new rows of a tile: the given rows
+// from token t0 of (b, h) on go to the cache rows from row0 on, by the threads
+// from `first` on.  A row is spread over D / VEC lanes, and a lane group has
+// UR rows in flight.  HELD: x holds the last pass's values as stored.
+template <int VEC, int DT, bool F16, bool HELD, int UR>
+DV_DEV void write_side(const KvAppendArgs &a, int side, int first, int b, int h, int t0, int rows,
+                       size_t row0, float (&x)[UR][VEC])
+{
+    using T = typename Store<DT>::T;
+    const KvCacheArgs &c = a.c;
+    const int lpr = c.D / VEC, part = threadIdx.x % lpr;
+    const int groups = (kWriteThreads - first) / lpr, group = (threadIdx.x - first) / lpr;
+    const KvRowsArgs &src = side ? a.v : a.k;
+    const size_t es = F16 ? 2 : 4;
+    const char *from = static_cast<const char *>(src.p) +
+                       es * (b * src.sb + t0 * src.st + h * src.sh + part * VEC);
+    const long long step = es * src.st;
+    T *to = static_cast<T *>(side ? c.v : c.k) + row0 * c.D + part * VEC;
+    float *scale = (side ? c.vs : c.ks) + row0;
+    for (int u0 = group; u0 < rows + group; u0 += UR * groups) {
+#pragma unroll
+        for (int i = 0; i < UR; ++i) {
+            const int u = u0 + i * groups;
+            // (past the last row: that row once more, not written)
+            ld_rows<VEC, F16>(from + min(u, rows - 1) * step, x[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < UR; ++i) {
+            const int u = u0 + i * groups;
+            const float s = write_row<VEC, DT, HELD>(x[i], to + (size_t)u * c.D, lpr, u < rows);
+            if (DT == DV_I8 && u < rows && part == 0)
+                scale[u] = s;
         }
     }
 }
@@ -73,9 +152,10 @@ DV_DEV void write_row(const KvCacheArgs &c, const KvRowsArgs &src, long long at,
 // One CTA owns the positions of one aligned tile (a block, where means are
 // kept) of one (row, KV head): it writes the new tokens that fall into it
 // and, when the tile's last position is among them, the block's mean.
-__global__ void __launch_bounds__(kWriteThreads) k_kv_append(const KvAppendArgs a)
+template <int VEC, int DT, bool F16>
+__global__ void __launch_bounds__(kWriteThreads, 4) k_kv_append(const KvAppendArgs a)
 {
-    __shared__ MeanSmem sm;
+    constexpr int UR = VEC == 16 ? 2 : 4;
     const KvCacheArgs &c = a.c;
     const int BH = a.B * c.Hkv, bhi = blockIdx.x % BH;  // neighbouring heads together:
     const int b = bhi / c.Hkv, h = bhi % c.Hkv;         // their given rows lie side by side
@@ -87,26 +167,100 @@ __global__ void __launch_bounds__(kWriteThreads) k_kv_append(const KvAppendArgs 
     const int lo = max(len, tile * a.tile), hi = min(len + n, (tile + 1) * a.tile);
     if (lo >= hi)
         return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const size_t bh = (size_t)b * c.Hkv + h;
-    for (int u = warp; u < 2 * (hi - lo); u += kWriteThreads / 32) {
-        const int p = lo + (u >> 1);
-        const KvRowsArgs &src = (u & 1) ? a.v : a.k;
-        const long long at = b * src.sb + (long long)(p - len) * src.st + h * src.sh;
-        write_row(c, src, at, (u & 1) ? c.v : c.k, (u & 1) ? c.vs : c.ks,
-                  bh * (size_t)c.cap + p, lane);
-    }
-    if (c.block && hi == (tile + 1) * a.tile) {
+    const int lpr = c.D / VEC, part = threadIdx.x % lpr, rows = hi - lo;
+    const size_t bh = (size_t)b * c.Hkv + h, row0 = bh * (size_t)c.cap + lo;
+    const bool mean = c.block && hi == (tile + 1) * a.tile;
+    float x[UR][VEC];
+    if (VEC == 16 && mean && rows == c.block && rows <= UR * (kWriteThreads / lpr)) {
+        // a whole new block, one pass of the CTA: its mean from the registers
+        __shared__ int s_max, s_sum[256];
+        for (int d = threadIdx.x; d < c.D; d += kWriteThreads)
+            s_sum[d] = 0;
+        if (threadIdx.x == 0)
+            s_max = 0;
         __syncthreads();
-        block_mean(c, bh, tile, sm);
+        write_side<VEC, DT, F16, true>(a, 0, 0, b, h, lo - len, rows, row0, x);
+        float mx = 0.f;
+#pragma unroll
+        for (int i = 0; i < UR; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if ((int)(threadIdx.x / lpr) + i * (kWriteThreads / lpr) >= rows)
+                    x[i][e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < UR; ++i)
+            mx = amax_of(x[i], mx);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            mx = amax2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        if ((threadIdx.x & 31) == 0)  // (non-negative numbers, infinity and NaN in this order)
+            atomicMax(&s_max, __float_as_int(mx));
+        __syncthreads();
+        const float top = __int_as_float(s_max);
+        const bool fine = top <= 3.402823466e38f;
+        const int e2 = mean_exponent(fine ? top : 0.f);
+        const float inv = ldexpf(1.f / c.block, 24 - e2);
+        if (fine) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                int acc = 0;
+#pragma unroll
+                for (int i = 0; i < UR; ++i)
+                    acc += mean_units(x[i][e], inv);
+                for (int o = lpr; o < 32; o <<= 1)
+                    acc += __shfl_xor_sync(0xffffffffu, acc, o);
+                if ((int)(threadIdx.x & 31) < lpr)
+                    atomicAdd(&s_sum[part * VEC + e], acc);
+            }
+        }
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            int acc[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                acc[e] = s_sum[part * VEC + e];
+            store_mean<VEC>(c, bh * (size_t)(c.cap / c.block) + tile, acc, e2, fine, part, lpr);
+        }
+        write_side<VEC, DT, F16, false>(a, 1, 0, b, h, lo - len, rows, row0, x);
+        return;
+    }
+    write_side<VEC, DT, F16, false>(a, 0, 0, b, h, lo - len, rows, row0, x);
+    if (mean) {  // warp 0 takes the mean from the cache while the others write the values
+        __syncthreads();
+        if (threadIdx.x < 32)
+            warp_mean<DT>(c, bh, tile);
+        else
+            write_side<VEC, DT, F16, false>(a, 1, 32, b, h, lo - len, rows, row0, x);
+    } else {
+        write_side<VEC, DT, F16, false>(a, 1, 0, b, h, lo - len, rows, row0, x);
     }
 }
 
-// Four values per thread.
+// VEC cached values as numbers, without their scale.
+template <int VEC, int DT>
+DV_DEV void ld_values(const typename Store<DT>::T *p, float (&f)[VEC])
+{
+    if constexpr (DT == DV_I8) {
+        static_assert(VEC == 8, "half a 16-byte chunk");
+        const uint2 u = __ldcs(reinterpret_cast<const uint2 *>(p));
+        float g[16];
+        Store<DV_I8>::unpack(make_uint4(u.x, u.y, 0x80808080u, 0x80808080u), g);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            f[i] = g[i];
+    } else {
+        ld_rows<VEC, DT == DV_F16>(p, f);
+    }
+}
+
+// VEC values per thread of UR rows, keys and values.
+template <int VEC, int DT, bool F16>
 __global__ void __launch_bounds__(kWriteThreads) k_kv_read(const KvReadArgs a)
 {
+    constexpr int UR = kReadRows;
+    using T = typename Store<DT>::T;
     const KvCacheArgs &c = a.c;
-    const int lpr = c.D / 4, rows = kWriteThreads / lpr;
+    const int lpr = c.D / VEC, rows = kWriteThreads / lpr;
     const int BH = a.B * c.Hkv, bhi = blockIdx.x % BH;
     const int b = bhi / c.Hkv, h = bhi % c.Hkv;
     const int s0 = __ldg(a.start + b);
@@ -116,25 +270,56 @@ __global__ void __launch_bounds__(kWriteThreads) k_kv_read(const KvReadArgs a)
         return;
     }
     const size_t bh = (size_t)b * c.Hkv + h;
-    const int t = blockIdx.x / BH * rows + threadIdx.x / lpr, d = (threadIdx.x % lpr) * 4;
-    if (t >= a.T)
-        return;
-    const size_t row = bh * (size_t)c.cap + s0 + t;
-    const size_t o = (bh * (size_t)a.T + t) * c.D + d;
+    const int t0 = blockIdx.x / BH * (UR * rows) + threadIdx.x / lpr;
+    const int d = (threadIdx.x % lpr) * VEC;
+    float x[UR][2][VEC], s[UR][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float4 x = ld_cached4(i ? c.v : c.k, c.dtype, row * c.D + d);
-        if (c.dtype == DV_I8) {
-            const float s = (i ? c.vs : c.ks)[row];
-            x = make_float4(x.x * s, x.y * s, x.z * s, x.w * s);
+    for (int i = 0; i < UR; ++i) {
+        if (t0 + i * rows >= a.T)
+            break;
+        const size_t row = bh * (size_t)c.cap + s0 + t0 + i * rows;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            ld_values<VEC, DT>(static_cast<const T *>(k ? c.v : c.k) + row * c.D + d, x[i][k]);
+            s[i][k] = DT == DV_I8 ? __ldg((k ? c.vs : c.ks) + row) : 1.f;
         }
-        void *dst = i ? a.v_out : a.k_out;
-        if (a.f16) {
-            __half2 hh[2] = {__floats2half2_rn(x.x, x.y), __floats2half2_rn(x.z, x.w)};
-            *reinterpret_cast<uint2 *>(static_cast<__half *>(dst) + o) =
-                *reinterpret_cast<uint2 *>(hh);
-        } else {
-            *reinterpret_cast<float4 *>(static_cast<float *>(dst) + o) = x;
+    }
+#pragma unroll
+    for (int i = 0; i < UR; ++i) {
+        if (t0 + i * rows >= a.T)
+            break;
+        const size_t o = (bh * (size_t)a.T + t0 + i * rows) * c.D + d;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            void *dst = k ? a.v_out : a.k_out;
+            if (DT == DV_I8) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    x[i][k][e] *= s[i][k];
+            }
+            if (F16) {
+                unsigned u[VEC / 2];
+#pragma unroll
+                for (int e = 0; e < VEC / 2; ++e) {
+                    const __half2 hh = __floats2half2_rn(x[i][k][2 * e], x[i][k][2 * e + 1]);
+                    u[e] = *reinterpret_cast<const unsigned *>(&hh);
+                }
+                __half *q = static_cast<__half *>(dst) + o;
+                if constexpr (VEC >= 8) {
+#pragma unroll
+                    for (int e = 0; e < VEC / 8; ++e)
+                        __stcs(reinterpret_cast<uint4 *>(q) + e,
+                               make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]));
+                } else {
+                    __stcs(reinterpret_cast<uint2 *>(q), make_uint2(u[0], u[1]));
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; e += 4)
+                    __stcs(reinterpret_cast<float4 *>(static_cast<float *>(dst) + o + e),
+                           make_float4(x[i][k][e], x[i][k][e + 1], x[i][k][e + 2],
+                                       x[i][k][e + 3]));
+            }
         }
     }
 }
@@ -145,7 +330,6 @@ __global__ void __launch_bounds__(kWriteThreads) k_kv_read(const KvReadArgs a)
 // reads.
 __global__ void __launch_bounds__(kWriteThreads) k_kv_keep(const KvKeepArgs a)
 {
-    __shared__ MeanSmem sm;
     __shared__ int path[DV_TREE_MAX_TOKENS];
     __shared__ int bad;
     const KvCacheArgs &c = a.c;
@@ -190,11 +374,18 @@ __global__ void __launch_bounds__(kWriteThreads) k_kv_keep(const KvKeepArgs a)
         if (move)
             s[p0 + threadIdx.x] = x;
     }
-    if (c.block && side == 0)
-        for (int j = len / c.block; (j + 1) * c.block <= len + n; ++j) {
-            __syncthreads();
-            block_mean(c, bh, j, sm);
+    if (c.block && side == 0) {  // the blocks that the kept span completes, a warp each
+        __syncthreads();
+        for (int j = len / c.block + (int)(threadIdx.x >> 5); (j + 1) * c.block <= len + n;
+             j += kWriteThreads / 32) {
+            if (c.dtype == DV_I8)
+                warp_mean<DV_I8>(c, bh, j);
+            else if (c.dtype == DV_F16)
+                warp_mean<DV_F16>(c, bh, j);
+            else
+                warp_mean<DV_F32>(c, bh, j);
         }
+    }
 }
 
 template <class K, class A>
@@ -207,19 +398,56 @@ cudaError_t launch(K kern, dim3 grid, const A &a, cudaStream_t st)
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
+template <int VEC, int DT>
+cudaError_t append_src(const KvAppendArgs &a, dim3 grid, cudaStream_t st)
+{
+    return a.k.f16 ? launch(k_kv_append<VEC, DT, true>, grid, a, st)
+                   : launch(k_kv_append<VEC, DT, false>, grid, a, st);
+}
+
+// (rows of fewer than 16 values are binary32 or binary16 ones)
+template <int VEC>
+cudaError_t append_dt(const KvAppendArgs &a, dim3 grid, cudaStream_t st)
+{
+    if (a.c.dtype == DV_F32)
+        return append_src<VEC, DV_F32>(a, grid, st);
+    if (a.c.dtype == DV_F16 || VEC < 16)
+        return append_src<VEC, DV_F16>(a, grid, st);
+    return append_src<VEC, VEC < 16 ? DV_F16 : DV_I8>(a, grid, st);
+}
+
+template <int VEC, int DT>
+cudaError_t read_out(const KvReadArgs &a, dim3 grid, cudaStream_t st)
+{
+    return a.f16 ? launch(k_kv_read<VEC, DT, true>, grid, a, st)
+                 : launch(k_kv_read<VEC, DT, false>, grid, a, st);
+}
+
+template <int VEC>
+cudaError_t read_dt(const KvReadArgs &a, dim3 grid, cudaStream_t st)
+{
+    if (a.c.dtype == DV_F32)
+        return read_out<VEC, DV_F32>(a, grid, st);
+    if (a.c.dtype == DV_F16 || VEC < 8)
+        return read_out<VEC, DV_F16>(a, grid, st);
+    return read_out<VEC, VEC < 8 ? DV_F16 : DV_I8>(a, grid, st);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t st)
 {
     // the aligned tiles that T positions at any offset can touch
     const int tiles = (a.T + a.tile - 2) / a.tile + 1;
-    return launch(k_kv_append, dim3(tiles * a.B * a.c.Hkv), a, st);
+    const dim3 grid(tiles * a.B * a.c.Hkv);
+    return a.c.D >= 16 ? append_dt<16>(a, grid, st) : append_dt<4>(a, grid, st);
 }
 
 cudaError_t launch_kv_read(const KvReadArgs &a, cudaStream_t st)
 {
-    const int rows = kWriteThreads / (a.c.D / 4);
-    return launch(k_kv_read, dim3((a.T + rows - 1) / rows * a.B * a.c.Hkv), a, st);
+    const int vec = a.c.D >= 8 ? 8 : 4, rows = kReadRows * (kWriteThreads / (a.c.D / vec));
+    const dim3 grid((a.T + rows - 1) / rows * a.B * a.c.Hkv);
+    return vec == 8 ? read_dt<8>(a, grid, st) : read_dt<4>(a, grid, st);
 }
 
 cudaError_t launch_kv_keep(const KvKeepArgs &a, cudaStream_t st)

@@ -439,6 +439,14 @@ def _kv_tensors(desc: KvDesc, batch: int):
     return t
 
 
+def _raw_stream(device_index: int) -> int:
+    """The current stream's handle (without a Stream object around it, where torch offers that)."""
+    return torch.cuda.current_stream(device_index).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
 class KvCache:
     """The tensors of one KV cache (attributes ``k``, ``v``, and where the
     descriptor has them ``k_scale``, ``v_scale``, ``k_mean``,
@@ -458,6 +466,7 @@ class KvCache:
         if set(tensors) != set(want):
             raise ValueError(f"this cache has the tensors {sorted(want)}, got {sorted(tensors)}")
         self.device = tensors["k"].device
+        self.device_index = tensors["k"].get_device()
         for n, (shape, dt) in want.items():
             t = tensors[n]
             if (tuple(t.shape) != shape or t.dtype != dt or not t.is_cuda
@@ -480,6 +489,7 @@ class KvWorkspace(Workspace):
             raise DvError("dv_kv_workspace_size", DV_ERR_INVALID_ARG)
         self.buf = torch.empty(n + 256, dtype=torch.uint8, device=device or "cuda")
         self.device = self.buf.device
+        self.device_index = self.buf.get_device()
         off = (-self.buf.data_ptr()) % 256
         self.ptr = self.buf.data_ptr() + off
         self.nbytes = n
@@ -490,35 +500,40 @@ class KvWorkspace(Workspace):
 
 def _kv_dev(cache: KvCache, ws: KvWorkspace, stream):
     """The stream of a call; its device must be the cache's and the current one."""
-    if ws.device != cache.device:
+    dev = cache.device_index
+    if ws.device_index != dev:
         raise ValueError("the workspace is not on the cache's device")
-    if torch.cuda.current_device() != cache.device.index:
+    if torch.cuda.current_device() != dev:
         raise ValueError("the cache is not on the current device (torch.cuda.device)")
-    if stream is not None and stream.device != cache.device:
+    if stream is None:
+        return _raw_stream(dev)
+    if stream.device_index != dev:
         raise ValueError("the stream is not of the cache's device")
-    return _stream(stream)
+    return stream.cuda_stream
 
 
 def _kv_tensor(name: str, t: Optional[torch.Tensor], cache: KvCache, shape, dtype):
     if t is None:
         return None
-    if (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()
-            or t.device != cache.device):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on the "
+    if (t.dtype != dtype or t.shape != shape or not t.is_contiguous()
+            or t.get_device() != cache.device_index):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on the "
                          "cache's device")
     return t.data_ptr()
 
 
 def _kv_rows(name: str, t: torch.Tensor, cache: KvCache, shape) -> KvRows:
-    if (t.dtype not in _ROW_DTYPE or tuple(t.shape) != tuple(shape) or t.device != cache.device
-            or (t.stride(-1) != 1 and t.shape[-1] != 1)):
-        raise ValueError(f"{name} must be a float32 or float16 tensor {tuple(shape)} on the "
+    dt = _ROW_DTYPE.get(t.dtype)
+    s = t.stride()
+    if (dt is None or t.shape != shape or t.get_device() != cache.device_index
+            or (s[-1] != 1 and shape[-1] != 1)):
+        raise ValueError(f"{name} must be a float32 or float16 tensor {shape} on the "
                          "cache's device, contiguous in its last dimension")
     # (a dimension of one row is never stepped over: its stride says nothing)
-    s = [0 if n == 1 else st for n, st in zip(t.shape, t.stride())]
-    if t.dim() == 3:  # (b, h): one query per row
-        s.insert(1, 0)
-    return KvRows(t.data_ptr(), _ROW_DTYPE[t.dtype], s[0], s[1], s[2])
+    if len(shape) == 4:
+        return KvRows(t.data_ptr(), dt, s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0,
+                      s[2] if shape[2] > 1 else 0)
+    return KvRows(t.data_ptr(), dt, s[0] if shape[0] > 1 else 0, 0, s[1] if shape[1] > 1 else 0)
 
 
 def dv_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, lens: torch.Tensor,

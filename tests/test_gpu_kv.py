@@ -163,6 +163,23 @@ def test_append_tiny_and_huge(dv):
     c.same_cache()
 
 
+@pytest.mark.parametrize("exp", [0, -30, -90, -118, 60])
+def test_append_near_halves(dv, exp):
+    """Values within a few last places of half a code: the rounded quotient decides."""
+    B, T, H, D = 1, 400, 2, 128
+    c = Case(dv, B, H, 1, D, T, "i8")
+    s = (c.rng.uniform(1, 2, (B, T, H, 1)) * 2.0 ** exp).astype(np.float32)
+    k = c.rng.integers(-126, 126, (B, T, H, D)) + 0.5
+    x = (k * s).astype(np.float32)
+    x = (x.view(np.int32) + c.rng.integers(-2, 3, x.shape).astype(np.int32)).view(np.float32)
+    x[..., 0] = 127 * s[..., 0]
+    dev = torch.from_numpy(x).cuda()
+    dv.dv_kv_append(c.cache, dev, dev, i32([0]), c.ws)
+    c.ok()
+    c.ref.append(x, x, [0], [T])
+    c.same_cache()
+
+
 @pytest.mark.parametrize("dtype,D", [("f32", 32), ("f16", 128), ("i8", 128), ("i8", 16)])
 def test_keep(dv, dtype, D):
     B, Hkv, T, cap = 6, 2, 37, 150

@@ -201,3 +201,14 @@ def test_all_blocks_is_dense():
     a, _ = kv_ref.block_attend(c, q, [99], idx, 0.25)
     b, _ = kv_ref.tree(c, q[:, None], [99], [1], [[0]], 0.25)
     np.testing.assert_allclose(a, b[:, 0], rtol=1e-12)
+
+
+def test_division_by_127_correction():
+    """q + (a - 127 q) / 127 rounds to a / 127 for every significand (the scale's arithmetic)."""
+    y = np.float32(1) / np.float32(127)
+    m = np.arange(1 << 23, 1 << 24, dtype=np.int64).astype(np.float32)
+    q = m * y
+    r = m.astype(np.float64) - 127.0 * q.astype(np.float64)
+    assert (r == r.astype(np.float32)).all()  # the remainder is exact
+    got = (q.astype(np.float64) + r * np.float64(y)).astype(np.float32)
+    assert (got == m / np.float32(127)).all()
