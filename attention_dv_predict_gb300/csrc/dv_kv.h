@@ -3,6 +3,7 @@
 // block selection), shared by dv_kv_abi.cu and the kernel translation units.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -99,7 +100,14 @@ cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t st);
 cudaError_t launch_kv_read(const KvReadArgs &a, cudaStream_t st);
 cudaError_t launch_kv_keep(const KvKeepArgs &a, cudaStream_t st);
 cudaError_t launch_kv_topk(const KvTopkArgs &a, cudaStream_t st);
-cudaError_t launch_kv_mma(const KvAttnArgs &a, int rows, int nsm, cudaStream_t st);
+// Tensor maps of a cache's keys and values for boxes of `rows` positions of
+// one (row, head), at most 128 bytes of a row wide (dv_kv_abi.cu): the box's
+// rows are swizzled over their own width.
+struct KvMaps {
+    CUtensorMap k, v;
+};
+cudaError_t kv_maps(const KvCacheArgs &c, int B, int rows, KvMaps *m);
+cudaError_t launch_kv_mma(const KvAttnArgs &a, int nsm, cudaStream_t st);
 cudaError_t launch_kv_attn(const KvAttnArgs &a, const KvPlan &p, int nsm, cudaStream_t st);
 
 }  // namespace dv

@@ -3,6 +3,9 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <mutex>
+
+#include <cudaTypedefs.h>
 
 #include "dv_kv.h"
 
@@ -112,6 +115,42 @@ P *at(void *ws, size_t off) { return reinterpret_cast<P *>(static_cast<char *>(w
 bool grid_ok(long long n) { return n > 0 && n <= INT_MAX; }
 
 }  // namespace
+
+namespace dv {
+
+// The driver's encoder is resolved through the runtime, so the library does
+// not link the driver library itself.
+cudaError_t kv_maps(const KvCacheArgs &c, int B, int rows, KvMaps *m)
+{
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    if (!encode)
+        return cudaErrorNotSupported;
+    const cuuint64_t rb = (cuuint64_t)c.D * esize(c.dtype);
+    const cuuint64_t dims[3] = {rb, (cuuint64_t)c.cap, (cuuint64_t)B * c.Hkv};
+    const cuuint64_t strides[2] = {rb, rb * c.cap};
+    const cuuint32_t box[3] = {(cuuint32_t)(rb < 128 ? rb : 128), (cuuint32_t)rows, 1};
+    const cuuint32_t steps[3] = {1, 1, 1};
+    const CUtensorMapSwizzle swz = rb < 128 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                            : CU_TENSOR_MAP_SWIZZLE_128B;
+    for (int i = 0; i < 2; ++i)
+        if (encode(i ? &m->v : &m->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, i ? c.v : c.k, dims,
+                   strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    return cudaSuccess;
+}
+
+}  // namespace dv
 
 extern "C" {
 

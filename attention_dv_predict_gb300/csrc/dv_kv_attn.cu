@@ -59,11 +59,12 @@ __global__ void __launch_bounds__(kGenThreads) k_kv_attn(const KvAttnArgs a)
     const T *V = static_cast<const T *>(a.c.v);
     const int G = a.H / a.c.Hkv;
     const Run run = sched_init<BLOCK>(a, RM, sm);
+    Finish<BLOCK, RM, kGenThreads> fin;
 
     for (long long w = run.lo; w < run.hi;) {
         const Unit x = sched_unit<BLOCK>(a, RM, sm, run, w);
         const long long wend = min(run.hi, x.w1);
-        const int t0 = (int)(w - x.w0), t1 = (int)(wend - x.w0);
+        const int t0 = tile_of(x, tile_place(x, w)), t1 = tile_of(x, wend);
         w = wend;
         if (x.h < 0)
             continue;
@@ -187,10 +188,9 @@ __global__ void __launch_bounds__(kGenThreads) k_kv_attn(const KvAttnArgs a)
             }
         }
         __syncthreads();
-        finish_unit<BLOCK, RM, kGenThreads>(
-            a, run, x, sm, so, um, ul, wgt, [&](int r, int d) { return r * D + d; },
-            [&](int i) { return i / D; });
+        fin.part(a, run, x, [&](int r, int d) { return so[r * D + d]; }, um, ul);
     }
+    fin.end(a, run, sm, um, ul, wgt);
 }
 
 template <typename T>
@@ -212,14 +212,14 @@ KvPlan kv_plan(int dtype, int D, int rows)
 {
     KvPlan p;
     p.mma = dtype != DV_F32 && (D == 64 || D == 128);
-    p.rows = !p.mma ? kKvGenRows : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    p.rows = p.mma ? 8 : kKvGenRows;
     return p;
 }
 
 cudaError_t launch_kv_attn(const KvAttnArgs &a, const KvPlan &p, int nsm, cudaStream_t st)
 {
     if (p.mma)
-        return launch_kv_mma(a, p.rows, nsm, st);
+        return launch_kv_mma(a, nsm, st);
     const int grid = nsm * 4 < kKvMaxCtas ? nsm * 4 : kKvMaxCtas;
     if (a.c.dtype == DV_I8)
         return launch_gen<int8_t>(a, grid, st);

@@ -4,15 +4,19 @@
 // member) of one (batch row, KV head) -- of one (batch row, query head) in
 // block mode -- and its work is the tiles of 64 cached positions it sees.
 // Lengths differ from row to row and are known on the device only, so the
-// tiles of all units are laid end to end and the grid's C CTAs take equal
-// runs of them: CTA c the tiles [W c / C, W (c + 1) / C).  A unit inside one
-// run is finished by its CTA; a unit cut by a run's end leaves a piece (max
-// m, sum l, weighted values o, per row) in a record, and the last of its CTAs
-// to arrive merges the pieces in the order of the positions, so the result
-// does not depend on who was last.  At most one cut unit starts in a CTA's
-// run, so a counter per CTA is enough, and a CTA has at most two pieces: one
-// that began before its run (or at its start), one that goes on after it.
-// No CTA waits for another.
+// tiles of all units are laid end to end, each unit's behind kUnitCost empty
+// places for what a unit costs beside its tiles, and the grid's C CTAs take
+// equal runs: CTA c the places [W c / C, W (c + 1) / C), an end among a
+// unit's empty places counting as the unit's start.  (Without them a ragged
+// batch's short rows all fell to a few CTAs: 32 rows of 1 to 8000 positions,
+// 48 blocks of 32 for each of 64 heads, 420 us against 230.)  A unit inside
+// one run is finished by its CTA; a unit cut by a run's end leaves a piece
+// (max m, sum l, weighted values o, per row) in a record, and the last of its
+// CTAs to arrive merges the pieces in the order of the positions, so the
+// result does not depend on who was last.  At most one cut unit starts in a
+// CTA's run, so a counter per CTA is enough, and a CTA has at most two
+// pieces: one that began before its run (or at its start), one that goes on
+// after it.  No CTA waits for another.
 #pragma once
 
 #include "dv_kv.cuh"
@@ -20,8 +24,10 @@
 namespace dv {
 namespace {
 
+constexpr int kUnitCost = 4;  // tiles that a unit's start and end take the time of
+
 struct SchedSmem {
-    long long pref[DV_KV_MAX_BATCH + 1];  // tiles before batch row b
+    long long pref[DV_KV_MAX_BATCH + 1];  // places before batch row b
     int tiles[DV_KV_MAX_BATCH];           // tiles of one unit of the row
     int mb[DV_KV_MAX_BATCH];              // units per head
     int last;
@@ -33,13 +39,41 @@ struct Unit {
     int row0, nrows;  // first query row and count
     int len, ntok;    // cached prefix, drafted tokens (block mode: 0)
     int ent;          // block mode: entries of the index list
-    long long w0, w1; // its tiles
+    long long w0, w1; // its places, its tiles from w0 + kUnitCost on
 };
 
 struct Run {
     long long W, lo, hi;
     int C, c, nsel;
 };
+
+// a / b for 0 <= a, 0 < b: in 32 bits where that does (a 64-bit division is a
+// subroutine of some 100 instructions, and a CTA starts with several).
+DV_DEV long long quot(long long a, long long b)
+{
+    return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
+// The batch row of place w.
+DV_DEV int sched_row(const KvAttnArgs &a, const SchedSmem &sm, long long w)
+{
+    int b = 0;
+    for (int step = 128; step > 0; step >>= 1)  // largest b with pref[b] <= w
+        if (b + step < a.B && sm.pref[b + step] <= w)
+            b += step;
+    return b;
+}
+
+// w, or the start of the unit whose empty places it is among.
+DV_DEV long long sched_snap(const KvAttnArgs &a, const SchedSmem &sm, long long w)
+{
+    const int b = sched_row(a, sm, w), size = sm.tiles[b] + kUnitCost;
+    if (w >= sm.pref[a.B])
+        return w;
+    const long long at = w - sm.pref[b];
+    const int in = (int)(at - quot(at, size) * size);
+    return in <= kUnitCost ? w - in : w;
+}
 
 // Fills sm (every thread of the CTA calls it) and returns this CTA's run.
 template <bool BLOCK>
@@ -73,7 +107,7 @@ DV_DEV Run sched_init(const KvAttnArgs &a, int rows, SchedSmem &sm)
         }
         sm.tiles[b] = tiles;
         sm.mb[b] = mb;
-        sm.pref[b + 1] = (long long)tiles * mb * nsel;
+        sm.pref[b + 1] = (long long)(tiles ? tiles + kUnitCost : 0) * mb * nsel;
     }
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -100,27 +134,23 @@ DV_DEV Run sched_init(const KvAttnArgs &a, int rows, SchedSmem &sm)
     r.C = (int)min((long long)gridDim.x, r.W);
     r.c = blockIdx.x;
     r.nsel = nsel;
-    r.lo = r.c < r.C ? r.W * r.c / r.C : 0;
-    r.hi = r.c < r.C ? r.W * (r.c + 1) / r.C : 0;
+    r.lo = r.c < r.C ? sched_snap(a, sm, quot(r.W * r.c, r.C)) : 0;
+    r.hi = r.c < r.C ? sched_snap(a, sm, quot(r.W * (r.c + 1), r.C)) : 0;
     return r;
 }
 
-// The unit of tile w (0 <= w < W).
+// The unit of place w (0 <= w < W).
 template <bool BLOCK>
 DV_DEV Unit sched_unit(const KvAttnArgs &a, int rows, const SchedSmem &sm, const Run &r,
                        long long w)
 {
-    int b = 0;
-    for (int step = 128; step > 0; step >>= 1)  // largest b with pref[b] <= w
-        if (b + step < a.B && sm.pref[b + step] <= w)
-            b += step;
-    const int tiles = sm.tiles[b], mb = sm.mb[b];
-    const int u = (int)((w - sm.pref[b]) / tiles);
+    const int b = sched_row(a, sm, w), size = sm.tiles[b] + kUnitCost, mb = sm.mb[b];
+    const int u = (int)quot(w - sm.pref[b], size);
     const int j = u / mb, m = u - j * mb;
     Unit x;
     x.b = b;
-    x.w0 = sm.pref[b] + (long long)u * tiles;
-    x.w1 = x.w0 + tiles;
+    x.w0 = sm.pref[b] + (long long)u * size;
+    x.w1 = x.w0 + size;
     x.len = __ldg(a.lens + b);
     if (BLOCK) {
         x.h = j;
@@ -143,6 +173,10 @@ DV_DEV Unit sched_unit(const KvAttnArgs &a, int rows, const SchedSmem &sm, const
     }
     return x;
 }
+
+// Tile of place w of unit x; the first place from w on that has one.
+DV_DEV int tile_of(const Unit &x, long long w) { return (int)(w - x.w0) - kUnitCost; }
+DV_DEV long long tile_place(const Unit &x, long long w) { return max(w, x.w0 + kUnitCost); }
 
 // Offset of a unit's query row among the given ones, and of its result.
 template <bool BLOCK>
@@ -190,97 +224,141 @@ DV_DEV int block_pos(const KvAttnArgs &a, const Unit &x, int i)
 
 DV_DEV float row_result(float o, float l) { return l == 0.f ? 0.f : o / l; }
 
-constexpr int kMergePieces = 16;  // pieces whose weights are in shared memory at a time
+constexpr int kMergePieces = 32;  // pieces whose weights are held in shared memory
 
-// A run's part of a unit is done: so[RM * D] (in the kernel's own order: at(row,
-// d) is the place of a value), u_m, u_l [RM] hold it merged over the CTA,
-// visible to every thread (m in units of log2).  Writes the result, or a
-// piece, and merges the pieces if it is the last.  Every thread of the CTA
-// (NTHR of them) calls it; the buffers may be reused after it returns.
-template <bool BLOCK, int RM, int NTHR, class F, class R>
-DV_DEV void finish_unit(const KvAttnArgs &a, const Run &r, const Unit &x, SchedSmem &sm,
-                        float *so, float *u_m, float *u_l, float (*wgt)[RM], F at, R rowof)
-{
-    const int D = a.c.D, n4 = RM * D / 4;
-    if (!(r.lo <= x.w0 && x.w1 <= r.hi)) {
+struct CtaSync {
+    DV_DEV static void sync() { __syncthreads(); }
+};
+
+// What becomes of a run's part of each unit.  NTHR threads (which meet in S)
+// call it together.
+template <bool BLOCK, int RM, int NTHR, class S = CtaSync>
+struct Finish {
+    long long w[2];  // first place of the units this CTA left a piece of
+    int got[2], n = 0;
+
+    // A part is done: val(row, d) and u_m, u_l [RM] give it merged over the
+    // CTA, visible to every thread (m in units of log2).  Writes the result,
+    // or a piece; whether the piece was the last of its unit is asked for
+    // here and looked at in end(), a memory round trip later.
+    template <class F>
+    DV_DEV void part(const KvAttnArgs &a, const Run &r, const Unit &x, F val, const float *u_m,
+                     const float *u_l)
+    {
+        const int D = a.c.D, lg = __ffs(D) - 1, items = x.nrows * D / 4;
+        const bool whole = r.lo <= x.w0 && x.w1 <= r.hi;
+        float *rec = a.rec + (2 * (size_t)r.c + (x.w0 > r.lo)) * ((size_t)RM * (D + 2));
+        for (int i = threadIdx.x; i < items; i += NTHR) {
+            const int row = (4 * i) >> lg, d = (4 * i) & (D - 1);
+            float4 v = make_float4(val(row, d), val(row, d + 1), val(row, d + 2), val(row, d + 3));
+            if (whole) {
+                const float l = u_l[row];
+                v = make_float4(row_result(v.x, l), row_result(v.y, l), row_result(v.z, l),
+                                row_result(v.w, l));
+                *reinterpret_cast<float4 *>(a.out + out_at<BLOCK>(a, x, row) + d) = v;
+            } else {
+                __stcg(reinterpret_cast<float4 *>(rec) + i, v);
+            }
+        }
+        if (!whole)
+            for (int i = threadIdx.x; i < x.nrows; i += NTHR) {
+                __stcg(rec + RM * D + i, u_m[i]);
+                __stcg(rec + RM * D + RM + i, u_l[i]);
+            }
+        S::sync();
+        if (!whole) {
+            // release of the CTA's stores above (ordered before it by the
+            // barrier), acquire of the other pieces'
+            if (threadIdx.x == 0)
+                asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                             : "=r"(got[n])
+                             : "l"(a.cnt + first_cta(r, x))
+                             : "memory");
+            w[n++] = x.w0;
+        }
+    }
+
+    DV_DEV static int first_cta(const Run &r, const Unit &x)
+    {
+        return (int)quot((x.w0 + kUnitCost + 1) * r.C - 1, r.W);
+    }
+
+    // The run is over: merges the units whose last piece was this CTA's, in
+    // the order of their positions.
+    DV_DEV void end(const KvAttnArgs &a, const Run &r, SchedSmem &sm, float *u_m, float *u_l,
+                    float (*wgt)[RM])
+    {
+        const int D = a.c.D, lg = __ffs(D) - 1, lane = threadIdx.x & 31;
         const size_t rsz = (size_t)RM * (D + 2);
-        float *rec = a.rec + (2 * (size_t)r.c + (x.w0 > r.lo)) * rsz;
-        for (int i = threadIdx.x; i < n4; i += NTHR)
-            __stcg(reinterpret_cast<float4 *>(rec) + i, reinterpret_cast<const float4 *>(so)[i]);
-        for (int i = threadIdx.x; i < RM; i += NTHR) {
-            __stcg(rec + RM * D + i, u_m[i]);
-            __stcg(rec + RM * D + RM + i, u_l[i]);
-        }
-        __threadfence();
-        __syncthreads();
-        const int c0 = (int)(((x.w0 + 1) * r.C - 1) / r.W), c1 = (int)((x.w1 * r.C - 1) / r.W);
-        if (threadIdx.x == 0)
-            sm.last = atomicAdd(a.cnt + c0, 1) == c1 - c0;
-        __syncthreads();
-        if (!sm.last)
-            return;
-        __threadfence();
-        // record of piece c (the unit's first CTA has it after its run's start, or at it)
-        auto piece = [&](int c) {
-            const bool late = c == c0 && x.w0 > r.W * c / r.C;
-            return a.rec + (2 * (size_t)c + late) * rsz;
-        };
-        const int lane = threadIdx.x & 31;
-        for (int row = threadIdx.x >> 5; row < RM; row += NTHR / 32) {
-            float M = -INFINITY, L = 0.f;
-            for (int c = c0 + lane; c <= c1; c += 32)
-                M = fmaxf(M, __ldcg(piece(c) + RM * D + row));
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            const float ms = M == -INFINITY ? 0.f : M;
-            for (int c = c0 + lane; c <= c1; c += 32) {
-                const float *p = piece(c) + RM * D;
-                L = fmaf(__ldcg(p + RM + row), exp2f(__ldcg(p + row) - ms), L);
+        for (int i = 0; i < 2; ++i) {
+            if (i >= n)
+                break;
+            const Unit x = sched_unit<BLOCK>(a, RM, sm, r, w[i]);
+            const int c0 = first_cta(r, x), c1 = (int)quot(x.w1 * r.C - 1, r.W), np = c1 - c0 + 1;
+            if (threadIdx.x == 0)
+                sm.last = got[i] == np - 1;
+            S::sync();
+            const bool last = sm.last;
+            S::sync();
+            if (!last)
+                continue;
+            // records: the unit's first CTA has it after its run's start, or at it
+            const float *rec0 = a.rec + (2 * (size_t)c0 + (x.w0 > quot(r.W * c0, r.C))) * rsz;
+            auto piece = [&](int k) {
+                return k == 0 ? rec0 : a.rec + 2 * (size_t)(c0 + k) * rsz;
+            };
+            for (int row = threadIdx.x >> 5; row < x.nrows; row += NTHR / 32) {
+                float M = -INFINITY, L = 0.f, mine = -INFINITY;
+                for (int k = lane; k < np; k += 32) {
+                    const float *p = piece(k) + RM * D + row;
+                    const float m = __ldcg(p), l = __ldcg(p + RM);
+                    const float mn = fmaxf(M, m), ms = mn == -INFINITY ? 0.f : mn;
+                    L = L * exp2f(M - ms) + l * exp2f(m - ms);
+                    M = mn;
+                    if (k < 32)
+                        mine = m;
+                }
+                float top = M;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float ms = top == -INFINITY ? 0.f : top;
+                L = warp_sum(L * exp2f(M - ms));
+                if (lane < kMergePieces)
+                    wgt[lane][row] = exp2f(mine - ms);
+                if (lane == 0) {
+                    u_m[row] = ms;
+                    u_l[row] = L;
+                }
             }
-            L = warp_sum(L);
-            if (lane == 0) {
-                u_m[row] = ms;
-                u_l[row] = L;
-            }
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < n4; i += NTHR)
-            reinterpret_cast<float4 *>(so)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int cb = c0; cb <= c1; cb += kMergePieces) {
-            const int nc = min(kMergePieces, c1 - cb + 1);
-            for (int i = threadIdx.x; i < nc * RM; i += NTHR) {
-                const int k = i / RM, row = i - k * RM;
-                wgt[k][row] = exp2f(__ldcg(piece(cb + k) + RM * D + row) - u_m[row]);
-            }
-            __syncthreads();
-            for (int i = threadIdx.x; i < n4; i += NTHR) {
-                float4 acc = reinterpret_cast<float4 *>(so)[i];
-                const int row = rowof(4 * i);
+            S::sync();
+            for (int it = threadIdx.x; it < x.nrows * D / 4; it += NTHR) {
+                const int row = (4 * it) >> lg, d = (4 * it) & (D - 1);
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-                for (int k = 0; k < nc; ++k) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(piece(cb + k)) + i);
-                    const float wt = wgt[k][row];
-                    // (a piece without a seen position has zeros, whatever else is NaN)
+                for (int k = 0; k < np; ++k) {
+                    const float *p = piece(k);
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(p) + it);
+                    const float wt = k < kMergePieces
+                                         ? wgt[k][row]
+                                         : exp2f(__ldcg(p + RM * D + row) - u_m[row]);
                     acc.x = fmaf(v.x, wt, acc.x);
                     acc.y = fmaf(v.y, wt, acc.y);
                     acc.z = fmaf(v.z, wt, acc.z);
                     acc.w = fmaf(v.w, wt, acc.w);
                 }
-                reinterpret_cast<float4 *>(so)[i] = acc;
+                const float l = u_l[row];
+                *reinterpret_cast<float4 *>(a.out + out_at<BLOCK>(a, x, row) + d) =
+                    make_float4(row_result(acc.x, l), row_result(acc.y, l), row_result(acc.z, l),
+                                row_result(acc.w, l));
             }
-            __syncthreads();
+            if (threadIdx.x == 0)
+                a.cnt[c0] = 0;  // ready for the next call
+            S::sync();
         }
-        if (threadIdx.x == 0)
-            a.cnt[c0] = 0;  // ready for the next call
     }
-    const int lg = __ffs(D) - 1;
-    for (int i = threadIdx.x; i < x.nrows * D; i += NTHR) {
-        const int row = i >> lg, d = i & (D - 1);
-        a.out[out_at<BLOCK>(a, x, row) + d] = row_result(so[at(row, d)], u_l[row]);
-    }
-    __syncthreads();
-}
+};
 
 }  // namespace
 }  // namespace dv

@@ -1,0 +1,157 @@
+// dv_kv_tma.cuh -- barriers, tensor-map copies and small arithmetic shared by
+// the KV attention kernels on tensor cores (sm_103a).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "dv_kv_sched.cuh"
+
+namespace dv {
+namespace {
+
+DV_DEV unsigned smem_addr(const void *p) { return (unsigned)__cvta_generic_to_shared(p); }
+
+DV_DEV void bar_init(unsigned bar, int count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+DV_DEV void bar_expect(unsigned bar, int bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                 "r"(bytes)
+                 : "memory");
+}
+DV_DEV void bar_arrive(unsigned bar)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// True once the phase with this parity is complete; false after a limit of
+// polls (each waits up to the hardware's own limit).
+constexpr int kKvSpin = 1 << 20;
+DV_DEV bool bar_wait(unsigned bar, unsigned parity)
+{
+    for (int it = 0; it < kKvSpin; ++it) {
+        unsigned ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok)
+            return true;
+    }
+    return false;
+}
+
+// Box at (byte x of the rows, position, (row, head)) of a cache side.
+DV_DEV void tma_load(unsigned dst, const CUtensorMap *map, int x, int pos, int bh, unsigned bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(pos), "r"(bh), "r"(bar)
+        : "memory");
+}
+
+DV_DEV void cp4(unsigned dst, const void *src, bool on)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(on ? 4 : 0)
+                 : "memory");
+}
+DV_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+DV_DEV void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+DV_DEV uint4 lds16(unsigned a)
+{
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "r"(a));
+    return r;
+}
+DV_DEV uint2 lds8(unsigned a)
+{
+    uint2 r;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    return r;
+}
+
+DV_DEV unsigned h2(float a, float b)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const unsigned *>(&h);
+}
+// The part of (a, b) that the binary16 pair `hi` leaves.
+DV_DEV unsigned h2_rest(float a, float b, unsigned hi)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    return h2(a - f.x, b - f.y);
+}
+
+DV_DEV float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+DV_DEV float quad_max(float v)
+{
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+
+// Four values of a query row, already scaled for the softmax, as binary16 high
+// and low parts {hi01, hi23}, {lo01, lo23} after a power of two takes the
+// row's largest element into [2^13, 2^14); *inv undoes it.  The lanes of a
+// warp hold the row (v: zeros past its end).
+struct SplitQ {
+    unsigned hi01, hi23, lo01, lo23;
+};
+DV_DEV SplitQ split_row(float4 v, float scale, float *inv)
+{
+    v = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+    float mx = amax3(amax2(v.x, v.y), v.z, v.w);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        mx = amax2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    int e = 0;
+    if (mx > 0.f && mx <= 3.402823466e38f)
+        frexpf(mx, &e);
+    e = min(max(14 - e, -126), 100);
+    const float al = ldexpf(1.f, e);
+    *inv = ldexpf(1.f, -e);
+    SplitQ q;
+    q.hi01 = h2(v.x * al, v.y * al);
+    q.hi23 = h2(v.z * al, v.w * al);
+    q.lo01 = h2_rest(v.x * al, v.y * al, q.hi01);
+    q.lo23 = h2_rest(v.z * al, v.w * al, q.hi23);
+    return q;
+}
+
+template <bool BLOCK>
+DV_DEV int unit_bh(const KvAttnArgs &a, const Unit &u)
+{
+    return u.b * a.c.Hkv + (BLOCK ? u.h / (a.H / a.c.Hkv) : u.h);
+}
+
+template <class K>
+cudaError_t kv_occupancy(K kern, int threads, size_t smem, int *per_sm)
+{
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+    if (e == cudaSuccess)
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, kern, threads, smem);
+    if (e == cudaSuccess && *per_sm < 1)
+        e = cudaErrorInvalidConfiguration;
+    return e;
+}
+
+}  // namespace
+}  // namespace dv
