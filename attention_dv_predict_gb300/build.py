@@ -21,7 +21,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdv.so")
 SOURCES = ["dv_abi.cu", "dv_rowdot.cu", "dv_colacc.cu", "dv_colacc_mma.cu", "dv_attn.cu",
            "dv_select.cu", "dv_stream.cu", "dv_mlp.cu", "dv_kv_abi.cu", "dv_kv_write.cu",
-           "dv_kv_topk.cu", "dv_kv_attn.cu", "dv_kv_mma.cu"]
+           "dv_kv_topk.cu", "dv_kv_attn.cu", "dv_kv_mma.cu", "dv_kv_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

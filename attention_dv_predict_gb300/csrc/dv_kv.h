@@ -108,6 +108,7 @@ struct KvMaps {
 };
 cudaError_t kv_maps(const KvCacheArgs &c, int B, int rows, KvMaps *m);
 cudaError_t launch_kv_mma(const KvAttnArgs &a, int nsm, cudaStream_t st);
+cudaError_t launch_kv_tc(const KvAttnArgs &a, int nsm, cudaStream_t st);
 cudaError_t launch_kv_attn(const KvAttnArgs &a, const KvPlan &p, int nsm, cudaStream_t st);
 
 }  // namespace dv

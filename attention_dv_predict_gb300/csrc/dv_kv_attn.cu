@@ -206,20 +206,20 @@ cudaError_t launch_gen(const KvAttnArgs &a, int grid, cudaStream_t st)
 
 }  // namespace
 
-// The tensor-core kernel serves binary16 and 8-bit rows of 64 and 128 values;
-// units of 8, 16, 32 or 64 query rows, the smallest that holds a token set.
+// Tensor cores serve binary16 and 8-bit rows of 64 and 128 values: units of 8
+// query rows on mma.sync, of 64 on tcgen05.
 KvPlan kv_plan(int dtype, int D, int rows)
 {
     KvPlan p;
     p.mma = dtype != DV_F32 && (D == 64 || D == 128);
-    p.rows = p.mma ? 8 : kKvGenRows;
+    p.rows = !p.mma ? kKvGenRows : rows <= 8 ? 8 : 64;
     return p;
 }
 
 cudaError_t launch_kv_attn(const KvAttnArgs &a, const KvPlan &p, int nsm, cudaStream_t st)
 {
     if (p.mma)
-        return launch_kv_mma(a, nsm, st);
+        return p.rows == 8 ? launch_kv_mma(a, nsm, st) : launch_kv_tc(a, nsm, st);
     const int grid = nsm * 4 < kKvMaxCtas ? nsm * 4 : kKvMaxCtas;
     if (a.c.dtype == DV_I8)
         return launch_gen<int8_t>(a, grid, st);

@@ -25,19 +25,19 @@ DV_DEV void bar_arrive(unsigned bar)
 {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// True once the phase with this parity is complete; false after a limit of
-// polls (each waits up to the hardware's own limit).
-constexpr int kKvSpin = 1 << 20;
+// True once the phase with this parity is complete; false after 2^21 polls
+// of at most a microsecond each.
+constexpr int kKvSpin = 1 << 21;
 DV_DEV bool bar_wait(unsigned bar, unsigned parity)
 {
     for (int it = 0; it < kKvSpin; ++it) {
         unsigned ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
-            : "r"(bar), "r"(parity)
+            : "r"(bar), "r"(parity), "r"(1000)
             : "memory");
         if (ok)
             return true;
