@@ -81,6 +81,7 @@ struct KvAttnArgs {
     int k;
     int blog;              // log2(block)
     int B, H, T;
+    float r_group;         // 1 / (query heads per KV head)
     float scale;           // softmax scale x log2(e)
     float *out;            // [B][T][H][D]
     // workspace

@@ -274,6 +274,7 @@ int dv_tree_attn(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_r
     a.B = batch;
     a.H = desc->n_heads;
     a.T = tokens;
+    a.r_group = (float)desc->n_kv_heads / (float)desc->n_heads;
     a.scale = scale * 1.4426950408889634f;
     a.out = out;
     a.rec = at<float>(ws, kKvRecOff);
@@ -334,6 +335,7 @@ int dv_block_attn(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_
     a.B = batch;
     a.H = desc->n_heads;
     a.T = 1;
+    a.r_group = (float)desc->n_kv_heads / (float)desc->n_heads;
     a.scale = scale * 1.4426950408889634f;
     a.out = out;
     a.rec = at<float>(ws, kKvRecOff);

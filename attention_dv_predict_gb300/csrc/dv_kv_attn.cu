@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kGenThreads) k_kv_attn(const KvAttnArgs a)
         unsigned long long bits[RM];
 #pragma unroll
         for (int r = 0; r < RM; ++r)
-            bits[r] = !BLOCK && r < x.nrows ? seen_bits(a, x, (x.row0 + r) / G) : 0ull;
+            bits[r] = !BLOCK && r < x.nrows ? seen_bits(a, x, row_token(a, x.row0 + r)) : 0ull;
         __syncthreads();
         const size_t base =
             ((size_t)x.b * a.c.Hkv + (BLOCK ? x.h / G : x.h)) * (size_t)a.c.cap;

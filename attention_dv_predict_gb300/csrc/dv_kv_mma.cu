@@ -88,7 +88,6 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
     float *so = reinterpret_cast<float *>(smem + C::RING + C::SCALES + C::QF);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
-    const int G = a.H / a.c.Hkv;
     if (lane == 0) {
         for (int i = 0; i < C::NST; ++i)
             bar_init(smem_addr(&s_bar[warp][i]), 1);
@@ -196,7 +195,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
         __syncthreads();
         const float inv = x.h >= 0 ? s_inv[g] : 0.f;
         const unsigned long long bits =
-            !BLOCK && g < x.nrows ? seen_bits(a, x, (x.row0 + g) / G) : 0ull;
+            !BLOCK && g < x.nrows ? seen_bits(a, x, row_token(a, x.row0 + g)) : 0ull;
 
         float o[NT][4];
 #pragma unroll

@@ -178,13 +178,16 @@ DV_DEV Unit sched_unit(const KvAttnArgs &a, int rows, const SchedSmem &sm, const
 DV_DEV int tile_of(const Unit &x, long long w) { return (int)(w - x.w0) - kUnitCost; }
 DV_DEV long long tile_place(const Unit &x, long long w) { return max(w, x.w0 + kUnitCost); }
 
+// Drafted token of query row n (n / group size; n < 2^14).
+DV_DEV int row_token(const KvAttnArgs &a, int n) { return (int)((n + 0.5f) * a.r_group); }
+
 // Offset of a unit's query row among the given ones, and of its result.
 template <bool BLOCK>
 DV_DEV long long q_at(const KvAttnArgs &a, const Unit &x, int r)
 {
     if (BLOCK)
         return x.b * a.q.sb + x.h * a.q.sh;
-    const int G = a.H / a.c.Hkv, t = (x.row0 + r) / G, g = (x.row0 + r) - t * G;
+    const int G = a.H / a.c.Hkv, t = row_token(a, x.row0 + r), g = (x.row0 + r) - t * G;
     return x.b * a.q.sb + t * a.q.st + (long long)(x.h * G + g) * a.q.sh;
 }
 template <bool BLOCK>
@@ -192,7 +195,7 @@ DV_DEV size_t out_at(const KvAttnArgs &a, const Unit &x, int r)
 {
     if (BLOCK)
         return ((size_t)x.b * a.H + x.h) * a.c.D;
-    const int G = a.H / a.c.Hkv, t = (x.row0 + r) / G, g = (x.row0 + r) - t * G;
+    const int G = a.H / a.c.Hkv, t = row_token(a, x.row0 + r), g = (x.row0 + r) - t * G;
     return (((size_t)x.b * a.T + t) * a.H + x.h * G + g) * a.c.D;
 }
 
@@ -222,7 +225,12 @@ DV_DEV int block_pos(const KvAttnArgs &a, const Unit &x, int i)
     return p < x.len ? p : -1;
 }
 
-DV_DEV float row_result(float o, float l) { return l == 0.f ? 0.f : o / l; }
+// o / l by the reciprocal (one more rounding); 0 where nothing was seen.
+DV_DEV float4 row_result(const float4 &o, float l)
+{
+    const float r = l == 0.f ? 0.f : __frcp_rn(l);
+    return make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
+}
 
 constexpr int kMergePieces = 32;  // pieces whose weights are held in shared memory
 
@@ -252,10 +260,8 @@ struct Finish {
             const int row = (4 * i) >> lg, d = (4 * i) & (D - 1);
             float4 v = make_float4(val(row, d), val(row, d + 1), val(row, d + 2), val(row, d + 3));
             if (whole) {
-                const float l = u_l[row];
-                v = make_float4(row_result(v.x, l), row_result(v.y, l), row_result(v.z, l),
-                                row_result(v.w, l));
-                *reinterpret_cast<float4 *>(a.out + out_at<BLOCK>(a, x, row) + d) = v;
+                *reinterpret_cast<float4 *>(a.out + out_at<BLOCK>(a, x, row) + d) =
+                    row_result(v, u_l[row]);
             } else {
                 __stcg(reinterpret_cast<float4 *>(rec) + i, v);
             }
@@ -348,10 +354,8 @@ struct Finish {
                     acc.z = fmaf(v.z, wt, acc.z);
                     acc.w = fmaf(v.w, wt, acc.w);
                 }
-                const float l = u_l[row];
                 *reinterpret_cast<float4 *>(a.out + out_at<BLOCK>(a, x, row) + d) =
-                    make_float4(row_result(acc.x, l), row_result(acc.y, l), row_result(acc.z, l),
-                                row_result(acc.w, l));
+                    row_result(acc, u_l[row]);
             }
             if (threadIdx.x == 0)
                 a.cnt[c0] = 0;  // ready for the next call

@@ -15,14 +15,15 @@
 //             own score, weight and output columns in tensor memory; they are
 //             merged when a unit ends, so neither waits for the other
 //   8-11      8-bit caches: codes to binary16, raw ring -> operand ring
-//   next      one warp of tensor-map copies (and scales by cp.async)
-//   last      one thread issuing the MMAs; its warp owns tensor memory
+//   next      one of tensor-map copies (and scales by cp.async)
+//   last      one whose elected thread issues the MMAs; owns tensor memory
 // Keys are the K-major operand of the scores; values, as they lie, the
 // MN-major operand of Q = softmax weights (A from tensor memory) x V.
 // Hand-overs are mbarriers; every wait has a limit (DV_ERR_TIMEOUT).
 //
-// The running max only moves when a row's scores exceed it by 2^8, so the
-// output in tensor memory is rarely rescaled; weights are kept below 2^14.
+// A row's reference point only moves when a weight leaves binary16's range
+// (dv_kv_tma.cuh), so the output in tensor memory is rarely rescaled and a
+// tile's softmax needs no reduction over the row.
 #include "dv_kv_tma.cuh"
 
 namespace dv {
@@ -153,6 +154,14 @@ DV_DEV void tm_st_pairs(unsigned addr, const unsigned (&r)[16])
         : "memory");
 }
 
+DV_DEV bool elect_one()
+{
+    unsigned p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(p));
+    return p != 0;
+}
+
 // A role's waits: after one has run out the others no longer wait (the
 // results are lost, the status says so, every loop still ends).
 struct Waiter {
@@ -279,60 +288,79 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             bar_wait(smem_addr(I8 ? &b_raw_full[k % (I8 ? C::NSR : 1)] : &b_kv_full[k % NSF]),
                      (k / NS) & 1);
     } else if (warp == W_MMA) {
-        // ---- products
-        if (lane == 0) {
-            constexpr uint32_t ID_S = tc_idesc(TP, false), ID_O = tc_idesc(D, true);
-            int i = 0, seg = 0, ph[2] = {0, 0};
-            for (long long w = run.lo; w < run.hi;) {
-                const Unit x = sched_unit<false>(a, RM, sm, run, w);
-                const long long wend = min(run.hi, x.w1);
-                if (x.h < 0) {
-                    w = wend;
-                    continue;
-                }
-                const int n = (int)(wend - tile_place(x, w));
-                w = wend;
-                wait(smem_addr(&b_q_full), seg & 1);
-                ++seg;
-                for (int t = 0; t <= n; ++t) {
-                    if (t < n) {
-                        const int st = (i + t) % NSF;
-                        wait(smem_addr(&b_kv_full[st]), ((i + t) / NSF) & 1);
-                        tc_fence_after();
-                        const unsigned kb = sbase + C::OFF_OP + st * 2 * C::OPER;
+        // ---- products.  The warp runs the loop together, so that descriptors
+        // stay in uniform registers, and one thread issues (with the loop in
+        // one thread, building them took longer than the products).
+        constexpr uint32_t ID_S = tc_idesc(TP, false), ID_O = tc_idesc(D, true);
+        constexpr unsigned STAGE = 2 * C::OPER >> 4;
+        const uint64_t dq = tc_desc(sbase, 16), dk0 = tc_desc(sbase + C::OFF_OP, 16),
+                       dv0 = tc_desc(sbase + C::OFF_OP + C::OPER, TP * 128);
+        const bool one = elect_one();
+        int st = 0, kvp = 0, sv = 0, seg = 0, pp = 0;  // stages; phases
+        for (long long w = run.lo; w < run.hi;) {
+            const Unit x = sched_unit<false>(a, RM, sm, run, w);
+            const long long wend = min(run.hi, x.w1);
+            int n = x.h < 0 ? 0 : (int)(wend - tile_place(x, w));
+            n = __shfl_sync(0xffffffffu, n, 0);
+            w = wend;
+            if (n == 0)
+                continue;
+            wait(smem_addr(&b_q_full), seg & 1);
+            ++seg;
+            for (int t = 0; t <= n; ++t) {
+                if (t < n) {
+                    wait(smem_addr(&b_kv_full[st]), kvp);
+                    tc_fence_after();
+                    const uint64_t dk = dk0 + (uint64_t)(unsigned)st * STAGE;
+                    if (one) {
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
                             tc_mma_ss(tmem + C::T_S + (t & 1) * 64,
-                                      tc_desc(sbase + (kk / 4) * (128 * 128) + (kk % 4) * 32, 16),
-                                      tc_desc(kb + (kk / 4) * (TP * 128) + (kk % 4) * 32, 16), ID_S,
-                                      kk > 0);
+                                      dq + (kk / 4) * (128 * 128 >> 4) + (kk % 4) * 2,
+                                      dk + (kk / 4) * (TP * 128 >> 4) + (kk % 4) * 2, ID_S, kk > 0);
                         tc_commit(smem_addr(&b_s_full[t & 1]));
                     }
-                    if (t > 0) {
-                        const int st = (i + t - 1) % NSF, g = (t - 1) & 1;
-                        wait(smem_addr(&b_p_full[g]), ph[g] & 1);
-                        ++ph[g];
-                        tc_fence_after();
-                        const unsigned vb = sbase + C::OFF_OP + st * 2 * C::OPER + C::OPER;
+                    __syncwarp();
+                    if (++st == NSF) {
+                        st = 0;
+                        kvp ^= 1;
+                    }
+                }
+                if (t > 0) {
+                    const int g = (t - 1) & 1;
+                    wait(smem_addr(&b_p_full[g]), (pp >> g) & 1);
+                    pp ^= 1 << g;
+                    tc_fence_after();
+                    const uint64_t dv = dv0 + (uint64_t)(unsigned)sv * STAGE;
+                    if (one) {
 #pragma unroll
                         for (int kk = 0; kk < TP / 16; ++kk)
                             tc_mma_ts(tmem + C::T_O + g * 128, tmem + C::T_P + g * 32 + kk * 8,
-                                      tc_desc(vb + kk * 16 * 128, TP * 128), ID_O,
-                                      t > 2 || kk > 0);
+                                      dv + kk * (16 * 128 >> 4), ID_O, t > 2 || kk > 0);
                         tc_commit(smem_addr(&b_pv_done[g]));
-                        tc_commit(smem_addr(&b_kv_empty[st]));
+                        tc_commit(smem_addr(&b_kv_empty[sv]));
                     }
+                    __syncwarp();
+                    sv = sv + 1 == NSF ? 0 : sv + 1;
                 }
-                i += n;
             }
-            tc_commit(smem_addr(&b_end));  // every product is done before tensor memory goes
-            bar_wait(smem_addr(&b_end), 0);
         }
+        if (one)
+            tc_commit(smem_addr(&b_end));  // every product is done before tensor memory goes
         __syncwarp();
-    } else if (I8 && warp >= 8) {
+        bar_wait(smem_addr(&b_end), 0);
+    } else if (I8 && warp >= 8 && warp < 12) {
         // ---- codes to binary16
-        const int cw = tid - 256;  // 0 .. 127
+        // A thread keeps its 16-byte chunk c and its row modulo 16 (32).  Eight
+        // lanes that access shared memory together take half of one row's chunks
+        // and the other half of the next one's, which keeps the swizzled reads
+        // and writes free of bank conflicts.
         constexpr int CPR = C::RB / 16;
+        const int cw = tid - 256, u = cw % (2 * CPR), odd = (u >> 2) & 1;
+        const int c = (u & 3) + (CPR == 8 ? 4 * (odd ^ (u >> 3)) : 0);
+        const int r = cw / (2 * CPR) * 2 + odd;
+        const unsigned src0 = r * C::RB + ((CPR == 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+        const unsigned dst0 = (c >> 2) * (TP * 128) + r * 128 + ((((2 * c) & 7) ^ (r & 7)) << 4);
         int i = 0;
         for (long long w = run.lo; w < run.hi;) {
             const Unit x = sched_unit<false>(a, RM, sm, run, w);
@@ -344,32 +372,26 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 wait(smem_addr(&b_raw_full[rs]), (i / (I8 ? C::NSR : 1)) & 1);
                 if (i >= NSF)
                     wait(smem_addr(&b_kv_empty[fs]), (i / NSF - 1) & 1);
-                const unsigned src = sbase + C::OFF_RAW + rs * 2 * C::RAW;
+                const unsigned src = sbase + C::OFF_RAW + rs * 2 * C::RAW + src0;
                 const unsigned dst = sbase + C::OFF_OP + fs * 2 * C::OPER;
-#pragma unroll 4
-                for (int id = cw; id < 2 * TP * CPR; id += 128) {
-                    const int side = id / (TP * CPR), r = id / CPR % TP, pc = id % CPR;
-                    // (the copy swizzled the row's chunks)
-                    const int c = C::RB == 64 ? pc ^ ((r >> 1) & 3) : pc ^ (r & 7);
-                    const uint4 u = lds16(src + side * C::RAW + r * C::RB + pc * 16);
-                    const unsigned b[4] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u,
-                                           u.w ^ 0x80808080u};
-                    const unsigned row = dst + side * C::OPER + (c >> 2) * (TP * 128) + r * 128;
-                    const unsigned e = row + ((((2 * c) & 7) ^ (r & 7)) << 4);
-                    const unsigned o = row + ((((2 * c + 1) & 7) ^ (r & 7)) << 4);
-                    const bool odd = c >= 4;  // the halves in turn: no bank conflicts
-                    const uint4 lo = make_uint4(codes_lo(b[0]), codes_hi(b[0]), codes_lo(b[1]),
-                                                codes_hi(b[1]));
-                    const uint4 hi = make_uint4(codes_lo(b[2]), codes_hi(b[2]), codes_lo(b[3]),
-                                                codes_hi(b[3]));
-                    const uint4 f = odd ? hi : lo, s = odd ? lo : hi;
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(odd ? o : e),
-                                 "r"(f.x), "r"(f.y), "r"(f.z), "r"(f.w)
-                                 : "memory");
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(odd ? e : o),
-                                 "r"(s.x), "r"(s.y), "r"(s.z), "r"(s.w)
-                                 : "memory");
-                }
+                constexpr int STEP = 128 / CPR;  // rows a pass
+#pragma unroll 1
+                for (int side = 0; side < 2; ++side)
+#pragma unroll
+                    for (int off = 0; off < TP; off += STEP) {
+                        const uint4 u = lds16(src + side * C::RAW + off * C::RB);
+                        const unsigned b0 = u.x ^ 0x80808080u, b1 = u.y ^ 0x80808080u,
+                                       b2 = u.z ^ 0x80808080u, b3 = u.w ^ 0x80808080u;
+                        const unsigned at = dst + side * C::OPER + off * 128;
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + dst0),
+                                     "r"(codes_lo(b0)), "r"(codes_hi(b0)), "r"(codes_lo(b1)),
+                                     "r"(codes_hi(b1))
+                                     : "memory");
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + (dst0 ^ 16)),
+                                     "r"(codes_lo(b2)), "r"(codes_hi(b2)), "r"(codes_lo(b3)),
+                                     "r"(codes_hi(b3))
+                                     : "memory");
+                    }
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -378,13 +400,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
             }
         }
-    } else {
+    } else if (warp < 8) {
         // ---- softmax
         const int wg = warp >> 2, ww = warp & 3, g = lane >> 2, t4 = lane & 3;
         const unsigned lanes = (unsigned)(32 * ww) << 16, low = 16u << 16;
         const unsigned tS = tmem + lanes + C::T_S + wg * 64, tO = tmem + lanes + C::T_O + wg * 128,
                        tP = tmem + lanes + C::T_P + wg * 32;
-        const int G = a.H / a.c.Hkv;
         Finish<false, RM, C::SOFT, SoftSync> fin;
         int i0 = 0, nt = 0;  // tile of the run; this group's tiles so far
         for (long long w = run.lo; w < run.hi;) {
@@ -395,12 +416,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 continue;
             const int n = (int)(wend - wb), tile0 = tile_of(x, wb);
             // the queries' parts (8 rows a warp)
-            for (int r = warp; r < RM; r += 8) {
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (r < x.nrows && lane * 4 < D)
-                    v = ld_row4(a.q, q_at<false>(a, x, r) + lane * 4);
+            float4 qv[RM / 8];
+#pragma unroll
+            for (int k = 0; k < RM / 8; ++k) {
+                const int r = warp + 8 * k;
+                qv[k] = r < x.nrows && lane * 4 < D
+                            ? ld_row4(a.q, q_at<false>(a, x, r) + lane * 4)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < RM / 8; ++k) {
+                const int r = warp + 8 * k;
                 float inv;
-                const SplitQ q = split_row(v, a.scale, &inv);
+                const SplitQ q = split_row(qv[k], a.scale, &inv);
                 if (lane * 4 < D) {
                     const int row = 32 * (r >> 4) + (r & 15), d = lane * 4;
                     unsigned char *p = smem + (d >> 6) * (128 * 128) + row * 128 +
@@ -416,16 +444,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             SoftSync::sync();
             if (lane == 0)
                 bar_arrive(smem_addr(&b_q_full));
-            float inv[2], m[2], l[2], sg[2];
+            float inv[2], m[2], l[2];
             unsigned long long bits[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int row = 16 * ww + g + 8 * r;
                 inv[r] = s_inv[row];
-                bits[r] = row < x.nrows ? seen_bits(a, x, (x.row0 + row) / G) : 0ull;
+                bits[r] = row < x.nrows ? seen_bits(a, x, row_token(a, x.row0 + row)) : 0ull;
                 m[r] = -INFINITY;
                 l[r] = 0.f;
-                sg[r] = 1.f;
             }
 
             for (int t = wg; t < n; t += 2, ++nt) {
@@ -433,41 +460,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const bool edge = p0 + TP > x.len;
                 wait(smem_addr(&b_s_full[wg]), nt & 1);
                 tc_fence_after();
-                float v[32], vl[32];
-                tm_ld64(tS, v);
-                tm_ld64(tS + low, vl);
-                const float *sc = scales + ((i0 + t) % C::NSC) * 2 * TP;
+                const float *sc = scales + ((i0 + t) % C::NSC) * 2 * TP + 2 * t4;
                 if (I8)
                     wait(smem_addr(&b_sc_full[(i0 + t) % C::NSC]), ((i0 + t) / C::NSC) & 1);
-                tm_wait_ld(v);
-                tm_wait_ld(vl);
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    v[e] += vl[e];
-                if (I8) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 k = *reinterpret_cast<const float2 *>(sc + 8 * j + 2 * t4);
-                        v[4 * j] *= k.x;
-                        v[4 * j + 1] *= k.y;
-                        v[4 * j + 2] *= k.x;
-                        v[4 * j + 3] *= k.y;
-                    }
-                }
                 unsigned seen[2] = {0xffffu, 0xffffu};  // bit 2 j + c: column 8 j + 2 t4 + c
                 if (edge) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
+                    for (int e = 0; e < 16; ++e) {
+                        const int q = p0 + 8 * (e >> 1) + 2 * t4 + (e & 1) - x.len;
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const int q = p0 + 8 * j + 2 * t4 + c - x.len;
-#pragma unroll
-                            for (int r = 0; r < 2; ++r)
-                                if (!(q < 0 || (q < 64 && ((bits[r] >> q) & 1)))) {
-                                    v[4 * j + 2 * r + c] = -INFINITY;
-                                    seen[r] &= ~(1u << (2 * j + c));
-                                }
-                        }
+                        for (int r = 0; r < 2; ++r)
+                            if (!(q < 0 || (q < 64 && ((bits[r] >> q) & 1))))
+                                seen[r] &= ~(1u << e);
+                    }
                     if (!I8) {
                         // a NaN or an infinity among the values must not reach rows
                         // that do not see it: taken out of the operand here
@@ -479,8 +484,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         unsigned char *vb = smem + C::OFF_OP + st * 2 * C::OPER + C::OPER;
                         for (int k = tid & 127; k < C::OPER / 16; k += 128) {
                             uint4 *q = reinterpret_cast<uint4 *>(vb) + k;
-                            uint4 u = *q;
-                            unsigned wd[4] = {u.x, u.y, u.z, u.w};
+                            const uint4 u = *q;
+                            const unsigned wd[4] = {u.x, u.y, u.z, u.w};
                             bool bad = false;
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
@@ -497,59 +502,107 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
                     }
                 }
-                float f[2];
-                unsigned ph[16], pl[16];
-                bool moved = false;
+                float v[32];
+                // scores (without the row's factor): v[4 j + 2 r + c]
+                auto scores = [&]() {
+                    float lo[32];
+                    tm_ld64(tS, v);
+                    tm_ld64(tS + low, lo);
+                    tm_wait_ld(v);
+                    tm_wait_ld(lo);
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float mx = v[2 * r];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        mx = fmaxf(mx, fmaxf(v[4 * j + 2 * r], v[4 * j + 2 * r + 1]));
-                    mx = quad_max(mx) * inv[r];
-                    f[r] = 1.f;
-                    if (mx > m[r] + 8.f) {
-                        f[r] = ex2(m[r] - mx);
-                        m[r] = mx;
-                    }
-                    const float ms = m[r] == -INFINITY ? 0.f : m[r];
-                    float sum = 0.f, big = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float &p = v[4 * j + 2 * r + c];
-                            p = ex2(fmaf(p, inv[r], -ms));
-                            sum += p;
-                        }
-                    l[r] = fmaf(l[r], f[r], sum);
-                    float up = 64.f;
+                    for (int e = 0; e < 32; e += 2)
+                        add2(v[e], v[e + 1], lo[e], lo[e + 1]);
                     if (I8) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const float2 k =
-                                *reinterpret_cast<const float2 *>(sc + TP + 8 * j + 2 * t4);
-                            float &p = v[4 * j + 2 * r], &q = v[4 * j + 2 * r + 1];
-                            p = (seen[r] >> (2 * j)) & 1 ? p * k.x : 0.f;
-                            q = (seen[r] >> (2 * j + 1)) & 1 ? q * k.y : 0.f;
-                            big = fmaxf(big, fmaxf(p, q));
+                            const float2 k = *reinterpret_cast<const float2 *>(sc + 8 * j);
+                            mul2(v[4 * j], v[4 * j + 1], k.x, k.y);
+                            mul2(v[4 * j + 2], v[4 * j + 3], k.x, k.y);
                         }
-                        // weights relative to about the largest so far
-                        big = fmaxf(sg[r] * f[r], quad_max(big));
-                        if (big >= 256.f * sg[r] || (big < sg[r] * 0x1p-10f && big > 0.f)) {
-                            const float now = fmaxf(
-                                __uint_as_float(__float_as_uint(big) & 0x7f800000u), 0x1p-100f);
-                            f[r] = f[r] * sg[r] / now;
-                            sg[r] = now;
-                        }
-                        up = 64.f / sg[r];
                     }
-                    moved |= f[r] != 1.f;
+                    if (edge) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((seen[(e >> 1) & 1] >> (2 * (e >> 2) + (e & 1))) & 1))
+                                v[e] = -INFINITY;
+                    }
+                };
+                // weights under references m0, m1; the sums of 2^(s - m) and
+                // the largest weight
+                auto weights = [&](float m0, float m1, float (&sum)[2], float (&big)[2]) {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float s0 = 0.f, s1 = 0.f;
+                        big[r] = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            float &p = v[4 * j + 2 * r], &q = v[4 * j + 2 * r + 1];
+                            fma2(p, q, inv[r], r ? -m1 : -m0);
+                            p = ex2(p);
+                            q = ex2(q);
+                            add2(s0, s1, p, q);
+                            if (I8) {
+                                const float2 k =
+                                    *reinterpret_cast<const float2 *>(sc + TP + 8 * j);
+                                mul2(p, q, k.x, k.y);
+                                if (edge) {
+                                    p = (seen[r] >> (2 * j)) & 1 ? p : 0.f;
+                                    q = (seen[r] >> (2 * j + 1)) & 1 ? q : 0.f;
+                                }
+                            }
+                            big[r] = fmaxf(fmaxf(big[r], p), q);
+                        }
+                        sum[r] = s0 + s1;
+                    }
+                };
+                float f[2] = {1.f, 1.f}, sum[2], big[2];
+                scores();
+                weights(m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1], sum, big);
+                bool moved = false;
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    moved |= !(big[r] <= kWeightMax && sum[r] <= kSumMax) || m[r] == -INFINITY;
+                moved = __any_sync(0xffffffffu, moved);
+                if (moved) {  // a row's first weights, or one out of range: rare
+                    scores();
+                    float mn[2], ms[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            top = fmaxf(top, fmaxf(v[4 * j + 2 * r], v[4 * j + 2 * r + 1]));
+                        mn[r] = ref_from_scores(m[r], quad_max(top) * inv[r]);
+                        ms[r] = mn[r] == -INFINITY ? 0.f : mn[r];
+                    }
+                    weights(ms[0], ms[1], sum, big);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float k = ref_shift(m[r] == -INFINITY, quad_max(big[r]));
+                        const float g2 = ex2(-k);
+                        mn[r] += k;
+                        sum[r] *= g2;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            mul2(v[4 * j + 2 * r], v[4 * j + 2 * r + 1], g2, g2);
+                        f[r] = mn[r] == -INFINITY ? 1.f : ex2(m[r] - mn[r]);
+                        m[r] = mn[r];
+                    }
+                }
+                unsigned ph[16], pl[16];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    l[r] = fmaf(l[r], f[r], sum[r]);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const float w0 = v[4 * j + 2 * r] * up, w1 = v[4 * j + 2 * r + 1] * up;
-                        ph[2 * j + r] = h2(w0, w1);
-                        pl[2 * j + r] = h2_rest(w0, w1, ph[2 * j + r]);
+                        const float p = v[4 * j + 2 * r], q = v[4 * j + 2 * r + 1];
+                        ph[2 * j + r] = h2(p, q);
+                        const float2 h =
+                            __half22float2(*reinterpret_cast<const __half2 *>(&ph[2 * j + r]));
+                        float dp = p, dq = q;
+                        add2(dp, dq, -h.x, -h.y);
+                        pl[2 * j + r] = h2(dp, dq);
                     }
                 }
                 if (!I8 && edge) {
@@ -568,7 +621,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 tc_fence_after();
                 tm_st_pairs(tP, ph);
                 tm_st_pairs(tP + low, pl);
-                if (t >= 2 && __any_sync(0xffffffffu, moved)) {
+                if (t >= 2 && moved) {
 #pragma unroll
                     for (int half = 0; half < 2; ++half)
 #pragma unroll
@@ -611,7 +664,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int r = 0; r < 2; ++r) {
                 const int row = 16 * ww + g + 8 * r;
                 const float M = fmaxf(s_m[0][row], s_m[1][row]), ms = M == -INFINITY ? 0.f : M;
-                fac[r] = ex2(m[r] - ms) * (sg[r] * (1.f / 64.f));
+                fac[r] = ex2(m[r] - ms);
                 if (wg == 0 && t4 == 0) {
                     u_m[row] = M;
                     u_l[row] = s_l[0][row] * ex2(s_m[0][row] - ms) +

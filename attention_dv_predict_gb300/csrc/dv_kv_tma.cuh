@@ -107,6 +107,59 @@ DV_DEV float quad_max(float v)
     return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
 
+// Two binary32 operations an instruction.
+DV_DEV unsigned long long pack2(float a, float b)
+{
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+DV_DEV void unpack2(unsigned long long v, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+DV_DEV void add2(float &a, float &b, float c, float d)
+{
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a, b)), "l"(pack2(c, d)));
+    unpack2(r, a, b);
+}
+DV_DEV void mul2(float &a, float &b, float c, float d)
+{
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a, b)), "l"(pack2(c, d)));
+    unpack2(r, a, b);
+}
+DV_DEV void fma2(float &a, float &b, float c, float d)  // a c + d, b c + d
+{
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(pack2(a, b)), "l"(pack2(c, c)), "l"(pack2(d, d)));
+    unpack2(r, a, b);
+}
+
+// A softmax row's reference point.  Weights are w_p = 2^(s_p - m) v_p (s: the
+// score in units of log2, v: the value row's scale, 1 in binary16 caches) and
+// l = sum 2^(s_p - m), o = sum w_p value_p, so m cancels from o / l and may be
+// anything that keeps w in binary16's range.  It is set so that a row's first
+// largest weight is between 1 and 2^14, and only raised when one exceeds
+// that: the low parts' last place, 2^-24, stays under the weights' sum times
+// binary32's, and no step needs a row's maximum.  m = -inf: nothing seen yet.
+constexpr float kWeightMax = 16384.f;
+constexpr float kWeightMin = 1.f;  // a row's first weights are shifted if all are smaller
+constexpr float kSumMax = 0x1p100f;  // 2^(s - m) itself must stay finite where v is tiny
+// The new reference for the scores' maximum top (over a row) before weights
+// are known, and its correction from the weights' maximum big under it.
+DV_DEV float ref_from_scores(float m, float top) { return fmaxf(m, top - 6.f); }
+DV_DEV float ref_shift(bool first, float big)
+{
+    if (!(big > 0.f) || !(big <= 3.402823466e38f))
+        return 0.f;
+    const float k = (float)((int)(__float_as_uint(big) >> 23) - 127 - 12);
+    return first ? fmaxf(k, -90.f) : fmaxf(k, 0.f);
+}
+
 // Four values of a query row, already scaled for the softmax, as binary16 high
 // and low parts {hi01, hi23}, {lo01, lo23} after a power of two takes the
 // row's largest element into [2^13, 2^14); *inv undoes it.  The lanes of a
@@ -121,12 +174,11 @@ DV_DEV SplitQ split_row(float4 v, float scale, float *inv)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         mx = amax2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    int e = 0;
-    if (mx > 0.f && mx <= 3.402823466e38f)
-        frexpf(mx, &e);
-    e = min(max(14 - e, -126), 100);
-    const float al = ldexpf(1.f, e);
-    *inv = ldexpf(1.f, -e);
+    // (its exponent field; none for a row that is zero or not finite)
+    const int field = (int)(__float_as_uint(mx) >> 23);
+    const int e = field == 255 || mx == 0.f ? 0 : min(140 - field, 100);
+    const float al = __int_as_float((127 + e) << 23);
+    *inv = __int_as_float((127 - e) << 23);
     SplitQ q;
     q.hi01 = h2(v.x * al, v.y * al);
     q.hi23 = h2(v.z * al, v.w * al);
