@@ -178,13 +178,21 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
         const Unit x = sched_unit<BLOCK>(a, RM, sm, run, w);
         const long long wend = min(run.hi, x.w1);
         // ---- queries: scaled, split, in fragment order (two rows a warp)
-        if (x.h >= 0)
-            for (int r = warp; r < RM; r += WP) {
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (r < x.nrows && lane * 4 < D)
-                    v = ld_row4(a.q, q_at<BLOCK>(a, x, r) + lane * 4);
+        if (x.h >= 0) {
+            constexpr int N = RM / WP;
+            long long at[N];
+            float4 v[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int r = warp + WP * i;
+                at[i] = r < x.nrows && lane * 4 < D ? q_at<BLOCK>(a, x, r) + lane * 4 : -1;
+            }
+            ld_queries(a.q, at, v);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int r = warp + WP * i;
                 float inv;
-                const SplitQ q = split_row(v, a.scale, &inv);
+                const SplitQ q = split_row(v[i], a.scale, &inv);
                 constexpr int EPC = C::I8 ? 16 : 8, SPC = EPC / 4;  // steps per 16-byte chunk
                 const int c = lane * 4 / EPC, s = SPC * (c / 4) + lane % SPC;
                 if (lane * 4 < D)
@@ -192,6 +200,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
                 if (lane == 0)
                     s_inv[r] = inv;
             }
+        }
         __syncthreads();
         const float inv = x.h >= 0 ? s_inv[g] : 0.f;
         const unsigned long long bits =

@@ -162,7 +162,7 @@ DV_DEV Unit sched_unit(const KvAttnArgs &a, int rows, const SchedSmem &sm, const
         const int G = a.H / a.c.Hkv;
         x.h = a.u_h ? __ldg(a.u_h + j) : j;
         if (x.h < 0 || x.h >= a.c.Hkv) {
-            if (threadIdx.x == 0)
+            if ((threadIdx.x & 31) == 0)
                 set_status(a.status, DV_ERR_DEVICE_INDEX);
             x.h = -1;
         }
@@ -254,33 +254,50 @@ struct Finish {
                      const float *u_l)
     {
         const int D = a.c.D, lg = __ffs(D) - 1, items = x.nrows * D / 4;
-        const bool whole = r.lo <= x.w0 && x.w1 <= r.hi;
-        float *rec = a.rec + (2 * (size_t)r.c + (x.w0 > r.lo)) * ((size_t)RM * (D + 2));
+        const bool all = whole(r, x);
+        float *rec = record(a, r, x);
         for (int i = threadIdx.x; i < items; i += NTHR) {
             const int row = (4 * i) >> lg, d = (4 * i) & (D - 1);
-            float4 v = make_float4(val(row, d), val(row, d + 1), val(row, d + 2), val(row, d + 3));
-            if (whole) {
+            const float4 v =
+                make_float4(val(row, d), val(row, d + 1), val(row, d + 2), val(row, d + 3));
+            if (all)
                 *reinterpret_cast<float4 *>(a.out + out_at<BLOCK>(a, x, row) + d) =
                     row_result(v, u_l[row]);
-            } else {
+            else
                 __stcg(reinterpret_cast<float4 *>(rec) + i, v);
-            }
         }
-        if (!whole)
+        if (!all)
             for (int i = threadIdx.x; i < x.nrows; i += NTHR) {
                 __stcg(rec + RM * D + i, u_m[i]);
                 __stcg(rec + RM * D + RM + i, u_l[i]);
             }
+        done(a, r, x);
+    }
+
+    // The unit lies within the run; the record of this CTA's piece of it, [RM][D]
+    // values, then m and l [RM] each.
+    DV_DEV static bool whole(const Run &r, const Unit &x) { return r.lo <= x.w0 && x.w1 <= r.hi; }
+    DV_DEV static float *record(const KvAttnArgs &a, const Run &r, const Unit &x)
+    {
+        return a.rec + (2 * (size_t)r.c + (x.w0 > r.lo)) * ((size_t)RM * (a.c.D + 2));
+    }
+
+    // The part's stores are made.
+    DV_DEV void done(const KvAttnArgs &a, const Run &r, const Unit &x)
+    {
         S::sync();
-        if (!whole) {
+        if (!whole(r, x)) {
             // release of the CTA's stores above (ordered before it by the
             // barrier), acquire of the other pieces'
-            if (threadIdx.x == 0)
+            if (threadIdx.x == 0) {
+                int was;
                 asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
-                             : "=r"(got[n])
+                             : "=r"(was)
                              : "l"(a.cnt + first_cta(r, x))
                              : "memory");
-            w[n++] = x.w0;
+                got[n & 1] = was;
+            }
+            w[n++ & 1] = x.w0;
         }
     }
 

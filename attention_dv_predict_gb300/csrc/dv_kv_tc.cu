@@ -12,11 +12,13 @@
 //
 // Warps of a CTA (one CTA per SM):
 //   0-3, 4-7  two softmax groups that take turns at the tiles, each with its
-//             own score, weight and output columns in tensor memory; they are
-//             merged when a unit ends, so neither waits for the other
+//             own output columns in tensor memory; they are merged when a unit
+//             ends, so neither waits for the other.  Four score buffers, whose
+//             weights take the scores' place, let scores run three tiles ahead
 //   8-11      8-bit caches: codes to binary16, raw ring -> operand ring
-//   next      one of tensor-map copies (and scales by cp.async)
-//   last      one whose elected thread issues the MMAs; owns tensor memory
+//   last four one that prepares a unit's queries while the unit before runs,
+//             one of tensor-map copies (and scales by cp.async), one whose
+//             elected thread issues the scores' MMAs, one the values'
 // Keys are the K-major operand of the scores; values, as they lie, the
 // MN-major operand of Q = softmax weights (A from tensor memory) x V.
 // Hand-overs are mbarriers; every wait has a limit (DV_ERR_TIMEOUT).
@@ -35,21 +37,23 @@ struct TcCfg {
     static constexpr int D = D_, RM = 64, TP = kKvTile;
     static constexpr int RB = D * (I8 ? 1 : 2);           // bytes of a cached row
     static constexpr int OPER = TP * D * 2;               // a binary16 operand tile
-    static constexpr int NSF = I8 ? 3 : (D == 128 ? 4 : 6);  // operand stages (K and V)
+    static constexpr int NK = I8 ? 2 : (D == 128 ? 4 : 8);  // key operands
+    static constexpr int NV = NK + 1;                     // value operands: held longer
     static constexpr int RAW = TP * RB;
-    static constexpr int NSR = I8 ? (D == 128 ? 2 : 4) : 0;   // raw stages
-    static constexpr int NSC = 8;                         // scale slots (see the producer)
+    static constexpr int NSR = I8 ? (D == 128 ? 4 : 8) : 0;  // raw stages
+    static constexpr int NSC = D == 128 ? 8 : 16;         // scale slots (see the producer)
     static constexpr int QB = 128 * D * 2;
-    static constexpr int LDO = D + 4;                     // padded row of the output buffer
-    static constexpr int WARPS = 8 + (I8 ? 4 : 0) + 2, THREADS = 32 * WARPS;
+    static constexpr int WARPS = 8 + (I8 ? 4 : 0) + 4, THREADS = 32 * WARPS;
     static constexpr int SOFT = 256;                      // softmax threads
-    static constexpr int OFF_OP = QB;
-    static constexpr int OFF_RAW = OFF_OP + NSF * 2 * OPER;
-    static constexpr int OFF_SO = OFF_RAW + NSR * 2 * RAW;
-    static constexpr int OFF_SC = OFF_SO + RM * LDO * 4;
+    static constexpr int OFF_OP = 2 * QB;
+    static constexpr int OFF_V = OFF_OP + NK * OPER;
+    static constexpr int OFF_RAW = OFF_V + NV * OPER;
+    static constexpr int OFF_SC = OFF_RAW + NSR * 2 * RAW;
+    static_assert(kMergePieces * RM * 4 <= 2 * QB, "the merge's weights fit them");
     static constexpr size_t SMEM = 1024 + OFF_SC + (I8 ? NSC * 2 * TP * 4 : 0);
     // tensor-memory columns
-    static constexpr int T_S = 0, T_O = 128, T_P = 384, T_COLS = 512;
+    static constexpr int NS = 4, T_S = 0, T_O = 64 * NS, T_COLS = 512;
+    static_assert(TP == 64 && T_O + 2 * 128 <= T_COLS, "score buffers, two outputs");
 };
 
 struct SoftSync {
@@ -180,25 +184,29 @@ template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     k_kv_tc(const KvAttnArgs a, const __grid_constant__ KvMaps maps)
 {
-    constexpr int D = C::D, RM = C::RM, TP = C::TP, NSF = C::NSF;
+    constexpr int D = C::D, RM = C::RM, TP = C::TP, NK = C::NK, NV = C::NV;
     constexpr bool I8 = C::I8;
     extern __shared__ unsigned char smem_raw[];
     __shared__ SchedSmem sm;
-    __shared__ float s_m[2][RM], s_l[2][RM], u_m[RM], u_l[RM], s_inv[RM];
-    __shared__ float wgt[kMergePieces][RM];
+    __shared__ float s_m[2][RM], s_l[2][RM], u_m[RM], u_l[RM];
+    // what the query warp prepares, for two units: beside the operand
+    __shared__ float s_inv[2][RM];
+    __shared__ unsigned long long s_bits[2][RM];
+    __shared__ Unit s_unit[2];
+    __shared__ int s_tile0[2], s_n[2];  // first tile; tiles (0: the run is over)
     __shared__ unsigned s_bad[2][2];  // binary16 edge tiles: positions not finite
     __shared__ __align__(8) uint64_t b_raw_full[I8 ? C::NSR : 1], b_raw_empty[I8 ? C::NSR : 1],
-        b_sc_full[C::NSC], b_kv_full[NSF], b_kv_empty[NSF], b_s_full[2], b_p_full[2],
-        b_pv_done[2], b_q_full, b_end;
+        b_sc_full[C::NSC], b_k_full[NK], b_k_empty[NK], b_v_full[NV], b_v_empty[NV], b_s_full[C::NS],
+        b_p_full[C::NS], b_pv_done[2], b_s_free[C::NS], b_q_full[2], b_q_free[2], b_end[2];
     __shared__ unsigned s_tmem;
     unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const unsigned sbase = smem_addr(smem);
-    float *so = reinterpret_cast<float *>(smem + C::OFF_SO);
     float *scales = reinterpret_cast<float *>(smem + C::OFF_SC);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int W_MMA = C::WARPS - 1, W_LOAD = C::WARPS - 2;
+    constexpr int W_PV = C::WARPS - 1, W_QK = C::WARPS - 2, W_LOAD = C::WARPS - 3,
+                  W_Q = C::WARPS - 4;
 
-    if (warp == W_MMA) {
+    if (warp == W_PV) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_addr(&s_tmem)),
                      "r"(C::T_COLS)
@@ -212,17 +220,26 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         for (int i = 0; i < C::NSC; ++i)
             bar_init(smem_addr(&b_sc_full[i]), 32);
-        for (int i = 0; i < NSF; ++i) {
-            bar_init(smem_addr(&b_kv_full[i]), I8 ? 4 : 1);
-            bar_init(smem_addr(&b_kv_empty[i]), 1);
+        for (int i = 0; i < NV; ++i) {
+            if (i < NK) {
+                bar_init(smem_addr(&b_k_full[i]), I8 ? 4 : 1);
+                bar_init(smem_addr(&b_k_empty[i]), 1);
+            }
+            bar_init(smem_addr(&b_v_full[i]), I8 ? 4 : 1);
+            bar_init(smem_addr(&b_v_empty[i]), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::NS; ++i) {
             bar_init(smem_addr(&b_s_full[i]), 1);
             bar_init(smem_addr(&b_p_full[i]), 4);
-            bar_init(smem_addr(&b_pv_done[i]), 1);
+            bar_init(smem_addr(&b_s_free[i]), 1);
+            if (i < 2) {
+                bar_init(smem_addr(&b_pv_done[i]), 1);
+                bar_init(smem_addr(&b_q_full[i]), 1);
+                bar_init(smem_addr(&b_q_free[i]), 8);
+            }
         }
-        bar_init(smem_addr(&b_q_full), 8);
-        bar_init(smem_addr(&b_end), 1);
+        bar_init(smem_addr(&b_end[0]), 1);
+        bar_init(smem_addr(&b_end[1]), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tc_fence_before();
@@ -233,12 +250,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
     if (warp == W_LOAD) {
         // ---- copies.  A scale slot is reused 8 tiles later: by then the raw
-        // (NSR) and operand (NSF) rings between have only let the copies this
-        // far because the slot's tile has left the softmax.
-        constexpr int NS = I8 ? C::NSR : NSF, BYTES = I8 ? C::RAW : C::OPER;
-        static_assert(!I8 || C::NSR + NSF + 1 <= C::NSC, "scale slots");
-        const unsigned ring = sbase + (I8 ? C::OFF_RAW : C::OFF_OP);
+        // (NSR) and value (NV) rings between have only let the copies this far
+        // because the slot's tile has left the softmax.
+        static_assert(!I8 || C::NSR + NV <= C::NSC, "scale slots");
         int i = 0;  // tile of the run
+        auto boxes = [&](unsigned dst, const CUtensorMap *map, int p, int bh, unsigned bar) {
+#pragma unroll
+            for (int xb = 0; xb < C::RB; xb += 128)
+                tma_load(dst + xb * TP, map, xb, p, bh, bar);
+        };
         for (long long w = run.lo; w < run.hi;) {
             const Unit x = sched_unit<false>(a, RM, sm, run, w);
             const long long wend = min(run.hi, x.w1);
@@ -248,15 +268,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             const int bh = unit_bh<false>(a, x);
             for (w = tile_place(x, w); w < wend; ++w, ++i) {
-                const int slot = i % NS, p = tile_of(x, w) * TP;
-                const unsigned full = smem_addr(I8 ? &b_raw_full[slot % (I8 ? C::NSR : 1)]
-                                                   : &b_kv_full[slot % NSF]);
-                const unsigned empty = smem_addr(I8 ? &b_raw_empty[slot % (I8 ? C::NSR : 1)]
-                                                    : &b_kv_empty[slot % NSF]);
-                if (i >= NS)
-                    wait(empty, (i / NS - 1) & 1);
-                if (I8) {
-                    const int sc = i % C::NSC;
+                const int p = tile_of(x, w) * TP;
+                if constexpr (I8) {
+                    const int slot = i % C::NSR, sc = i % C::NSC;
+                    if (i >= C::NSR)
+                        wait(smem_addr(&b_raw_empty[slot]), (i / C::NSR - 1) & 1);
                     const unsigned dst = sbase + C::OFF_SC + sc * 2 * TP * 4;
 #pragma unroll
                     for (int k = 0; k < 2 * TP; k += 32) {
@@ -268,87 +284,215 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                                      smem_addr(&b_sc_full[sc]))
                                  : "memory");
-                }
-                if (lane == 0) {
-                    bar_expect(full, 2 * BYTES);
-                    const unsigned dst = ring + slot * 2 * BYTES;
-#pragma unroll
-                    for (int xb = 0; xb < C::RB; xb += 128) {
-                        tma_load(dst + xb * TP, &maps.k, xb, p, bh, full);
-                        tma_load(dst + BYTES + xb * TP, &maps.v, xb, p, bh, full);
+                    if (lane == 0) {
+                        const unsigned full = smem_addr(&b_raw_full[slot]);
+                        const unsigned raw = sbase + C::OFF_RAW + slot * 2 * C::RAW;
+                        bar_expect(full, 2 * C::RAW);
+                        boxes(raw, &maps.k, p, bh, full);
+                        boxes(raw + C::RAW, &maps.v, p, bh, full);
+                    }
+                } else {
+                    const int sk = i % NK, sv = i % NV;
+                    if (i >= NK)
+                        wait(smem_addr(&b_k_empty[sk]), (i / NK - 1) & 1);
+                    if (lane == 0) {
+                        const unsigned full = smem_addr(&b_k_full[sk]);
+                        bar_expect(full, C::OPER);
+                        boxes(sbase + C::OFF_OP + sk * C::OPER, &maps.k, p, bh, full);
+                    }
+                    __syncwarp();
+                    if (i >= NV)
+                        wait(smem_addr(&b_v_empty[sv]), (i / NV - 1) & 1);
+                    if (lane == 0) {
+                        const unsigned full = smem_addr(&b_v_full[sv]);
+                        bar_expect(full, C::OPER);
+                        boxes(sbase + C::OFF_V + sv * C::OPER, &maps.v, p, bh, full);
                     }
                 }
                 __syncwarp();
             }
         }
-        if (I8)
-            asm volatile("cp.async.wait_all;" ::: "memory");
         // no copy may outlive the CTA
-        for (int k = max(0, i - NS); k < i; ++k)
-            bar_wait(smem_addr(I8 ? &b_raw_full[k % (I8 ? C::NSR : 1)] : &b_kv_full[k % NSF]),
-                     (k / NS) & 1);
-    } else if (warp == W_MMA) {
-        // ---- products.  The warp runs the loop together, so that descriptors
-        // stay in uniform registers, and one thread issues (with the loop in
-        // one thread, building them took longer than the products).
-        constexpr uint32_t ID_S = tc_idesc(TP, false), ID_O = tc_idesc(D, true);
-        constexpr unsigned STAGE = 2 * C::OPER >> 4;
-        const uint64_t dq = tc_desc(sbase, 16), dk0 = tc_desc(sbase + C::OFF_OP, 16),
-                       dv0 = tc_desc(sbase + C::OFF_OP + C::OPER, TP * 128);
-        const bool one = elect_one();
-        int st = 0, kvp = 0, sv = 0, seg = 0, pp = 0;  // stages; phases
+        if constexpr (I8) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            for (int k = max(0, i - C::NSR); k < i; ++k)
+                bar_wait(smem_addr(&b_raw_full[k % C::NSR]), (k / C::NSR) & 1);
+        } else {
+            for (int k = max(0, i - NK); k < i; ++k)
+                bar_wait(smem_addr(&b_k_full[k % NK]), (k / NK) & 1);
+            for (int k = max(0, i - NV); k < i; ++k)
+                bar_wait(smem_addr(&b_v_full[k % NV]), (k / NV) & 1);
+        }
+    } else if (warp == W_Q) {
+        // ---- queries: each unit's, split and in place, a unit ahead
+        int k = 0;
+        auto take = [&](int buf) {  // buffer `buf` is free (unit k - 2 has left it)
+            if (k >= 2)
+                wait(smem_addr(&b_q_free[buf]), (k / 2 - 1) & 1);
+        };
         for (long long w = run.lo; w < run.hi;) {
             const Unit x = sched_unit<false>(a, RM, sm, run, w);
-            const long long wend = min(run.hi, x.w1);
-            int n = x.h < 0 ? 0 : (int)(wend - tile_place(x, w));
-            n = __shfl_sync(0xffffffffu, n, 0);
+            const long long wend = min(run.hi, x.w1), wb = tile_place(x, w);
             w = wend;
-            if (n == 0)
+            if (x.h < 0)
                 continue;
-            wait(smem_addr(&b_q_full), seg & 1);
-            ++seg;
-            for (int t = 0; t <= n; ++t) {
-                if (t < n) {
-                    wait(smem_addr(&b_kv_full[st]), kvp);
+            const int buf = k & 1;
+            take(buf);
+            // a row over D / 16 lanes, the next pass's rows on their way
+            constexpr int LPR = D / 16, RPP = 32 / LPR;
+            unsigned char *qs = smem + buf * C::QB;
+            const int part = lane % LPR;
+            float4 v[4], nx[4];
+            auto fetch = [&](int r0, float4 (&to)[4]) {
+                const int r = r0 + lane / LPR;
+                long long at[4];
+                const long long q0 = r < x.nrows ? q_at<false>(a, x, r) + part * 16 : -1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    at[i] = q0 < 0 ? -1 : q0 + 4 * i;
+                ld_queries(a.q, at, to);
+            };
+            fetch(0, nx);
+#pragma unroll 1
+            for (int r0 = 0; r0 < RM; r0 += RPP) {
+                const int r = r0 + lane / LPR;
+                float mx = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = nx[i];
+                    mul2(v[i].x, v[i].y, a.scale, a.scale);
+                    mul2(v[i].z, v[i].w, a.scale, a.scale);
+                    mx = amax3(amax3(mx, v[i].x, v[i].y), v[i].z, v[i].w);
+                }
+                if (r0 + RPP < RM)
+                    fetch(r0 + RPP, nx);
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1)
+                    mx = amax2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                float inv;
+                const float al = query_power(mx, &inv);
+                unsigned hi[8], lo[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mul2(v[i].x, v[i].y, al, al);
+                    mul2(v[i].z, v[i].w, al, al);
+                    hi[2 * i] = h2(v[i].x, v[i].y);
+                    hi[2 * i + 1] = h2(v[i].z, v[i].w);
+                    lo[2 * i] = h2_rest(v[i].x, v[i].y, hi[2 * i]);
+                    lo[2 * i + 1] = h2_rest(v[i].z, v[i].w, hi[2 * i + 1]);
+                }
+                // 64 dimensions a region of 128 rows; a row's low parts 16 rows on, at
+                // the same place in the swizzle
+                const int row = 32 * (r >> 4) + (r & 15), c = 2 * (part & 3);
+                unsigned char *p = qs + (part >> 2) * (128 * 128) + row * 128;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    unsigned char *q = p + (((c + k) ^ (row & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(q) =
+                        make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+                    *reinterpret_cast<uint4 *>(q + 16 * 128) =
+                        make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                }
+                if (part == 0)
+                    s_inv[buf][r] = inv;
+            }
+            for (int r = lane; r < RM; r += 32)
+                s_bits[buf][r] =
+                    r < x.nrows ? seen_bits(a, x, row_token(a, x.row0 + r)) : 0ull;
+            if (lane == 0) {
+                s_unit[buf] = x;
+                s_tile0[buf] = tile_of(x, wb);
+                s_n[buf] = (int)(wend - wb);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(smem_addr(&b_q_full[buf]));
+            ++k;
+        }
+        take(k & 1);
+        if (lane == 0) {
+            s_n[k & 1] = 0;
+            bar_arrive(smem_addr(&b_q_full[k & 1]));
+        }
+    } else if (warp == W_QK || warp == W_PV) {
+        // ---- products, the scores' and the values' each by a warp.  The warp
+        // runs its loop together, so that descriptors stay in uniform
+        // registers, and one thread issues (with the loop in one thread,
+        // building them took longer than the products).
+        constexpr uint32_t ID_S = tc_idesc(TP, false), ID_O = tc_idesc(D, true);
+        constexpr unsigned STAGE = C::OPER >> 4;
+        const uint64_t dq = tc_desc(sbase, 16), dk0 = tc_desc(sbase + C::OFF_OP, 16),
+                       dv0 = tc_desc(sbase + C::OFF_V, TP * 128);
+        const bool one = elect_one(), scores = warp == W_QK;
+        int st = 0, stp = 0, sb = 0, sbp = 0;  // operand stage, score buffer; their phases
+        bool used = false;                     // every score buffer has been used
+        for (int k = 0;; ++k) {
+            wait(smem_addr(&b_q_full[k & 1]), (k >> 1) & 1);
+            const int n = wait.dead ? 0 : __shfl_sync(0xffffffffu, s_n[k & 1], 0);
+            if (n == 0)
+                break;
+            if (scores) {
+                const uint64_t da = dq + (uint64_t)(unsigned)(k & 1) * (C::QB >> 4);
+                for (int t = 0; t < n; ++t) {
+                    if (used)  // the weights that took the buffer's scores' place are read
+                        wait(smem_addr(&b_s_free[sb]), sbp ^ 1);
+                    wait(smem_addr(&b_k_full[st]), stp);
                     tc_fence_after();
                     const uint64_t dk = dk0 + (uint64_t)(unsigned)st * STAGE;
                     if (one) {
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
-                            tc_mma_ss(tmem + C::T_S + (t & 1) * 64,
-                                      dq + (kk / 4) * (128 * 128 >> 4) + (kk % 4) * 2,
+                            tc_mma_ss(tmem + C::T_S + sb * 64,
+                                      da + (kk / 4) * (128 * 128 >> 4) + (kk % 4) * 2,
                                       dk + (kk / 4) * (TP * 128 >> 4) + (kk % 4) * 2, ID_S, kk > 0);
-                        tc_commit(smem_addr(&b_s_full[t & 1]));
+                        tc_commit(smem_addr(&b_s_full[sb]));
+                        tc_commit(smem_addr(&b_k_empty[st]));
                     }
                     __syncwarp();
-                    if (++st == NSF) {
+                    if (++sb == C::NS) {
+                        sb = 0;
+                        sbp ^= 1;
+                        used = true;
+                    }
+                    if (++st == NK) {
                         st = 0;
-                        kvp ^= 1;
+                        stp ^= 1;
                     }
                 }
-                if (t > 0) {
-                    const int g = (t - 1) & 1;
-                    wait(smem_addr(&b_p_full[g]), (pp >> g) & 1);
-                    pp ^= 1 << g;
+            } else {
+                for (int t = 0; t < n; ++t) {
+                    const int g = t & 1;
+                    wait(smem_addr(&b_v_full[st]), stp);
+                    wait(smem_addr(&b_p_full[sb]), sbp);
                     tc_fence_after();
-                    const uint64_t dv = dv0 + (uint64_t)(unsigned)sv * STAGE;
+                    const uint64_t dv = dv0 + (uint64_t)(unsigned)st * STAGE;
                     if (one) {
 #pragma unroll
                         for (int kk = 0; kk < TP / 16; ++kk)
-                            tc_mma_ts(tmem + C::T_O + g * 128, tmem + C::T_P + g * 32 + kk * 8,
-                                      dv + kk * (16 * 128 >> 4), ID_O, t > 2 || kk > 0);
+                            tc_mma_ts(tmem + C::T_O + g * 128, tmem + C::T_S + sb * 64 + kk * 8,
+                                      dv + kk * (16 * 128 >> 4), ID_O, t > 1 || kk > 0);
                         tc_commit(smem_addr(&b_pv_done[g]));
-                        tc_commit(smem_addr(&b_kv_empty[sv]));
+                        tc_commit(smem_addr(&b_v_empty[st]));
+                        tc_commit(smem_addr(&b_s_free[sb]));
                     }
                     __syncwarp();
-                    sv = sv + 1 == NSF ? 0 : sv + 1;
+                    if (++sb == C::NS) {
+                        sb = 0;
+                        sbp ^= 1;
+                    }
+                    if (++st == NV) {
+                        st = 0;
+                        stp ^= 1;
+                    }
                 }
             }
         }
+        // every product is done before tensor memory goes
         if (one)
-            tc_commit(smem_addr(&b_end));  // every product is done before tensor memory goes
+            tc_commit(smem_addr(&b_end[scores]));
         __syncwarp();
-        bar_wait(smem_addr(&b_end), 0);
+        bar_wait(smem_addr(&b_end[scores]), 0);
     } else if (I8 && warp >= 8 && warp < 12) {
         // ---- codes to binary16
         // A thread keeps its 16-byte chunk c and its row modulo 16 (32).  Eight
@@ -368,21 +512,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const int n = x.h < 0 ? 0 : (int)(wend - tile_place(x, w));
             w = wend;
             for (int t = 0; t < n; ++t, ++i) {
-                const int rs = i % (I8 ? C::NSR : 1), fs = i % NSF;
+                const int rs = i % (I8 ? C::NSR : 1);
                 wait(smem_addr(&b_raw_full[rs]), (i / (I8 ? C::NSR : 1)) & 1);
-                if (i >= NSF)
-                    wait(smem_addr(&b_kv_empty[fs]), (i / NSF - 1) & 1);
-                const unsigned src = sbase + C::OFF_RAW + rs * 2 * C::RAW + src0;
-                const unsigned dst = sbase + C::OFF_OP + fs * 2 * C::OPER;
                 constexpr int STEP = 128 / CPR;  // rows a pass
 #pragma unroll 1
-                for (int side = 0; side < 2; ++side)
+                for (int side = 0; side < 2; ++side) {
+                    const int ns = side ? NV : NK, fs = i % ns;
+                    if (i >= ns)
+                        wait(smem_addr(side ? &b_v_empty[fs] : &b_k_empty[fs]), (i / ns - 1) & 1);
+                    const unsigned src =
+                        sbase + C::OFF_RAW + rs * 2 * C::RAW + side * C::RAW + src0;
+                    const unsigned dst = sbase + (side ? C::OFF_V : C::OFF_OP) + fs * C::OPER;
 #pragma unroll
                     for (int off = 0; off < TP; off += STEP) {
-                        const uint4 u = lds16(src + side * C::RAW + off * C::RB);
+                        const uint4 u = lds16(src + off * C::RB);
                         const unsigned b0 = u.x ^ 0x80808080u, b1 = u.y ^ 0x80808080u,
                                        b2 = u.z ^ 0x80808080u, b3 = u.w ^ 0x80808080u;
-                        const unsigned at = dst + side * C::OPER + off * 128;
+                        const unsigned at = dst + off * 128;
                         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + dst0),
                                      "r"(codes_lo(b0)), "r"(codes_hi(b0)), "r"(codes_lo(b1)),
                                      "r"(codes_hi(b1))
@@ -392,73 +538,47 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                      "r"(codes_hi(b3))
                                      : "memory");
                     }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    bar_arrive(smem_addr(&b_kv_full[fs]));
-                    bar_arrive(smem_addr(&b_raw_empty[rs]));
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        bar_arrive(smem_addr(side ? &b_v_full[fs] : &b_k_full[fs]));
                 }
+                if (lane == 0)
+                    bar_arrive(smem_addr(&b_raw_empty[rs]));
             }
         }
     } else if (warp < 8) {
         // ---- softmax
         const int wg = warp >> 2, ww = warp & 3, g = lane >> 2, t4 = lane & 3;
         const unsigned lanes = (unsigned)(32 * ww) << 16, low = 16u << 16;
-        const unsigned tS = tmem + lanes + C::T_S + wg * 64, tO = tmem + lanes + C::T_O + wg * 128,
-                       tP = tmem + lanes + C::T_P + wg * 32;
+        const unsigned tO = tmem + lanes + C::T_O + wg * 128;
         Finish<false, RM, C::SOFT, SoftSync> fin;
         int i0 = 0, nt = 0;  // tile of the run; this group's tiles so far
-        for (long long w = run.lo; w < run.hi;) {
-            const Unit x = sched_unit<false>(a, RM, sm, run, w);
-            const long long wend = min(run.hi, x.w1), wb = tile_place(x, w);
-            w = wend;
-            if (x.h < 0)
-                continue;
-            const int n = (int)(wend - wb), tile0 = tile_of(x, wb);
-            // the queries' parts (8 rows a warp)
-            float4 qv[RM / 8];
-#pragma unroll
-            for (int k = 0; k < RM / 8; ++k) {
-                const int r = warp + 8 * k;
-                qv[k] = r < x.nrows && lane * 4 < D
-                            ? ld_row4(a.q, q_at<false>(a, x, r) + lane * 4)
-                            : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-#pragma unroll
-            for (int k = 0; k < RM / 8; ++k) {
-                const int r = warp + 8 * k;
-                float inv;
-                const SplitQ q = split_row(qv[k], a.scale, &inv);
-                if (lane * 4 < D) {
-                    const int row = 32 * (r >> 4) + (r & 15), d = lane * 4;
-                    unsigned char *p = smem + (d >> 6) * (128 * 128) + row * 128 +
-                                       ((((d & 63) >> 3) ^ (row & 7)) << 4) + (d & 4) * 2;
-                    *reinterpret_cast<uint2 *>(p) = make_uint2(q.hi01, q.hi23);
-                    // (16 rows on: the same place in the swizzle)
-                    *reinterpret_cast<uint2 *>(p + 16 * 128) = make_uint2(q.lo01, q.lo23);
-                }
-                if (lane == 0)
-                    s_inv[r] = inv;
-            }
-            fence_async_smem();
-            SoftSync::sync();
-            if (lane == 0)
-                bar_arrive(smem_addr(&b_q_full));
+        for (int k = 0;; ++k) {
+            const int buf = k & 1;
+            wait(smem_addr(&b_q_full[buf]), (k >> 1) & 1);
+            const int n = wait.dead ? 0 : s_n[buf], tile0 = s_tile0[buf];
+            if (n == 0)
+                break;
+            const int len = s_unit[buf].len;
             float inv[2], m[2], l[2];
             unsigned long long bits[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int row = 16 * ww + g + 8 * r;
-                inv[r] = s_inv[row];
-                bits[r] = row < x.nrows ? seen_bits(a, x, row_token(a, x.row0 + row)) : 0ull;
+                inv[r] = s_inv[buf][row];
+                bits[r] = s_bits[buf][row];
                 m[r] = -INFINITY;
                 l[r] = 0.f;
             }
 
             for (int t = wg; t < n; t += 2, ++nt) {
                 const int p0 = (tile0 + t) * TP;
-                const bool edge = p0 + TP > x.len;
-                wait(smem_addr(&b_s_full[wg]), nt & 1);
+                const bool edge = p0 + TP > len;
+                // (weights overwrite their own scores)
+                const int sb = (i0 + t) % C::NS;
+                const unsigned tS = tmem + lanes + C::T_S + sb * 64;
+                wait(smem_addr(&b_s_full[sb]), ((i0 + t) / C::NS) & 1);
                 tc_fence_after();
                 const float *sc = scales + ((i0 + t) % C::NSC) * 2 * TP + 2 * t4;
                 if (I8)
@@ -467,7 +587,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (edge) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const int q = p0 + 8 * (e >> 1) + 2 * t4 + (e & 1) - x.len;
+                        const int q = p0 + 8 * (e >> 1) + 2 * t4 + (e & 1) - len;
 #pragma unroll
                         for (int r = 0; r < 2; ++r)
                             if (!(q < 0 || (q < 64 && ((bits[r] >> q) & 1))))
@@ -476,12 +596,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if (!I8) {
                         // a NaN or an infinity among the values must not reach rows
                         // that do not see it: taken out of the operand here
-                        const int st = (i0 + t) % NSF;
-                        wait(smem_addr(&b_kv_full[st]), ((i0 + t) / NSF) & 1);
+                        const int st = (i0 + t) % NV;
+                        wait(smem_addr(&b_v_full[st]), ((i0 + t) / NV) & 1);
                         if (ww == 0 && lane < 2)
                             s_bad[wg][lane] = 0u;
                         asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
-                        unsigned char *vb = smem + C::OFF_OP + st * 2 * C::OPER + C::OPER;
+                        unsigned char *vb = smem + C::OFF_V + st * C::OPER;
                         for (int k = tid & 127; k < C::OPER / 16; k += 128) {
                             uint4 *q = reinterpret_cast<uint4 *>(vb) + k;
                             const uint4 u = *q;
@@ -615,13 +735,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 l[r] = __int_as_float(0x7fc00000);  // its result is NaN
                         }
                 }
-                // the group's product before this one is done: weights and output are free
-                if (t >= 2)
-                    wait(smem_addr(&b_pv_done[wg]), (nt - 1) & 1);
-                tc_fence_after();
-                tm_st_pairs(tP, ph);
-                tm_st_pairs(tP + low, pl);
+                tm_st_pairs(tS, ph);
+                tm_st_pairs(tS + low, pl);
                 if (t >= 2 && moved) {
+                    wait(smem_addr(&b_pv_done[wg]), (nt - 1) & 1);  // the output is at rest
+                    tc_fence_after();
 #pragma unroll
                     for (int half = 0; half < 2; ++half)
 #pragma unroll
@@ -640,7 +758,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    bar_arrive(smem_addr(&b_p_full[wg]));
+                    bar_arrive(smem_addr(&b_p_full[sb]));
             }
             i0 += n;
 
@@ -659,54 +777,94 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
             }
             SoftSync::sync();
-            float fac[2];
+            // Each group finishes one half of the columns (64 of them; the first
+            // group all where there are no more): the other group's half goes
+            // through the unit's query operand, whose products are all done.
+            const Unit x = s_unit[buf];
+            const bool all = fin.whole(run, x);
+            float *rec = fin.record(a, run, x);
+            float fac[2], lsum[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int row = 16 * ww + g + 8 * r;
                 const float M = fmaxf(s_m[0][row], s_m[1][row]), ms = M == -INFINITY ? 0.f : M;
                 fac[r] = ex2(m[r] - ms);
-                if (wg == 0 && t4 == 0) {
-                    u_m[row] = M;
-                    u_l[row] = s_l[0][row] * ex2(s_m[0][row] - ms) +
-                               s_l[1][row] * ex2(s_m[1][row] - ms);
+                lsum[r] = s_l[0][row] * ex2(s_m[0][row] - ms) + s_l[1][row] * ex2(s_m[1][row] - ms);
+                if (wg == 0 && t4 == 0 && !all && row < x.nrows) {
+                    __stcg(rec + RM * D + row, M);
+                    __stcg(rec + RM * D + RM + row, lsum[r]);
                 }
             }
-            for (int k = 0; k < 2; ++k) {
-                if (k == wg && (have || k == 0)) {
+            float2 *const xq = reinterpret_cast<float2 *>(smem + buf * C::QB) + ww * 16 * 32 + lane;
+            auto load_o = [&](int cb, float (&o)[32]) {
+                float lo[32];
+                tm_ld64(tO + cb, o);
+                tm_ld64(tO + low + cb, lo);
+                tm_wait_ld(o);
+                tm_wait_ld(lo);
 #pragma unroll
-                    for (int cb = 0; cb < D; cb += 64) {
-                        float o[32], ol[32];
-                        tm_ld64(tO + cb, o);
-                        tm_ld64(tO + low + cb, ol);
-                        tm_wait_ld(o);
-                        tm_wait_ld(ol);
+                for (int e = 0; e < 32; ++e)
+                    o[e] = (o[e] + lo[e]) * fac[(e >> 1) & 1];
+            };
+            constexpr int HB = C::RM * 64 / 2;  // float2 places of a half
+            const int mine = D == 128 ? wg : 0, other = mine ^ 1;
+            float o[32];
+            if (have && (D == 128 || wg == 1)) {
+                load_o(D == 128 ? other * 64 : 0, o);
+                float2 *q = xq + (D == 128 ? other * HB : 0);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
+                for (int e = 0; e < 16; ++e)
+                    q[e * 32] = make_float2(o[2 * e], o[2 * e + 1]);
+            }
+            if (have && (D == 128 || wg == 0))
+                load_o(mine * 64, o);
+            tc_fence_before();
+            SoftSync::sync();
+            if (D == 128 || wg == 0) {
+                if (!have) {
 #pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                float2 *q = reinterpret_cast<float2 *>(
-                                    so + (16 * ww + g + 8 * r) * C::LDO + cb + 8 * j + 2 * t4);
-                                const int e = 4 * j + 2 * r;
-                                float2 val = make_float2((o[e] + ol[e]) * fac[r],
-                                                         (o[e + 1] + ol[e + 1]) * fac[r]);
-                                if (k) {
-                                    const float2 was = *q;
-                                    val = make_float2(was.x + val.x, was.y + val.y);
-                                }
-                                *q = val;
-                            }
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = 0.f;
+                }
+                if (wg == 1 || n > 1) {  // the other group took a tile
+                    const float2 *q = xq + mine * HB;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 v = q[e * 32];
+                        o[2 * e] += v.x;
+                        o[2 * e + 1] += v.y;
                     }
-                    tc_fence_before();
                 }
-                SoftSync::sync();
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int row = 16 * ww + g + 8 * r;
+                    if (row >= x.nrows)
+                        continue;
+                    const float rl = lsum[r] == 0.f ? 0.f : __frcp_rn(lsum[r]);
+                    float *dst = (all ? a.out + out_at<false>(a, x, row) : rec + row * D) +
+                                 mine * 64 + 2 * t4;
+                    const float f = all ? rl : 1.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 v =
+                            make_float2(o[4 * j + 2 * r] * f, o[4 * j + 2 * r + 1] * f);
+                        if (all)
+                            *reinterpret_cast<float2 *>(dst + 8 * j) = v;
+                        else
+                            __stcg(reinterpret_cast<float2 *>(dst + 8 * j), v);
+                    }
+                }
             }
-            fin.part(a, run, x, [&](int row, int d) { return so[row * C::LDO + d]; }, u_m, u_l);
+            fin.done(a, run, x);
+            if (lane == 0)
+                bar_arrive(smem_addr(&b_q_free[buf]));
         }
-        fin.end(a, run, sm, u_m, u_l, wgt);
+        // (the query operands are at rest)
+        fin.end(a, run, sm, u_m, u_l, reinterpret_cast<float(*)[RM]>(smem));
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == W_MMA) {
+    if (warp == W_PV) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(C::T_COLS)

@@ -45,6 +45,20 @@ DV_DEV bool bar_wait(unsigned bar, unsigned parity)
     return false;
 }
 
+// Whether it is complete now.
+DV_DEV bool bar_test(unsigned bar, unsigned parity)
+{
+    unsigned ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Box at (byte x of the rows, position, (row, head)) of a cache side.
 DV_DEV void tma_load(unsigned dst, const CUtensorMap *map, int x, int pos, int bh, unsigned bar)
 {
@@ -164,6 +178,14 @@ DV_DEV float ref_shift(bool first, float big)
 // and low parts {hi01, hi23}, {lo01, lo23} after a power of two takes the
 // row's largest element into [2^13, 2^14); *inv undoes it.  The lanes of a
 // warp hold the row (v: zeros past its end).
+DV_DEV float query_power(float mx, float *inv)
+{
+    // (mx's exponent field; none for a row that is zero or not finite)
+    const int field = (int)(__float_as_uint(mx) >> 23);
+    const int e = field == 255 || mx == 0.f ? 0 : min(140 - field, 100);
+    *inv = __int_as_float((127 - e) << 23);
+    return __int_as_float((127 + e) << 23);
+}
 struct SplitQ {
     unsigned hi01, hi23, lo01, lo23;
 };
@@ -174,17 +196,42 @@ DV_DEV SplitQ split_row(float4 v, float scale, float *inv)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         mx = amax2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    // (its exponent field; none for a row that is zero or not finite)
-    const int field = (int)(__float_as_uint(mx) >> 23);
-    const int e = field == 255 || mx == 0.f ? 0 : min(140 - field, 100);
-    const float al = __int_as_float((127 + e) << 23);
-    *inv = __int_as_float((127 - e) << 23);
+    const float al = query_power(mx, inv);
     SplitQ q;
     q.hi01 = h2(v.x * al, v.y * al);
     q.hi23 = h2(v.z * al, v.w * al);
     q.lo01 = h2_rest(v.x * al, v.y * al, q.hi01);
     q.lo23 = h2_rest(v.z * al, v.w * al, q.hi23);
     return q;
+}
+
+// Four values at each of N query rows, zeros where at < 0; the loads go out
+// together (one branch on the type around them all, not one each).
+template <int N>
+DV_DEV void ld_queries(const KvRowsArgs &q, const long long (&at)[N], float4 (&v)[N])
+{
+    if (q.f16) {
+        uint2 u[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            u[i] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __half *>(q.p) +
+                                                         (at[i] < 0 ? 0 : at[i])));
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u[i].x));
+            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&u[i].y));
+            v[i] = make_float4(a.x, a.y, b.x, b.y);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(q.p) +
+                                                          (at[i] < 0 ? 0 : at[i])));
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (at[i] < 0)
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 template <bool BLOCK>
