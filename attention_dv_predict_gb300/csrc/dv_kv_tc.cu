@@ -11,11 +11,13 @@
 // 32 rows at the 175B shape; see the launch rule for this kernel's time).
 //
 // Warps of a CTA (one CTA per SM):
-//   0-3, 4-7  two softmax groups that take turns at the tiles, each with its
+//   0-15      softmax: two streams that take turns at the tiles, each with its
 //             own output columns in tensor memory; they are merged when a unit
-//             ends, so neither waits for the other.  Four score buffers, whose
-//             weights take the scores' place, let scores run three tiles ahead
-//   8-11      8-bit caches: codes to binary16, raw ring -> operand ring
+//             ends, so neither waits for the other.  Eight warps of a stream
+//             take half of a tile's columns each four: a warp's own latency
+//             bounds it.  Four score buffers, whose weights take the scores'
+//             place, let scores run ahead
+//   16-19     8-bit caches: codes to binary16, raw ring -> operand ring
 //   last four one that prepares a unit's queries while the unit before runs,
 //             one of tensor-map copies (and scales by cp.async), one whose
 //             elected thread issues the scores' MMAs, one the values'
@@ -43,8 +45,8 @@ struct TcCfg {
     static constexpr int NSR = I8 ? (D == 128 ? 4 : 8) : 0;  // raw stages
     static constexpr int NSC = D == 128 ? 8 : 16;         // scale slots (see the producer)
     static constexpr int QB = 128 * D * 2;
-    static constexpr int WARPS = 8 + (I8 ? 4 : 0) + 4, THREADS = 32 * WARPS;
-    static constexpr int SOFT = 256;                      // softmax threads
+    static constexpr int WARPS = 16 + (I8 ? 4 : 0) + 4, THREADS = 32 * WARPS;
+    static constexpr int SOFT = 512;                      // softmax threads
     static constexpr int OFF_OP = 2 * QB;
     static constexpr int OFF_V = OFF_OP + NK * OPER;
     static constexpr int OFF_RAW = OFF_V + NV * OPER;
@@ -57,7 +59,7 @@ struct TcCfg {
 };
 
 struct SoftSync {
-    DV_DEV static void sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+    DV_DEV static void sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
 };
 
 DV_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -100,63 +102,80 @@ DV_DEV void tc_commit(unsigned bar)
         : "memory");
 }
 
-// 16 lanes x 64 columns: thread (g, t) = (lane / 4, lane % 4) holds columns 8 j
+// 16 lanes x 2 N columns: thread (g, t) = (lane / 4, lane % 4) holds columns 8 j
 // + 2 t, + 1 of lanes g (v[4 j], v[4 j + 1]) and g + 8 (v[4 j + 2], v[4 j + 3]).
-DV_DEV void tm_ld64(unsigned addr, float (&v)[32])
+template <int N>
+DV_DEV void tm_ld(unsigned addr, float (&v)[N])
 {
-    unsigned r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
-        "%29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr));
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        v[i] = __uint_as_float(r[i]);
+    static_assert(N == 16 || N == 8, "32 or 16 columns");
+    if constexpr (N == 0)
+        ;
+    else if constexpr (N == 16)
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+                     : "r"(addr));
+    else if constexpr (N == 8)
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                     : "r"(addr));
+}
+template <int N>
+DV_DEV void tm_st(unsigned addr, const float (&v)[N])
+{
+    if constexpr (N == 0)
+        ;
+    else if constexpr (N == 16)
+        asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+                     "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+                     : "memory");
+    else if constexpr (N == 8)
+        asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+                     "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                     : "memory");
 }
 // The loads into v have landed (v passes through, so that no use moves before it).
-DV_DEV void tm_wait_ld(float (&v)[32])
+template <int N>
+DV_DEV void tm_wait_ld(float (&v)[N])
 {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
-                 :
-                 : "memory");
+    if constexpr (N == 0)
+        ;
+    else if constexpr (N == 16)
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+                     :
+                     : "memory");
+    else if constexpr (N == 8)
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7])
+                     :
+                     : "memory");
 }
 DV_DEV void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-DV_DEV void tm_st64(unsigned addr, const float (&v)[32])
-{
-    unsigned r[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        r[i] = __float_as_uint(v[i]);
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
-        "%29, %30, %31, %32};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-        "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-// 16 lanes x 32 columns of binary16 pairs: r[2 j] columns 4 j + t of lane g,
+// 16 lanes x 16 columns of binary16 pairs: r[2 j] columns 4 j + t of lane g,
 // r[2 j + 1] of lane g + 8.
-DV_DEV void tm_st_pairs(unsigned addr, const unsigned (&r)[16])
+DV_DEV void tm_st_pairs(unsigned addr, const unsigned (&r)[8])
 {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15])
-        : "memory");
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                     addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7])
+                 : "memory");
 }
+
+// Whether any of N threads says so (a barrier among them).
+template <int N>
+DV_DEV bool any_of(int bar, bool v)
+{
+    unsigned r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"((unsigned)v), "r"(bar), "n"(N)
+        : "memory");
+    return r != 0;
+}
+DV_DEV bool stream_any(int stream, bool v) { return any_of<256>(2 + stream, v); }
 
 DV_DEV bool elect_one()
 {
@@ -188,12 +207,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     constexpr bool I8 = C::I8;
     extern __shared__ unsigned char smem_raw[];
     __shared__ SchedSmem sm;
-    __shared__ float s_m[2][RM], s_l[2][RM], u_m[RM], u_l[RM];
+    __shared__ float s_m[2][RM], s_l[4][RM], u_m[RM], u_l[RM];
     // what the query warp prepares, for two units: beside the operand
     __shared__ float s_inv[2][RM];
     __shared__ unsigned long long s_bits[2][RM];
     __shared__ Unit s_unit[2];
     __shared__ int s_tile0[2], s_n[2];  // first tile; tiles (0: the run is over)
+    __shared__ float s_max[2][2][RM];  // rare: a row's maximum over both halves
     __shared__ unsigned s_bad[2][2];  // binary16 edge tiles: positions not finite
     __shared__ __align__(8) uint64_t b_raw_full[I8 ? C::NSR : 1], b_raw_empty[I8 ? C::NSR : 1],
         b_sc_full[C::NSC], b_k_full[NK], b_k_empty[NK], b_v_full[NV], b_v_empty[NV], b_s_full[C::NS],
@@ -230,12 +250,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         for (int i = 0; i < C::NS; ++i) {
             bar_init(smem_addr(&b_s_full[i]), 1);
-            bar_init(smem_addr(&b_p_full[i]), 4);
+            bar_init(smem_addr(&b_p_full[i]), 8);
             bar_init(smem_addr(&b_s_free[i]), 1);
             if (i < 2) {
                 bar_init(smem_addr(&b_pv_done[i]), 1);
                 bar_init(smem_addr(&b_q_full[i]), 1);
-                bar_init(smem_addr(&b_q_free[i]), 8);
+                bar_init(smem_addr(&b_q_free[i]), 16);
             }
         }
         bar_init(smem_addr(&b_end[0]), 1);
@@ -493,14 +513,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             tc_commit(smem_addr(&b_end[scores]));
         __syncwarp();
         bar_wait(smem_addr(&b_end[scores]), 0);
-    } else if (I8 && warp >= 8 && warp < 12) {
+    } else if (I8 && warp >= 16 && warp < 20) {
         // ---- codes to binary16
         // A thread keeps its 16-byte chunk c and its row modulo 16 (32).  Eight
         // lanes that access shared memory together take half of one row's chunks
         // and the other half of the next one's, which keeps the swizzled reads
         // and writes free of bank conflicts.
         constexpr int CPR = C::RB / 16;
-        const int cw = tid - 256, u = cw % (2 * CPR), odd = (u >> 2) & 1;
+        const int cw = tid - C::SOFT, u = cw % (2 * CPR), odd = (u >> 2) & 1;
         const int c = (u & 3) + (CPR == 8 ? 4 * (odd ^ (u >> 3)) : 0);
         const int r = cw / (2 * CPR) * 2 + odd;
         const unsigned src0 = r * C::RB + ((CPR == 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
@@ -547,32 +567,31 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     bar_arrive(smem_addr(&b_raw_empty[rs]));
             }
         }
-    } else if (warp < 8) {
-        // ---- softmax
-        const int wg = warp >> 2, ww = warp & 3, g = lane >> 2, t4 = lane & 3;
+    } else if (warp < 16) {
+        // ---- softmax: stream sx takes every other tile, half hx of its columns
+        constexpr int HC = TP / 2;  // columns of a half
+        const int sx = (warp >> 2) & 1, hx = warp >> 3, ww = warp & 3, g = lane >> 2, t4 = lane & 3;
         const unsigned lanes = (unsigned)(32 * ww) << 16, low = 16u << 16;
-        const unsigned tO = tmem + lanes + C::T_O + wg * 128;
+        const unsigned tO = tmem + lanes + C::T_O + sx * 128;
         Finish<false, RM, C::SOFT, SoftSync> fin;
-        int i0 = 0, nt = 0;  // tile of the run; this group's tiles so far
+        int i0 = 0, nt = 0;  // tile of the run; this stream's tiles so far
         for (int k = 0;; ++k) {
             const int buf = k & 1;
             wait(smem_addr(&b_q_full[buf]), (k >> 1) & 1);
-            const int n = wait.dead ? 0 : s_n[buf], tile0 = s_tile0[buf];
+            // (all end together, or a barrier among them would not)
+            const int n = any_of<C::SOFT>(1, wait.dead) ? 0 : s_n[buf], tile0 = s_tile0[buf];
             if (n == 0)
                 break;
             const int len = s_unit[buf].len;
             float inv[2], m[2], l[2];
-            unsigned long long bits[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int row = 16 * ww + g + 8 * r;
-                inv[r] = s_inv[buf][row];
-                bits[r] = s_bits[buf][row];
+                inv[r] = s_inv[buf][16 * ww + g + 8 * r];
                 m[r] = -INFINITY;
                 l[r] = 0.f;
             }
 
-            for (int t = wg; t < n; t += 2, ++nt) {
+            for (int t = sx; t < n; t += 2, ++nt) {
                 const int p0 = (tile0 + t) * TP;
                 const bool edge = p0 + TP > len;
                 // (weights overwrite their own scores)
@@ -580,30 +599,33 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const unsigned tS = tmem + lanes + C::T_S + sb * 64;
                 wait(smem_addr(&b_s_full[sb]), ((i0 + t) / C::NS) & 1);
                 tc_fence_after();
-                const float *sc = scales + ((i0 + t) % C::NSC) * 2 * TP + 2 * t4;
+                const float *sc =
+                    scales + ((i0 + t) % C::NSC) * 2 * TP + hx * HC + 2 * t4;
                 if (I8)
                     wait(smem_addr(&b_sc_full[(i0 + t) % C::NSC]), ((i0 + t) / C::NSC) & 1);
-                unsigned seen[2] = {0xffffu, 0xffffu};  // bit 2 j + c: column 8 j + 2 t4 + c
+                unsigned seen[2] = {0xffu, 0xffu};  // bit 2 j + c: column 8 j + 2 t4 + c of the half
                 if (edge) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int q = p0 + 8 * (e >> 1) + 2 * t4 + (e & 1) - len;
+                    for (int r = 0; r < 2; ++r) {
+                        const unsigned long long bits = s_bits[buf][16 * ww + g + 8 * r];
 #pragma unroll
-                        for (int r = 0; r < 2; ++r)
-                            if (!(q < 0 || (q < 64 && ((bits[r] >> q) & 1))))
+                        for (int e = 0; e < 8; ++e) {
+                            const int q = p0 + hx * HC + 8 * (e >> 1) + 2 * t4 + (e & 1) - len;
+                            if (!(q < 0 || (q < 64 && ((bits >> q) & 1))))
                                 seen[r] &= ~(1u << e);
+                        }
                     }
                     if (!I8) {
                         // a NaN or an infinity among the values must not reach rows
                         // that do not see it: taken out of the operand here
-                        const int st = (i0 + t) % NV;
+                        const int st = (i0 + t) % NV, tt = hx * 128 + (tid & 127);
                         wait(smem_addr(&b_v_full[st]), ((i0 + t) / NV) & 1);
-                        if (ww == 0 && lane < 2)
-                            s_bad[wg][lane] = 0u;
-                        asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
+                        if (tt < 2)
+                            s_bad[sx][tt] = 0u;
+                        stream_any(sx, false);
                         unsigned char *vb = smem + C::OFF_V + st * C::OPER;
-                        for (int k = tid & 127; k < C::OPER / 16; k += 128) {
-                            uint4 *q = reinterpret_cast<uint4 *>(vb) + k;
+                        for (int k2 = tt; k2 < C::OPER / 16; k2 += 256) {
+                            uint4 *q = reinterpret_cast<uint4 *>(vb) + k2;
                             const uint4 u = *q;
                             const unsigned wd[4] = {u.x, u.y, u.z, u.w};
                             bool bad = false;
@@ -614,58 +636,58 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             }
                             if (bad) {
                                 *q = make_uint4(0u, 0u, 0u, 0u);
-                                const int row = (k >> 3) & (TP - 1);
-                                atomicOr(&s_bad[wg][row >> 5], 1u << (row & 31));
+                                const int row = (k2 >> 3) & (TP - 1);
+                                atomicOr(&s_bad[sx][row >> 5], 1u << (row & 31));
                             }
                         }
                         fence_async_smem();
-                        asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
+                        stream_any(sx, false);
                     }
                 }
-                float v[32];
+                float v[16];
                 // scores (without the row's factor): v[4 j + 2 r + c]
                 auto scores = [&]() {
-                    float lo[32];
-                    tm_ld64(tS, v);
-                    tm_ld64(tS + low, lo);
+                    float lo[16];
+                    tm_ld(tS + hx * HC, v);
+                    tm_ld(tS + low + hx * HC, lo);
                     tm_wait_ld(v);
                     tm_wait_ld(lo);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2)
+                    for (int e = 0; e < 16; e += 2)
                         add2(v[e], v[e + 1], lo[e], lo[e + 1]);
                     if (I8) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float2 k = *reinterpret_cast<const float2 *>(sc + 8 * j);
-                            mul2(v[4 * j], v[4 * j + 1], k.x, k.y);
-                            mul2(v[4 * j + 2], v[4 * j + 3], k.x, k.y);
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 k2 = *reinterpret_cast<const float2 *>(sc + 8 * j);
+                            mul2(v[4 * j], v[4 * j + 1], k2.x, k2.y);
+                            mul2(v[4 * j + 2], v[4 * j + 3], k2.x, k2.y);
                         }
                     }
                     if (edge) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
+                        for (int e = 0; e < 16; ++e)
                             if (!((seen[(e >> 1) & 1] >> (2 * (e >> 2) + (e & 1))) & 1))
                                 v[e] = -INFINITY;
                     }
                 };
-                // weights under references m0, m1; the sums of 2^(s - m) and
-                // the largest weight
+                // weights under the references; the sums of 2^(s - m) and the
+                // largest weight
                 auto weights = [&](float m0, float m1, float (&sum)[2], float (&big)[2]) {
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         float s0 = 0.f, s1 = 0.f;
                         big[r] = 0.f;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
+                        for (int j = 0; j < 4; ++j) {
                             float &p = v[4 * j + 2 * r], &q = v[4 * j + 2 * r + 1];
                             fma2(p, q, inv[r], r ? -m1 : -m0);
                             p = ex2(p);
                             q = ex2(q);
                             add2(s0, s1, p, q);
                             if (I8) {
-                                const float2 k =
+                                const float2 k2 =
                                     *reinterpret_cast<const float2 *>(sc + TP + 8 * j);
-                                mul2(p, q, k.x, k.y);
+                                mul2(p, q, k2.x, k2.y);
                                 if (edge) {
                                     p = (seen[r] >> (2 * j)) & 1 ? p : 0.f;
                                     q = (seen[r] >> (2 * j + 1)) & 1 ? q : 0.f;
@@ -683,75 +705,90 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
                     moved |= !(big[r] <= kWeightMax && sum[r] <= kSumMax) || m[r] == -INFINITY;
-                moved = __any_sync(0xffffffffu, moved);
+                moved = stream_any(sx, moved);
                 if (moved) {  // a row's first weights, or one out of range: rare
                     scores();
                     float mn[2], ms[2];
+                    // a row's maximum over both halves, by way of shared memory
+                    auto row_max = [&](float (&x)[2], const bool scaled) {
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            x[r] = quad_max(x[r]) * (scaled ? inv[r] : 1.f);
+                            if (t4 == 0)
+                                s_max[sx][hx][16 * ww + g + 8 * r] = x[r];
+                        }
+                        stream_any(sx, false);
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+                            x[r] = fmaxf(x[r], s_max[sx][hx ^ 1][16 * ww + g + 8 * r]);
+                        stream_any(sx, false);
+                    };
+                    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        top[(e >> 1) & 1] = fmaxf(top[(e >> 1) & 1], v[e]);
+                    row_max(top, true);
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        float top = -INFINITY;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            top = fmaxf(top, fmaxf(v[4 * j + 2 * r], v[4 * j + 2 * r + 1]));
-                        mn[r] = ref_from_scores(m[r], quad_max(top) * inv[r]);
+                        mn[r] = ref_from_scores(m[r], top[r]);
                         ms[r] = mn[r] == -INFINITY ? 0.f : mn[r];
                     }
                     weights(ms[0], ms[1], sum, big);
+                    row_max(big, false);
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const float k = ref_shift(m[r] == -INFINITY, quad_max(big[r]));
-                        const float g2 = ex2(-k);
-                        mn[r] += k;
+                        const float k2 = ref_shift(m[r] == -INFINITY, big[r]);
+                        const float g2 = ex2(-k2);
+                        mn[r] += k2;
                         sum[r] *= g2;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
+                        for (int j = 0; j < 4; ++j)
                             mul2(v[4 * j + 2 * r], v[4 * j + 2 * r + 1], g2, g2);
                         f[r] = mn[r] == -INFINITY ? 1.f : ex2(m[r] - mn[r]);
                         m[r] = mn[r];
                     }
                 }
-                unsigned ph[16], pl[16];
+                unsigned ph[8], pl[8];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     l[r] = fmaf(l[r], f[r], sum[r]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < 4; ++j) {
                         const float p = v[4 * j + 2 * r], q = v[4 * j + 2 * r + 1];
                         ph[2 * j + r] = h2(p, q);
                         const float2 h =
                             __half22float2(*reinterpret_cast<const __half2 *>(&ph[2 * j + r]));
-                        float dp = p, dq = q;
-                        add2(dp, dq, -h.x, -h.y);
-                        pl[2 * j + r] = h2(dp, dq);
+                        float dp = p, dq2 = q;
+                        add2(dp, dq2, -h.x, -h.y);
+                        pl[2 * j + r] = h2(dp, dq2);
                     }
                 }
                 if (!I8 && edge) {
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int col = 8 * j + 2 * t4;
-                            if ((s_bad[wg][col >> 5] >> (col & 31)) & (seen[r] >> (2 * j)) & 3)
+                        for (int j = 0; j < 4; ++j)
+                            if ((s_bad[sx][hx] >> (8 * j + 2 * t4)) & (seen[r] >> (2 * j)) & 3)
                                 l[r] = __int_as_float(0x7fc00000);  // its result is NaN
-                        }
                 }
-                tm_st_pairs(tS, ph);
-                tm_st_pairs(tS + low, pl);
+                // (every score of the buffer was read before stream_any)
+                tm_st_pairs(tS + hx * (HC / 2), ph);
+                tm_st_pairs(tS + low + hx * (HC / 2), pl);
                 if (t >= 2 && moved) {
-                    wait(smem_addr(&b_pv_done[wg]), (nt - 1) & 1);  // the output is at rest
+                    wait(smem_addr(&b_pv_done[sx]), (nt - 1) & 1);  // the output is at rest
                     tc_fence_after();
 #pragma unroll
                     for (int half = 0; half < 2; ++half)
 #pragma unroll
-                        for (int cb = 0; cb < D; cb += 64) {
-                            float o[32];
-                            const unsigned at = tO + (half ? low : 0u) + cb;
-                            tm_ld64(at, o);
+                        for (int cb = 0; cb < D / 2; cb += 32) {
+                            float o[16];
+                            const unsigned at = tO + (half ? low : 0u) + hx * (D / 2) + cb;
+                            tm_ld(at, o);
                             tm_wait_ld(o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
+                            for (int e = 0; e < 16; ++e)
                                 o[e] *= f[(e >> 1) & 1];
-                            tm_st64(at, o);
+                            tm_st(at, o);
                         }
                 }
                 tm_wait_st();
@@ -762,24 +799,25 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             i0 += n;
 
-            // ---- the unit's (part's) end: both groups' outputs
-            const bool have = wg < n;  // this group took a tile
+            // ---- the unit's (part's) end: both streams' outputs
+            const bool have = sx < n;  // this stream took a tile
             if (have)
-                wait(smem_addr(&b_pv_done[wg]), (nt - 1) & 1);
+                wait(smem_addr(&b_pv_done[sx]), (nt - 1) & 1);
             tc_fence_after();
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
                 l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
                 if (t4 == 0) {
-                    s_m[wg][16 * ww + g + 8 * r] = m[r];
-                    s_l[wg][16 * ww + g + 8 * r] = l[r];
+                    s_m[sx][16 * ww + g + 8 * r] = m[r];
+                    s_l[2 * sx + hx][16 * ww + g + 8 * r] = l[r];
                 }
             }
             SoftSync::sync();
-            // Each group finishes one half of the columns (64 of them; the first
-            // group all where there are no more): the other group's half goes
-            // through the unit's query operand, whose products are all done.
+            // Group (sx, hx) finishes columns hx D / 2 + sx D / 4 and on, D / 4 of
+            // them; the other stream's share of them comes through the unit's
+            // query operand, whose products are all done.
+            constexpr int QC = D / 4, NE = QC / 2;
             const Unit x = s_unit[buf];
             const bool all = fin.whole(run, x);
             float *rec = fin.record(a, run, x);
@@ -789,70 +827,67 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const int row = 16 * ww + g + 8 * r;
                 const float M = fmaxf(s_m[0][row], s_m[1][row]), ms = M == -INFINITY ? 0.f : M;
                 fac[r] = ex2(m[r] - ms);
-                lsum[r] = s_l[0][row] * ex2(s_m[0][row] - ms) + s_l[1][row] * ex2(s_m[1][row] - ms);
-                if (wg == 0 && t4 == 0 && !all && row < x.nrows) {
+                lsum[r] = (s_l[0][row] + s_l[1][row]) * ex2(s_m[0][row] - ms) +
+                          (s_l[2][row] + s_l[3][row]) * ex2(s_m[1][row] - ms);
+                if (warp < 4 && t4 == 0 && !all && row < x.nrows) {
                     __stcg(rec + RM * D + row, M);
                     __stcg(rec + RM * D + RM + row, lsum[r]);
                 }
             }
-            float2 *const xq = reinterpret_cast<float2 *>(smem + buf * C::QB) + ww * 16 * 32 + lane;
-            auto load_o = [&](int cb, float (&o)[32]) {
-                float lo[32];
-                tm_ld64(tO + cb, o);
-                tm_ld64(tO + low + cb, lo);
+            auto load_o = [&](int col, float (&o)[NE]) {
+                float lo[NE];
+                tm_ld(tO + col, o);
+                tm_ld(tO + low + col, lo);
                 tm_wait_ld(o);
                 tm_wait_ld(lo);
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
+                for (int e = 0; e < NE; ++e)
                     o[e] = (o[e] + lo[e]) * fac[(e >> 1) & 1];
             };
-            constexpr int HB = C::RM * 64 / 2;  // float2 places of a half
-            const int mine = D == 128 ? wg : 0, other = mine ^ 1;
-            float o[32];
-            if (have && (D == 128 || wg == 1)) {
-                load_o(D == 128 ? other * 64 : 0, o);
-                float2 *q = xq + (D == 128 ? other * HB : 0);
+            // place of (hx, stream, ww, e / 2, lane): no bank conflicts
+            float2 *const xq = reinterpret_cast<float2 *>(smem + buf * C::QB) +
+                               (hx * 8 + ww) * (NE / 2) * 32 + lane;
+            constexpr int SXS = 4 * (NE / 2) * 32;
+            const int c0 = hx * (D / 2);
+            float o[NE];
+            if (have) {
+                load_o(c0 + (sx ^ 1) * QC, o);
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    q[e * 32] = make_float2(o[2 * e], o[2 * e + 1]);
+                for (int e = 0; e < NE / 2; ++e)
+                    xq[(sx ^ 1) * SXS + e * 32] = make_float2(o[2 * e], o[2 * e + 1]);
+                load_o(c0 + sx * QC, o);
+            } else {
+#pragma unroll
+                for (int e = 0; e < NE; ++e)
+                    o[e] = 0.f;
             }
-            if (have && (D == 128 || wg == 0))
-                load_o(mine * 64, o);
             tc_fence_before();
             SoftSync::sync();
-            if (D == 128 || wg == 0) {
-                if (!have) {
+            if (sx == 1 || n > 1) {  // the other stream took a tile
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        o[e] = 0.f;
+                for (int e = 0; e < NE / 2; ++e) {
+                    const float2 y = xq[sx * SXS + e * 32];
+                    o[2 * e] += y.x;
+                    o[2 * e + 1] += y.y;
                 }
-                if (wg == 1 || n > 1) {  // the other group took a tile
-                    const float2 *q = xq + mine * HB;
+            }
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 v = q[e * 32];
-                        o[2 * e] += v.x;
-                        o[2 * e + 1] += v.y;
-                    }
-                }
+            for (int r = 0; r < 2; ++r) {
+                const int row = 16 * ww + g + 8 * r;
+                if (row >= x.nrows)
+                    continue;
+                const float rl = lsum[r] == 0.f ? 0.f : __frcp_rn(lsum[r]);
+                float *dst = (all ? a.out + out_at<false>(a, x, row) : rec + row * D) + c0 +
+                             sx * QC + 2 * t4;
+                const float fr = all ? rl : 1.f;
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int row = 16 * ww + g + 8 * r;
-                    if (row >= x.nrows)
-                        continue;
-                    const float rl = lsum[r] == 0.f ? 0.f : __frcp_rn(lsum[r]);
-                    float *dst = (all ? a.out + out_at<false>(a, x, row) : rec + row * D) +
-                                 mine * 64 + 2 * t4;
-                    const float f = all ? rl : 1.f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 v =
-                            make_float2(o[4 * j + 2 * r] * f, o[4 * j + 2 * r + 1] * f);
-                        if (all)
-                            *reinterpret_cast<float2 *>(dst + 8 * j) = v;
-                        else
-                            __stcg(reinterpret_cast<float2 *>(dst + 8 * j), v);
-                    }
+                for (int j = 0; j < QC / 8; ++j) {
+                    const float2 y =
+                        make_float2(o[4 * j + 2 * r] * fr, o[4 * j + 2 * r + 1] * fr);
+                    if (all)
+                        *reinterpret_cast<float2 *>(dst + 8 * j) = y;
+                    else
+                        __stcg(reinterpret_cast<float2 *>(dst + 8 * j), y);
                 }
             }
             fin.done(a, run, x);
