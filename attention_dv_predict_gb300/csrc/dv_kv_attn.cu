@@ -207,7 +207,7 @@ cudaError_t launch_gen(const KvAttnArgs &a, int grid, cudaStream_t st)
 }  // namespace
 
 // Tensor cores serve binary16 and 8-bit rows of 64 and 128 values: units of 8
-// query rows on mma.sync, of 64 on tcgen05.
+// query rows on mma.sync, of 64 on tcgen05 (rows: the largest unit's).
 KvPlan kv_plan(int dtype, int D, int rows)
 {
     KvPlan p;
@@ -216,10 +216,28 @@ KvPlan kv_plan(int dtype, int D, int rows)
     return p;
 }
 
+// Whether units of 8 rows, which read the cache once for every 8, are the
+// faster ones for more than 8 rows.  Measured (us, units of 8 / of 64): 768
+// heads of 2112 positions of 128 values, 8 bits: 16 rows 183 / 218, 24 rows
+// 266 / 222, 40 rows 433 / 231; binary16: 12 rows 255 / 152; 120 heads of 17
+// tiles at most, 8 bits: 12 rows 23 / 37, 40 rows 30 / 44; binary16: 23 / 35,
+// 33 / 45.  So a tile of 64 positions takes the units of 8 about 3.6 (8-bit)
+// or 5.0 ns a pass over it and the units of 64 7.4 or 4.9 ns, and these take
+// about 15 us longer to start and to end.  The lengths are known on the device only:
+// the capacity stands for them.
+static bool kv_small_units(const KvAttnArgs &a)
+{
+    const int rows = a.T * (a.H / a.c.Hkv), passes = (rows + 7) / 8;
+    const double tiles = (double)a.B * (a.u_h ? a.max_u_h : a.c.Hkv) * ((a.c.cap + 63) / 64);
+    const bool i8 = a.c.dtype == DV_I8;
+    return tiles * (passes * (i8 ? 3.6 : 5.0) - (i8 ? 7.4 : 4.9)) <= 15000;
+}
+
 cudaError_t launch_kv_attn(const KvAttnArgs &a, const KvPlan &p, int nsm, cudaStream_t st)
 {
     if (p.mma)
-        return p.rows == 8 ? launch_kv_mma(a, nsm, st) : launch_kv_tc(a, nsm, st);
+        return p.rows == 8 || kv_small_units(a) ? launch_kv_mma(a, nsm, st)
+                                                : launch_kv_tc(a, nsm, st);
     const int grid = nsm * 4 < kKvMaxCtas ? nsm * 4 : kKvMaxCtas;
     if (a.c.dtype == DV_I8)
         return launch_gen<int8_t>(a, grid, st);

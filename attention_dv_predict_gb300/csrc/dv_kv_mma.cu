@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
 #pragma unroll
         for (int i = 0; i < NT; ++i)
             o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        float m = -INFINITY, l = 0.f, sg = 1.f;  // max, sum, power of two the weights are taken over
+        float m = -INFINITY, l = 0.f;  // reference point, sum
 
         for (w = tile_place(x, w); w < wend; ++w) {
             if (C::I8)
@@ -287,41 +287,35 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
                     }
                 }
             }
-            // ---- running max, weights, their power of two
-            const float mx = quad_max(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
-            const float mn = fmaxf(m, mx), ms = mn == -INFINITY ? 0.f : mn;
-            float f = ex2(m - ms), p[4];
-            m = mn;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                p[e] = ex2(v[e] - ms);
-            l = fmaf(l, f, (p[0] + p[1]) + (p[2] + p[3]));
-            float up = 16384.f;
-            if (C::I8) {
+            // ---- weights under the row's reference point (no reduction over the row)
+            float p[4], sum, big;
+            auto weights = [&](float ms) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    p[e] = (seen >> e) & 1 ? p[e] * vs[e] : 0.f;
-                // weights relative to the largest so far: the low part keeps its
-                // bits whatever the scales are
-                const float big =
-                    fmaxf(sg * f, quad_max(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]))));
-                if (big >= 2.f * sg || (big < sg * 0x1p-10f && big > 0.f)) {
-                    const float now =
-                        fmaxf(__uint_as_float(__float_as_uint(big) & 0x7f800000u), 0x1p-100f);
-                    f = f * sg / now;
-                    sg = now;
-                }
-                up = 16384.f / sg;
-            }
-            unsigned hh[2], ll[2];
+                    p[e] = ex2(v[e] - ms);
+                sum = (p[0] + p[1]) + (p[2] + p[3]);
+                if (C::I8) {
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                const float w0 = p[2 * nt] * up, w1 = p[2 * nt + 1] * up;
-                hh[nt] = h2(w0, w1);
-                ll[nt] = h2_rest(w0, w1, hh[nt]);
-            }
-            const uint4 pw = make_uint4(hh[0], ll[0], hh[1], ll[1]);
-            if (__any_sync(0xffffffffu, f != 1.f)) {
+                    for (int e = 0; e < 4; ++e)
+                        p[e] = (seen >> e) & 1 ? p[e] * vs[e] : 0.f;
+                }
+                big = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
+            };
+            weights(m == -INFINITY ? 0.f : m);
+            const bool range = big <= kWeightMax && sum <= kSumMax && m != -INFINITY;
+            if (!__all_sync(0xffffffffu, range)) {  // first weights, or one out of range: rare
+                const float top = quad_max(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
+                float mn = ref_from_scores(m, top);
+                weights(mn == -INFINITY ? 0.f : mn);
+                const float k = ref_shift(m == -INFINITY, quad_max(big)), g2 = ex2(-k);
+                mn += k;
+                sum *= g2;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    p[e] *= g2;
+                const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+                m = mn;
+                l *= f;
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     o[i][0] *= f;
@@ -330,6 +324,14 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
                     o[i][3] *= f;
                 }
             }
+            l += sum;
+            unsigned hh[2], ll[2];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                hh[nt] = h2(p[2 * nt], p[2 * nt + 1]);
+                ll[nt] = h2_rest(p[2 * nt], p[2 * nt + 1], hh[nt]);
+            }
+            const uint4 pw = make_uint4(hh[0], ll[0], hh[1], ll[1]);
             // ---- values
             unsigned bad = 0;  // edge tiles of binary16: positions not finite
             const int pos[4] = {pc0, pc1, 8 + pc0, 8 + pc1};
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
         for (int i = 0; i < WP; ++i)
             M = fmaxf(M, s_m[i][g]);
         const float ms = M == -INFINITY ? 0.f : M;
-        const float fac = ex2(m - ms) * (sg * (1.f / 16384.f));
+        const float fac = ex2(m - ms);
         if (warp == 0 && t == 0) {
             float L = 0.f;
 #pragma unroll

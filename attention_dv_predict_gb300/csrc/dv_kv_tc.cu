@@ -242,10 +242,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             bar_init(smem_addr(&b_sc_full[i]), 32);
         for (int i = 0; i < NV; ++i) {
             if (i < NK) {
-                bar_init(smem_addr(&b_k_full[i]), I8 ? 4 : 1);
+                bar_init(smem_addr(&b_k_full[i]), I8 ? 2 : 1);
                 bar_init(smem_addr(&b_k_empty[i]), 1);
             }
-            bar_init(smem_addr(&b_v_full[i]), I8 ? 4 : 1);
+            bar_init(smem_addr(&b_v_full[i]), I8 ? 2 : 1);
             bar_init(smem_addr(&b_v_empty[i]), 1);
         }
         for (int i = 0; i < C::NS; ++i) {
@@ -514,57 +514,62 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncwarp();
         bar_wait(smem_addr(&b_end[scores]), 0);
     } else if (I8 && warp >= 16 && warp < 20) {
-        // ---- codes to binary16
-        // A thread keeps its 16-byte chunk c and its row modulo 16 (32).  Eight
+        // ---- codes to binary16: two warps the keys, two the values.
+        // A thread keeps its 16-byte chunk c and its row modulo the pass.  Eight
         // lanes that access shared memory together take half of one row's chunks
         // and the other half of the next one's, which keeps the swizzled reads
         // and writes free of bank conflicts.
-        constexpr int CPR = C::RB / 16;
-        const int cw = tid - C::SOFT, u = cw % (2 * CPR), odd = (u >> 2) & 1;
+        constexpr int CPR = C::RB / 16, RPP = 64 / CPR, PASSES = TP / RPP;
+        constexpr int NSR = I8 ? C::NSR : 1;
+        const int side = (warp - 16) >> 1;
+        const int cw = tid & 63, u = cw % (2 * CPR), odd = (u >> 2) & 1;
         const int c = (u & 3) + (CPR == 8 ? 4 * (odd ^ (u >> 3)) : 0);
         const int r = cw / (2 * CPR) * 2 + odd;
         const unsigned src0 = r * C::RB + ((CPR == 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
         const unsigned dst0 = (c >> 2) * (TP * 128) + r * 128 + ((((2 * c) & 7) ^ (r & 7)) << 4);
-        int i = 0;
+        const int ns = side ? NV : NK;
+        const unsigned ring = sbase + (side ? C::OFF_V : C::OFF_OP);
+        uint64_t *const full = side ? b_v_full : b_k_full, *const empty = side ? b_v_empty : b_k_empty;
+        int i = 0, fs = 0, ph = 0;  // tile of the run; its slot and phase (counted: a
+                                    // division by ns took longer than the codes)
         for (long long w = run.lo; w < run.hi;) {
             const Unit x = sched_unit<false>(a, RM, sm, run, w);
             const long long wend = min(run.hi, x.w1);
             const int n = x.h < 0 ? 0 : (int)(wend - tile_place(x, w));
             w = wend;
             for (int t = 0; t < n; ++t, ++i) {
-                const int rs = i % (I8 ? C::NSR : 1);
-                wait(smem_addr(&b_raw_full[rs]), (i / (I8 ? C::NSR : 1)) & 1);
-                constexpr int STEP = 128 / CPR;  // rows a pass
-#pragma unroll 1
-                for (int side = 0; side < 2; ++side) {
-                    const int ns = side ? NV : NK, fs = i % ns;
-                    if (i >= ns)
-                        wait(smem_addr(side ? &b_v_empty[fs] : &b_k_empty[fs]), (i / ns - 1) & 1);
-                    const unsigned src =
-                        sbase + C::OFF_RAW + rs * 2 * C::RAW + side * C::RAW + src0;
-                    const unsigned dst = sbase + (side ? C::OFF_V : C::OFF_OP) + fs * C::OPER;
+                const int rs = i % NSR;
+                wait(smem_addr(&b_raw_full[rs]), (i / NSR) & 1);
+                if (i >= ns)
+                    wait(smem_addr(&empty[fs]), ph ^ 1);
+                const unsigned src = sbase + C::OFF_RAW + rs * 2 * C::RAW + side * C::RAW + src0;
+                const unsigned dst = ring + fs * C::OPER;
 #pragma unroll
-                    for (int off = 0; off < TP; off += STEP) {
-                        const uint4 u = lds16(src + off * C::RB);
-                        const unsigned b0 = u.x ^ 0x80808080u, b1 = u.y ^ 0x80808080u,
-                                       b2 = u.z ^ 0x80808080u, b3 = u.w ^ 0x80808080u;
-                        const unsigned at = dst + off * 128;
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + dst0),
-                                     "r"(codes_lo(b0)), "r"(codes_hi(b0)), "r"(codes_lo(b1)),
-                                     "r"(codes_hi(b1))
-                                     : "memory");
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + (dst0 ^ 16)),
-                                     "r"(codes_lo(b2)), "r"(codes_hi(b2)), "r"(codes_lo(b3)),
-                                     "r"(codes_hi(b3))
-                                     : "memory");
+                for (int p0 = 0; p0 < PASSES; p0 += 4) {
+                    uint4 q[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        q[j] = lds16(src + (p0 + j) * RPP * C::RB);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const unsigned b0 = q[j].x ^ 0x80808080u, b1 = q[j].y ^ 0x80808080u,
+                                       b2 = q[j].z ^ 0x80808080u, b3 = q[j].w ^ 0x80808080u;
+                        const unsigned at = dst + (p0 + j) * RPP * 128;
+                        sts16(at + dst0, codes_lo(b0), codes_hi(b0), codes_lo(b1), codes_hi(b1));
+                        sts16(at + (dst0 ^ 16), codes_lo(b2), codes_hi(b2), codes_lo(b3),
+                              codes_hi(b3));
                     }
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        bar_arrive(smem_addr(side ? &b_v_full[fs] : &b_k_full[fs]));
                 }
-                if (lane == 0)
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    bar_arrive(smem_addr(&full[fs]));
                     bar_arrive(smem_addr(&b_raw_empty[rs]));
+                }
+                if (++fs == ns) {
+                    fs = 0;
+                    ph ^= 1;
+                }
             }
         }
     } else if (warp < 16) {

@@ -90,6 +90,12 @@ DV_DEV uint4 lds16(unsigned a)
                  : "r"(a));
     return r;
 }
+DV_DEV void sts16(unsigned a, unsigned x, unsigned y, unsigned z, unsigned w)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z),
+                 "r"(w)
+                 : "memory");
+}
 DV_DEV uint2 lds8(unsigned a)
 {
     uint2 r;
