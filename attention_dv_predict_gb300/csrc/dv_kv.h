@@ -8,6 +8,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "dv.h"
 #include "dv_internal.h"
 
@@ -96,6 +98,9 @@ struct KvPlan {
     bool mma;    // tensor-core kernel
 };
 KvPlan kv_plan(int dtype, int D, int rows);
+
+// Units of dv_tree_attn where both kinds serve: 0 by rule, 1 of 8 rows, 2 of 64.
+extern std::atomic<int> g_tree_variant;
 
 cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t st);
 cudaError_t launch_kv_read(const KvReadArgs &a, cudaStream_t st);

@@ -154,6 +154,14 @@ cudaError_t kv_maps(const KvCacheArgs &c, int B, int rows, KvMaps *m)
 
 extern "C" {
 
+dv_status dv_set_tree_kernel(int variant)
+{
+    if (variant < 0 || variant > 2)
+        return DV_ERR_INVALID_ARG;
+    g_tree_variant.store(variant);
+    return DV_OK;
+}
+
 size_t dv_kv_workspace_size(const dv_kv_desc *desc, int batch, int tokens)
 {
     if (check_desc(desc) != DV_OK || batch < 1 || batch > DV_KV_MAX_BATCH || tokens < 1 ||

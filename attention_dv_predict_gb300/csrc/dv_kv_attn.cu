@@ -206,6 +206,8 @@ cudaError_t launch_gen(const KvAttnArgs &a, int grid, cudaStream_t st)
 
 }  // namespace
 
+std::atomic<int> g_tree_variant{0};
+
 // Tensor cores serve binary16 and 8-bit rows of 64 and 128 values: units of 8
 // query rows on mma.sync, of 64 on tcgen05 (rows: the largest unit's).
 KvPlan kv_plan(int dtype, int D, int rows)
@@ -227,6 +229,8 @@ KvPlan kv_plan(int dtype, int D, int rows)
 // the capacity stands for them.
 static bool kv_small_units(const KvAttnArgs &a)
 {
+    if (const int v = g_tree_variant.load())
+        return v == 1;
     const int rows = a.T * (a.H / a.c.Hkv), passes = (rows + 7) / 8;
     const double tiles = (double)a.B * (a.u_h ? a.max_u_h : a.c.Hkv) * ((a.c.cap + 63) / 64);
     const bool i8 = a.c.dtype == DV_I8;

@@ -17,7 +17,7 @@
 //             take half of a tile's columns each four: a warp's own latency
 //             bounds it.  Four score buffers, whose weights take the scores'
 //             place, let scores run ahead
-//   16-19     8-bit caches: codes to binary16, raw ring -> operand ring
+//   16-23     8-bit caches: codes to binary16, raw ring -> operand ring
 //   last four one that prepares a unit's queries while the unit before runs,
 //             one of tensor-map copies (and scales by cp.async), one whose
 //             elected thread issues the scores' MMAs, one the values'
@@ -45,7 +45,7 @@ struct TcCfg {
     static constexpr int NSR = I8 ? (D == 128 ? 4 : 8) : 0;  // raw stages
     static constexpr int NSC = D == 128 ? 8 : 16;         // scale slots (see the producer)
     static constexpr int QB = 128 * D * 2;
-    static constexpr int WARPS = 16 + (I8 ? 4 : 0) + 4, THREADS = 32 * WARPS;
+    static constexpr int WARPS = 16 + (I8 ? 8 : 0) + 4, THREADS = 32 * WARPS;
     static constexpr int SOFT = 512;                      // softmax threads
     static constexpr int OFF_OP = 2 * QB;
     static constexpr int OFF_V = OFF_OP + NK * OPER;
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     __shared__ unsigned s_bad[2][2];  // binary16 edge tiles: positions not finite
     __shared__ __align__(8) uint64_t b_raw_full[I8 ? C::NSR : 1], b_raw_empty[I8 ? C::NSR : 1],
         b_sc_full[C::NSC], b_k_full[NK], b_k_empty[NK], b_v_full[NV], b_v_empty[NV], b_s_full[C::NS],
-        b_p_full[C::NS], b_pv_done[2], b_s_free[C::NS], b_q_full[2], b_q_free[2], b_end[2];
+        b_p_full[C::NS], b_s_free[C::NS], b_q_full[2], b_q_free[2], b_end[2];
     __shared__ unsigned s_tmem;
     unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const unsigned sbase = smem_addr(smem);
@@ -236,16 +236,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (tid == 0) {
         for (int i = 0; i < C::NSR; ++i) {
             bar_init(smem_addr(&b_raw_full[i]), 1);
-            bar_init(smem_addr(&b_raw_empty[i]), 4);
+            bar_init(smem_addr(&b_raw_empty[i]), 8);
         }
         for (int i = 0; i < C::NSC; ++i)
             bar_init(smem_addr(&b_sc_full[i]), 32);
         for (int i = 0; i < NV; ++i) {
             if (i < NK) {
-                bar_init(smem_addr(&b_k_full[i]), I8 ? 2 : 1);
+                bar_init(smem_addr(&b_k_full[i]), I8 ? 4 : 1);
                 bar_init(smem_addr(&b_k_empty[i]), 1);
             }
-            bar_init(smem_addr(&b_v_full[i]), I8 ? 2 : 1);
+            bar_init(smem_addr(&b_v_full[i]), I8 ? 4 : 1);
             bar_init(smem_addr(&b_v_empty[i]), 1);
         }
         for (int i = 0; i < C::NS; ++i) {
@@ -253,7 +253,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             bar_init(smem_addr(&b_p_full[i]), 8);
             bar_init(smem_addr(&b_s_free[i]), 1);
             if (i < 2) {
-                bar_init(smem_addr(&b_pv_done[i]), 1);
                 bar_init(smem_addr(&b_q_full[i]), 1);
                 bar_init(smem_addr(&b_q_free[i]), 16);
             }
@@ -492,7 +491,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         for (int kk = 0; kk < TP / 16; ++kk)
                             tc_mma_ts(tmem + C::T_O + g * 128, tmem + C::T_S + sb * 64 + kk * 8,
                                       dv + kk * (16 * 128 >> 4), ID_O, t > 1 || kk > 0);
-                        tc_commit(smem_addr(&b_pv_done[g]));
                         tc_commit(smem_addr(&b_v_empty[st]));
                         tc_commit(smem_addr(&b_s_free[sb]));
                     }
@@ -513,16 +511,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             tc_commit(smem_addr(&b_end[scores]));
         __syncwarp();
         bar_wait(smem_addr(&b_end[scores]), 0);
-    } else if (I8 && warp >= 16 && warp < 20) {
-        // ---- codes to binary16: two warps the keys, two the values.
+    } else if (I8 && warp >= 16 && warp < 24) {
+        // ---- codes to binary16: four warps the keys, four the values
         // A thread keeps its 16-byte chunk c and its row modulo the pass.  Eight
         // lanes that access shared memory together take half of one row's chunks
         // and the other half of the next one's, which keeps the swizzled reads
         // and writes free of bank conflicts.
-        constexpr int CPR = C::RB / 16, RPP = 64 / CPR, PASSES = TP / RPP;
+        constexpr int CPR = C::RB / 16, RPP = 128 / CPR, PASSES = TP / RPP, PQ = PASSES < 4 ? PASSES : 4;
         constexpr int NSR = I8 ? C::NSR : 1;
-        const int side = (warp - 16) >> 1;
-        const int cw = tid & 63, u = cw % (2 * CPR), odd = (u >> 2) & 1;
+        const int side = (warp - 16) >> 2;
+        const int cw = tid & 127, u = cw % (2 * CPR), odd = (u >> 2) & 1;
         const int c = (u & 3) + (CPR == 8 ? 4 * (odd ^ (u >> 3)) : 0);
         const int r = cw / (2 * CPR) * 2 + odd;
         const unsigned src0 = r * C::RB + ((CPR == 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
@@ -545,13 +543,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const unsigned src = sbase + C::OFF_RAW + rs * 2 * C::RAW + side * C::RAW + src0;
                 const unsigned dst = ring + fs * C::OPER;
 #pragma unroll
-                for (int p0 = 0; p0 < PASSES; p0 += 4) {
-                    uint4 q[4];
+                for (int p0 = 0; p0 < PASSES; p0 += PQ) {
+                    uint4 q[PQ];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < PQ; ++j)
                         q[j] = lds16(src + (p0 + j) * RPP * C::RB);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < PQ; ++j) {
                         const unsigned b0 = q[j].x ^ 0x80808080u, b1 = q[j].y ^ 0x80808080u,
                                        b2 = q[j].z ^ 0x80808080u, b3 = q[j].w ^ 0x80808080u;
                         const unsigned at = dst + (p0 + j) * RPP * 128;
@@ -579,7 +577,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const unsigned lanes = (unsigned)(32 * ww) << 16, low = 16u << 16;
         const unsigned tO = tmem + lanes + C::T_O + sx * 128;
         Finish<false, RM, C::SOFT, SoftSync> fin;
-        int i0 = 0, nt = 0;  // tile of the run; this stream's tiles so far
+        int i0 = 0;  // tile of the run
         for (int k = 0;; ++k) {
             const int buf = k & 1;
             wait(smem_addr(&b_q_full[buf]), (k >> 1) & 1);
@@ -596,7 +594,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 l[r] = 0.f;
             }
 
-            for (int t = sx; t < n; t += 2, ++nt) {
+            for (int t = sx; t < n; t += 2) {
                 const int p0 = (tile0 + t) * TP;
                 const bool edge = p0 + TP > len;
                 // (weights overwrite their own scores)
@@ -780,7 +778,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 tm_st_pairs(tS + hx * (HC / 2), ph);
                 tm_st_pairs(tS + low + hx * (HC / 2), pl);
                 if (t >= 2 && moved) {
-                    wait(smem_addr(&b_pv_done[sx]), (nt - 1) & 1);  // the output is at rest
+                    // the output is at rest once the stream's tile before is through
+                    wait(smem_addr(&b_s_free[(sb + 2) % C::NS]), ((i0 + t - 2) / C::NS) & 1);
                     tc_fence_after();
 #pragma unroll
                     for (int half = 0; half < 2; ++half)
@@ -802,12 +801,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (lane == 0)
                     bar_arrive(smem_addr(&b_p_full[sb]));
             }
-            i0 += n;
 
             // ---- the unit's (part's) end: both streams' outputs
+            // (A buffer's phase can be waited for because its next product needs this
+            // stream's weights; a count of the stream's products could not: two
+            // may be outstanding, and a parity does not tell them apart.)
             const bool have = sx < n;  // this stream took a tile
+            const int last = i0 + n - 1 - ((n - 1 - sx) & 1);
             if (have)
-                wait(smem_addr(&b_pv_done[sx]), (nt - 1) & 1);
+                wait(smem_addr(&b_s_free[last % C::NS]), (last / C::NS) & 1);
+            i0 += n;
             tc_fence_after();
 #pragma unroll
             for (int r = 0; r < 2; ++r) {

@@ -106,6 +106,7 @@ _SIGS = {
     "dv_layer_decode_host": ([_D, _W, _P, _P, _I, _I, _I, _P, _P, _I, _S, _P, _P, _SZ, _P], _I),
     "dv_hbm_copy": ([_P, _P, _SZ, _P], _I),
     "dv_test_hold_wait": ([_P, _SZ, _I, _I, _P], _I),
+    "dv_set_tree_kernel": ([_I], _I),
     "dv_kv_workspace_size": ([_KD, _I, _I], _SZ),
     "dv_kv_append": ([_KD, _KC, _KR, _KR, _I, _I, _P, _P, _P, _SZ, _P], _I),
     "dv_kv_read": ([_KD, _KC, _I, _I, _P, _I, _P, _P, _P, _SZ, _P], _I),
@@ -597,6 +598,11 @@ def dv_tree_attn(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, out: torch
         _kv_tensor("u_h", u_h, cache, (m,), torch.int32),
         _kv_tensor("n_u_h", n_u_h, cache, (1,), torch.int32), m,
         _kv_tensor("out", out, cache, shape, torch.float32), ws.ptr, ws.nbytes, st))
+
+
+def dv_set_tree_kernel(variant: int) -> None:
+    """dv_tree_attn above 8 query rows a KV head: 0 by rule, 1 mma.sync, 2 tcgen05."""
+    _check("dv_set_tree_kernel", _lib.dv_set_tree_kernel(int(variant)))
 
 
 def dv_block_topk(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, idx: torch.Tensor,

@@ -557,6 +557,17 @@ int dv_tree_attn(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_r
                  float scale, const int32_t *u_h, const int32_t *n_u_h, int max_u_h, float *out,
                  void *ws, size_t ws_bytes, void *stream);
 
+/* Kernel of dv_tree_attn for more than 8 query rows per KV head (tokens x
+ * group) over binary16 and 8-bit rows of 64 or 128 values, process-wide, for
+ * calls issued after it returns:
+ *   0  the faster one by the sizes known on the host (the default);
+ *   1  mma.sync, 8 query rows at a time (the cache is read once for every 8);
+ *   2  tcgen05, 64 query rows at a time.
+ * Results agree within the binary32 error; the bits may not.
+ * DV_ERR_INVALID_ARG for another value.  Not thread-safe against calls in
+ * flight on other threads. */
+dv_status dv_set_tree_kernel(int variant);
+
 /*
  * dv_block_topk -- the blocks of cached positions each query attends to.
  * desc.block = n > 0; row b has nb = ceil(lens[b] / n) blocks.

@@ -26,6 +26,19 @@ def dv():
 DT = {"f32": 0, "f16": 1, "i8": 2}
 
 
+@pytest.fixture(params=[1, 2], ids=["mma", "tcgen05"])
+def variant(dv, request):
+    """Both tree kernels (they are the same one where only one serves)."""
+    dv.dv_set_tree_kernel(request.param)
+    yield request.param
+    dv.dv_set_tree_kernel(0)
+
+
+def skip_same(variant, dtype, D, rows):
+    if variant == 2 and (dtype == "f32" or D not in (64, 128) or rows <= 8):
+        pytest.skip("one kernel serves this shape")
+
+
 class Case:
     """A random cache on the device and its host twin."""
 
@@ -265,7 +278,8 @@ TREES = [
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "i8"])
 @pytest.mark.parametrize("Hkv,G,D,T,cap", TREES)
-def test_tree_attn(dv, dtype, Hkv, G, D, T, cap):
+def test_tree_attn(dv, variant, dtype, Hkv, G, D, T, cap):
+    skip_same(variant, dtype, D, T * G)
     if dtype == "f32" and D == 256:
         pytest.skip("head_dim * 4 above 512 bytes is not supported")
     B = 5
@@ -297,8 +311,9 @@ def test_tree_attn(dv, dtype, Hkv, G, D, T, cap):
 
 @pytest.mark.parametrize("dtype", ["f16", "i8", "f32"])
 @pytest.mark.parametrize("T", [1, 12, 40])
-def test_tree_attn_listed_heads(dv, dtype, T):
+def test_tree_attn_listed_heads(dv, variant, dtype, T):
     """Only the listed KV heads are computed; repeated and bad entries do no harm."""
+    skip_same(variant, dtype, 64, 2 * T)
     B, Hkv, G, D, cap = 2, 9, 2, 64 if dtype != "f32" else 32, 190
     c = Case(dv, B, Hkv, G, D, cap, dtype, tokens=T)
     lens, q = [120, 77], c.normal(B, T, Hkv * G, D)
@@ -323,8 +338,9 @@ def test_tree_attn_listed_heads(dv, dtype, T):
 @pytest.mark.parametrize("dtype", ["f32", "f16", "i8"])
 @pytest.mark.parametrize("bad", ["nan", "inf", "huge"])
 @pytest.mark.parametrize("T", [6, 24])
-def test_unseen_positions_cannot_change_a_result(dv, dtype, bad, T):
+def test_unseen_positions_cannot_change_a_result(dv, variant, dtype, bad, T):
     """NaN, infinities and huge values behind the last token and in drafted tokens others see."""
+    skip_same(variant, dtype, 64, T)
     B, Hkv, D, cap = 2, 2, 64, 140
     c = Case(dv, B, Hkv, 1, D, cap, dtype, tokens=T, seed=3)
     lens, n_tok = [70, 13], [T - 1, T]
@@ -357,11 +373,12 @@ def test_unseen_positions_cannot_change_a_result(dv, dtype, bad, T):
                 assert not np.isfinite(got[b, t]).all(-1).any()
 
 
-def test_tree_attn_wide_range(dv):
+@pytest.mark.parametrize("T", [3, 20])
+def test_tree_attn_wide_range(dv, variant, T):
     """Scores far apart, weights that underflow, values of very different size."""
     for dtype in ("f32", "f16", "i8"):
         c = Case(dv, 1, 1, 1, 64, 500, dtype)
-        q = 40 * c.normal(1, 3, 1, 64)
+        q = 40 * c.normal(1, T, 1, 64)
         size = 10.0 ** c.rng.uniform(-3, 3, (1, 1, 500, 1))
         v = (c.ref.values("v") * size).astype(np.float32)
         if dtype == "i8":
@@ -369,24 +386,38 @@ def test_tree_attn_wide_range(dv):
         else:
             c.ref.raw["v"] = v.astype(c.ref.raw["v"].dtype)
         c.upload()
-        out = torch.zeros(1, 3, 1, 64, device="cuda")
-        dv.dv_tree_attn(c.cache, torch.from_numpy(q).cuda(), i32([497]), out, c.ws)
+        out = torch.zeros(1, T, 1, 64, device="cuda")
+        dv.dv_tree_attn(c.cache, torch.from_numpy(q).cuda(), i32([500 - T]), out, c.ws)
         c.ok()
-        close(out, *kv_ref.tree(c.ref, q, [497], [3], None, 0.125))
+        close(out, *kv_ref.tree(c.ref, q, [500 - T], [T], None, 0.125))
 
 
-def test_tree_attn_one_long_row_among_short_ones(dv):
+@pytest.mark.parametrize("T,dtype", [(3, "i8"), (11, "i8"), (11, "f16")])
+def test_tree_attn_one_long_row_among_short_ones(dv, variant, T, dtype):
     """Units cut over many CTAs, and many units in one, in one call; twice on one workspace."""
+    skip_same(variant, dtype, 128, T)
     B = 40
-    c = Case(dv, B, 2, 1, 128, 5000, "i8", tokens=3)
-    lens = [4990] + [b % 7 for b in range(1, B)]
-    q = c.normal(B, 3, 2, 128)
-    out = torch.zeros(B, 3, 2, 128, device="cuda")
+    c = Case(dv, B, 2, 1, 128, 5000, dtype, tokens=T)
+    lens = [4980] + [b % 7 for b in range(1, B)]
+    q = c.normal(B, T, 2, 128)
+    out = torch.zeros(B, T, 2, 128, device="cuda")
     for _ in range(2):
         out.fill_(1.0)
         dv.dv_tree_attn(c.cache, torch.from_numpy(q).cuda(), i32(lens), out, c.ws)
         c.ok()
-        close(out, *kv_ref.tree(c.ref, q, lens, [3] * B, None, 128 ** -0.5))
+        close(out, *kv_ref.tree(c.ref, q, lens, [T] * B, None, 128 ** -0.5))
+
+
+def test_tree_attn_rules_choose_both_kernels(dv):
+    """Sizes on both sides of the launch rule, without a forced variant."""
+    for dtype, T, Hkv, cap in (("f16", 30, 8, 1500), ("i8", 64, 12, 1100), ("i8", 12, 2, 300)):
+        c = Case(dv, 6, Hkv, 1, 128, cap, dtype, tokens=T)
+        lens = [cap - T - 97 * b if cap > 1000 else 40 * b for b in range(6)]
+        q = c.normal(6, T, Hkv, 128)
+        out = torch.zeros(q.shape, device="cuda")
+        dv.dv_tree_attn(c.cache, torch.from_numpy(q).cuda(), i32(lens), out, c.ws)
+        c.ok()
+        close(out, *kv_ref.tree(c.ref, q, lens, [T] * 6, None, 128 ** -0.5))
 
 
 # ------------------------------------------------------------------ selected blocks
@@ -460,7 +491,7 @@ def test_block_topk_ties_and_extremes(dv):
 
 
 @pytest.mark.parametrize("dtype,D", [("i8", 128), ("f16", 64), ("f32", 32)])
-def test_a_speculative_decode(dv, dtype, D):
+def test_a_speculative_decode(dv, variant, dtype, D):
     """Prompt, then rounds of draft, tree attention, keep, and block-sparse decode of one token."""
     B, Hkv, G, T, block, cap = 3, 2, 2, 9, 16, 300
     c = Case(dv, B, Hkv, G, D, cap, dtype, block, tokens=T, seed=9)
@@ -500,7 +531,7 @@ def test_a_speculative_decode(dv, dtype, D):
     c.ok()
 
 
-def test_one_workspace_for_several_shapes(dv):
+def test_one_workspace_for_several_shapes(dv, variant):
     """Calls of different shapes, one after another, leave the workspace ready for each other."""
     big = Case(dv, 4, 4, 1, 128, 700, "i8", tokens=64)
     small = Case(dv, 2, 8, 4, 64, 900, "f16", 32, seed=1)
@@ -569,7 +600,7 @@ def test_graph_replay_and_side_stream(dv):
     c.ok()
 
 
-def test_results_repeat(dv):
+def test_results_repeat(dv, variant):
     """The same call twice gives the same bits (units cut over CTAs merge in a fixed order)."""
     c = Case(dv, 2, 3, 2, 128, 3000, "f16", 64, tokens=20)
     q = torch.from_numpy(c.normal(2, 20, 6, 128)).cuda()
@@ -578,6 +609,25 @@ def test_results_repeat(dv):
         dv.dv_tree_attn(c.cache, q, i32([2900, 1234]), o, c.ws)
     c.ok()
     assert all(torch.equal(out[0], o) for o in out[1:])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "i8"])
+def test_cold_calls_equal_warm_ones(dv, variant, dtype):
+    """The first call on a cache whose lines are in no cache, bit for bit as later ones: hand-overs
+    inside the kernels must not depend on how long a load takes."""
+    T = 11 if variant == 2 else 5
+    flush = torch.empty(1 << 28, dtype=torch.int8, device="cuda")
+    for seed in range(4):
+        c = Case(dv, 40, 2, 1, 128, 3000, dtype, tokens=T, seed=seed)
+        lens = i32([2900] + [(b * 37) % 200 for b in range(1, 40)])
+        q = torch.from_numpy(c.normal(40, T, 2, 128)).cuda()
+        out = [torch.zeros(40, T, 2, 128, device="cuda") for _ in range(4)]
+        for i, o in enumerate(out):
+            if i < 3:
+                flush.fill_(i)
+            dv.dv_tree_attn(c.cache, q, lens, o, c.ws)
+        c.ok()
+        assert all(torch.equal(out[3], o) for o in out)
 
 
 def test_offsets_beyond_32_bits(dv):

@@ -152,6 +152,16 @@ def test_wrappers_refuse_host_tensors(dv):
         dv.KvCache(dv.make_kv_desc(8, 3, 32, 64, dv.DV_F32), 1, tensors={})
 
 
+def test_tree_kernel_variant_switch(dv):
+    """Host-only: the variant switch accepts 0, 1 and 2 and refuses the rest."""
+    for bad in (-1, 3):
+        with pytest.raises(dv.DvError) as e:
+            dv.dv_set_tree_kernel(bad)
+        assert e.value.status == dv.DV_ERR_INVALID_ARG
+    for ok in (1, 2, 0):
+        dv.dv_set_tree_kernel(ok)
+
+
 # ------------------------------------------------------------------ the host forms themselves
 
 
