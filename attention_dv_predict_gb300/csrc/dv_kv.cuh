@@ -87,9 +87,8 @@ DV_DEV float quant_inv(float s)  // (s lies in [2^-126, 2^121]: no subnormals)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
     return fmaf(inv, fmaf(-s, inv, 1.f), inv);
 }
-// Four values: their codes' bytes; HELD: x becomes the values as stored.
-template <bool HELD>
-DV_DEV unsigned quant4(float *x, float s, float inv)
+// Four values: their codes' bytes.
+DV_DEV unsigned quant4(const float *x, float s, float inv)
 {
     float u[4], d[4];
 #pragma unroll
@@ -103,14 +102,8 @@ DV_DEV unsigned quant4(float *x, float s, float inv)
             if (fabsf(d[i]) > 0.5f - 0x1p-15f)
                 u[i] = code_at_half(x[i], s, x[i] * inv) + kMagic;
     }
-    const unsigned w = low_bytes(__float_as_uint(u[0]), __float_as_uint(u[1]),
-                                 __float_as_uint(u[2]), __float_as_uint(u[3]));
-    if (HELD) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            x[i] = __fmul_rn(u[i] - kMagic, s);
-    }
-    return w;
+    return low_bytes(__float_as_uint(u[0]), __float_as_uint(u[1]), __float_as_uint(u[2]),
+                     __float_as_uint(u[3]));
 }
 
 // Pairs of codes as binary16: a code's byte with its sign bit flipped is
@@ -232,7 +225,7 @@ DV_DEV void store_mean(const KvCacheArgs &c, size_t row, const int (&acc)[EPC], 
         unsigned *dst = reinterpret_cast<unsigned *>(c.mean + row * c.D + part * EPC);
 #pragma unroll
         for (int e = 0; e < EPC / 4; ++e)
-            dst[e] = fine ? quant4<false>(mean + 4 * e, s, inv) : 0u;
+            dst[e] = fine ? quant4(mean + 4 * e, s, inv) : 0u;
         if (part == 0)
             c.mean_scale[row] = fine ? s : INFINITY;
     }

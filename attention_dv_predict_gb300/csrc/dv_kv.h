@@ -16,6 +16,7 @@
 namespace dv {
 
 constexpr int kKvTile = 64;        // cached positions per attention tile
+constexpr int kKvWriteTile = 256;  // positions per CTA of dv_kv_append: a multiple of every block
 constexpr int kKvMaxCtas = 608;    // attention CTAs (four per SM of 152); sizes the records
 constexpr int kKvGenRows = 4;      // query rows per unit of the CUDA-core attention kernel
 constexpr int kKvMaxBlocks = 16384;  // selectable blocks per row (scores in shared memory)
@@ -44,7 +45,7 @@ struct KvAppendArgs {
     KvRowsArgs k, v;
     const int32_t *lens, *n_tok;
     int B, T;
-    int tile;              // positions per CTA (the block, or kKvTile)
+    int tile;              // positions per CTA (kKvWriteTile)
     int *status;
 };
 

@@ -188,7 +188,7 @@ int dv_kv_append(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_r
         return DV_ERR_INVALID_ARG;
     if ((s = check_ws(*desc, 1, ws, ws_bytes)))
         return s;
-    a.tile = desc->block ? desc->block : kKvTile;
+    a.tile = kKvWriteTile;
     if (!grid_ok((long long)batch * desc->n_kv_heads * ((tokens - 2) / a.tile + 2)))
         return DV_ERR_UNSUPPORTED;
     a.lens = lens;

@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kTopkThreads) k_kv_topk(const KvTopkArgs a)
     const float s = quant_scale(block_amax(fabsf(x), red));
     if (tid < D) {
         float v[4] = {x, 0.f, 0.f, 0.f};
-        qc[tid] = s == s ? (int8_t)quant4<false>(v, s, quant_inv(s)) : (int8_t)0;
+        qc[tid] = s == s ? (int8_t)quant4(v, s, quant_inv(s)) : (int8_t)0;
     }
     __syncthreads();
     // scores of the blocks that are not taken anyway (complete ones: the

@@ -6,7 +6,7 @@
 namespace dv {
 namespace {
 
-constexpr int kWriteThreads = 256;
+constexpr int kWriteThreads = 256;  // (dv_kv_append: 128 for up to 64 rows)
 constexpr int kReadRows = 2;  // rows a thread of dv_kv_read has in flight
 
 // Count of new tokens of row b, 0 and a recorded fault where its position or
@@ -62,9 +62,8 @@ DV_DEV void ld_rows(const void *p, float (&x)[VEC])
 
 // VEC values of a row into the cache at p; a row is spread over lpr lanes
 // (all of them call it, `on` or not).  Returns the row's scale (DV_I8).
-// HELD: x becomes the values as stored.
-template <int VEC, int DT, bool HELD>
-DV_DEV float write_row(float (&x)[VEC], typename Store<DT>::T *p, int lpr, bool on)
+template <int VEC, int DT>
+DV_DEV float write_row(const float (&x)[VEC], typename Store<DT>::T *p, int lpr, bool on)
 {
     if constexpr (DT == DV_I8) {
         float mx = amax_of(x);
@@ -75,7 +74,7 @@ DV_DEV float write_row(float (&x)[VEC], typename Store<DT>::T *p, int lpr, bool 
         unsigned w[VEC / 4];
 #pragma unroll
         for (int i = 0; i < VEC / 4; ++i) {
-            w[i] = quant4<HELD>(x + 4 * i, s, inv);  // (NaN where the row is not finite)
+            w[i] = quant4(x + 4 * i, s, inv);  // (NaN where the row is not finite)
             w[i] = s == s ? w[i] : 0u;
         }
         if (on) {
@@ -91,11 +90,6 @@ DV_DEV float write_row(float (&x)[VEC], typename Store<DT>::T *p, int lpr, bool 
         for (int i = 0; i < VEC / 2; ++i) {
             const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
             w[i] = *reinterpret_cast<const unsigned *>(&h);
-            if (HELD) {
-                const float2 f = __half22float2(h);
-                x[2 * i] = f.x;
-                x[2 * i + 1] = f.y;
-            }
         }
         if (on) {
             if constexpr (VEC == 16) {
@@ -116,15 +110,15 @@ DV_DEV float write_row(float (&x)[VEC], typename Store<DT>::T *p, int lpr, bool 
 // One side (0 keys, 1 values) of the `rows` new rows of a tile: the given rows
 // from token t0 of (b, h) on go to the cache rows from row0 on, by the threads
 // from `first` on.  A row is spread over D / VEC lanes, and a lane group has
-// UR rows in flight.  HELD: x holds the last pass's values as stored.
-template <int VEC, int DT, bool F16, bool HELD, int UR>
+// UR rows in flight.
+template <int VEC, int DT, bool F16, int UR, int NTHR>
 DV_DEV void write_side(const KvAppendArgs &a, int side, int first, int b, int h, int t0, int rows,
                        size_t row0, float (&x)[UR][VEC])
 {
     using T = typename Store<DT>::T;
     const KvCacheArgs &c = a.c;
     const int lpr = c.D / VEC, part = threadIdx.x % lpr;
-    const int groups = (kWriteThreads - first) / lpr, group = (threadIdx.x - first) / lpr;
+    const int groups = (NTHR - first) / lpr, group = (threadIdx.x - first) / lpr;
     const KvRowsArgs &src = side ? a.v : a.k;
     const size_t es = F16 ? 2 : 4;
     const char *from = static_cast<const char *>(src.p) +
@@ -142,18 +136,17 @@ DV_DEV void write_side(const KvAppendArgs &a, int side, int first, int b, int h,
 #pragma unroll
         for (int i = 0; i < UR; ++i) {
             const int u = u0 + i * groups;
-            const float s = write_row<VEC, DT, HELD>(x[i], to + (size_t)u * c.D, lpr, u < rows);
+            const float s = write_row<VEC, DT>(x[i], to + (size_t)u * c.D, lpr, u < rows);
             if (DT == DV_I8 && u < rows && part == 0)
                 scale[u] = s;
         }
     }
 }
 
-// One CTA owns the positions of one aligned tile (a block, where means are
-// kept) of one (row, KV head): it writes the new tokens that fall into it
-// and, when the tile's last position is among them, the block's mean.
-template <int VEC, int DT, bool F16>
-__global__ void __launch_bounds__(kWriteThreads, 4) k_kv_append(const KvAppendArgs a)
+// One CTA owns the positions of one aligned tile of one (row, KV head): it writes the new tokens that fall into it and the means
+// of the blocks that they complete.
+template <int VEC, int DT, bool F16, int NTHR>
+__global__ void __launch_bounds__(NTHR, 1024 / NTHR) k_kv_append(const KvAppendArgs a)
 {
     constexpr int UR = VEC == 16 ? 2 : 4;
     const KvCacheArgs &c = a.c;
@@ -167,73 +160,24 @@ __global__ void __launch_bounds__(kWriteThreads, 4) k_kv_append(const KvAppendAr
     const int lo = max(len, tile * a.tile), hi = min(len + n, (tile + 1) * a.tile);
     if (lo >= hi)
         return;
-    const int lpr = c.D / VEC, part = threadIdx.x % lpr, rows = hi - lo;
+    const int rows = hi - lo;
     const size_t bh = (size_t)b * c.Hkv + h, row0 = bh * (size_t)c.cap + lo;
-    const bool mean = c.block && hi == (tile + 1) * a.tile;
     float x[UR][VEC];
-    if (VEC == 16 && mean && rows == c.block && rows <= UR * (kWriteThreads / lpr)) {
-        // a whole new block, one pass of the CTA: its mean from the registers
-        __shared__ int s_max, s_sum[256];
-        for (int d = threadIdx.x; d < c.D; d += kWriteThreads)
-            s_sum[d] = 0;
-        if (threadIdx.x == 0)
-            s_max = 0;
+    write_side<VEC, DT, F16, UR, NTHR>(a, 0, 0, b, h, lo - len, rows, row0, x);
+    // blocks whose last position is among the new ones: up to half of the warps
+    // take their means from the cache while the others write the values
+    const int j0 = c.block ? lo / c.block : 0, means = c.block ? hi / c.block - j0 : 0;
+    const int takers = min(means, NTHR / 64);
+    if (means > 0) {
         __syncthreads();
-        write_side<VEC, DT, F16, true>(a, 0, 0, b, h, lo - len, rows, row0, x);
-        float mx = 0.f;
-#pragma unroll
-        for (int i = 0; i < UR; ++i)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if ((int)(threadIdx.x / lpr) + i * (kWriteThreads / lpr) >= rows)
-                    x[i][e] = 0.f;
-#pragma unroll
-        for (int i = 0; i < UR; ++i)
-            mx = amax_of(x[i], mx);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            mx = amax2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if ((threadIdx.x & 31) == 0)  // (non-negative numbers, infinity and NaN in this order)
-            atomicMax(&s_max, __float_as_int(mx));
-        __syncthreads();
-        const float top = __int_as_float(s_max);
-        const bool fine = top <= 3.402823466e38f;
-        const int e2 = mean_exponent(fine ? top : 0.f);
-        const float inv = ldexpf(1.f / c.block, 24 - e2);
-        if (fine) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                int acc = 0;
-#pragma unroll
-                for (int i = 0; i < UR; ++i)
-                    acc += mean_units(x[i][e], inv);
-                for (int o = lpr; o < 32; o <<= 1)
-                    acc += __shfl_xor_sync(0xffffffffu, acc, o);
-                if ((int)(threadIdx.x & 31) < lpr)
-                    atomicAdd(&s_sum[part * VEC + e], acc);
-            }
+        const int warp = threadIdx.x >> 5;
+        if (warp < takers) {
+            for (int j = warp; j < means; j += takers)
+                warp_mean<DT>(c, bh, j0 + j);
+            return;
         }
-        __syncthreads();
-        if (threadIdx.x < 32) {
-            int acc[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                acc[e] = s_sum[part * VEC + e];
-            store_mean<VEC>(c, bh * (size_t)(c.cap / c.block) + tile, acc, e2, fine, part, lpr);
-        }
-        write_side<VEC, DT, F16, false>(a, 1, 0, b, h, lo - len, rows, row0, x);
-        return;
     }
-    write_side<VEC, DT, F16, false>(a, 0, 0, b, h, lo - len, rows, row0, x);
-    if (mean) {  // warp 0 takes the mean from the cache while the others write the values
-        __syncthreads();
-        if (threadIdx.x < 32)
-            warp_mean<DT>(c, bh, tile);
-        else
-            write_side<VEC, DT, F16, false>(a, 1, 32, b, h, lo - len, rows, row0, x);
-    } else {
-        write_side<VEC, DT, F16, false>(a, 1, 0, b, h, lo - len, rows, row0, x);
-    }
+    write_side<VEC, DT, F16, UR, NTHR>(a, 1, 32 * takers, b, h, lo - len, rows, row0, x);
 }
 
 // VEC cached values as numbers, without their scale.
@@ -389,11 +333,11 @@ __global__ void __launch_bounds__(kWriteThreads) k_kv_keep(const KvKeepArgs a)
 }
 
 template <class K, class A>
-cudaError_t launch(K kern, dim3 grid, const A &a, cudaStream_t st)
+cudaError_t launch(K kern, dim3 grid, const A &a, cudaStream_t st, int threads = kWriteThreads)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kWriteThreads);
+    cfg.blockDim = dim3(threads);
     cfg.stream = st;
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
@@ -401,8 +345,13 @@ cudaError_t launch(K kern, dim3 grid, const A &a, cudaStream_t st)
 template <int VEC, int DT>
 cudaError_t append_src(const KvAppendArgs &a, dim3 grid, cudaStream_t st)
 {
-    return a.k.f16 ? launch(k_kv_append<VEC, DT, true>, grid, a, st)
-                   : launch(k_kv_append<VEC, DT, false>, grid, a, st);
+    // a CTA's rows: more CTAs of fewer threads where they are few
+    const int rows = a.T < a.tile ? a.T : a.tile;
+    if (rows <= 64)
+        return a.k.f16 ? launch(k_kv_append<VEC, DT, true, 128>, grid, a, st, 128)
+                       : launch(k_kv_append<VEC, DT, false, 128>, grid, a, st, 128);
+    return a.k.f16 ? launch(k_kv_append<VEC, DT, true, 256>, grid, a, st, 256)
+                   : launch(k_kv_append<VEC, DT, false, 256>, grid, a, st, 256);
 }
 
 // (rows of fewer than 16 values are binary32 or binary16 ones)

@@ -427,7 +427,7 @@ def test_tree_attn_rules_choose_both_kernels(dv):
 @pytest.mark.parametrize("Hkv,G,D,block,k,first,last,cap", [
     (3, 1, 128, 64, 4, 1, 1, 1000), (2, 4, 128, 32, 9, 0, 2, 777), (2, 1, 64, 16, 20, 2, 1, 2000),
     (1, 2, 64, 128, 3, 1, 1, 900), (2, 1, 32, 16, 2, 1, 1, 400), (1, 1, 128, 16, 30, 0, 1, 9000),
-    (1, 1, 128, 64, 1, 0, 1, 300),
+    (1, 1, 128, 64, 1, 0, 1, 300), (1, 1, 32, 16, 40, 1, 1, 20000),
 ])
 def test_block_topk_and_attn(dv, dtype, Hkv, G, D, block, k, first, last, cap):
     B = 5
