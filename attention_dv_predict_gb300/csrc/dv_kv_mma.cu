@@ -59,6 +59,7 @@ struct Cfg {
     static constexpr int QF = KS * 32 * 16;
     static constexpr int SO = RM * D * 4;
     static constexpr size_t SMEM = 1024 + (size_t)RING + SCALES + QF + SO;
+    static constexpr int FLUSH = 64;  // tiles whose values the tensor cores sum
     static_assert(PW == 16, "one k step of the value product");
 };
 
@@ -211,6 +212,13 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
         for (int i = 0; i < NT; ++i)
             o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         float m = -INFINITY, l = 0.f;  // reference point, sum
+        // Tensor cores cut their sums off instead of rounding them: every step
+        // takes up to 2^-23 of a value, always towards zero.  So the values of
+        // FLUSH tiles at a time are added here in binary32 (in local memory,
+        // on purpose: as registers they would cost a CTA per SM).
+        volatile float acc[NT * 2 + 1];  // values; sum
+        int steps = 0;
+        bool flushed = false;
 
         for (w = tile_place(x, w); w < wend; ++w) {
             if (C::I8)
@@ -323,6 +331,10 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
                     o[i][2] *= f;
                     o[i][3] *= f;
                 }
+                if (flushed)
+#pragma unroll
+                    for (int i = 0; i <= 2 * NT; ++i)
+                        acc[i] = acc[i] * f;
             }
             l += sum;
             unsigned hh[2], ll[2];
@@ -399,11 +411,26 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
                 if (bad & seen)
                     l = __int_as_float(0x7fc00000);  // the row's result is NaN
             }
+            if (++steps == C::FLUSH) {
+                steps = 0;
+#pragma unroll
+                for (int i = 0; i < 2 * NT; ++i) {
+                    float *p = o[i >> 1];
+                    const float val = p[i & 1] + p[2 + (i & 1)];
+                    acc[i] = flushed ? acc[i] + val : val;
+                    p[i & 1] = p[2 + (i & 1)] = 0.f;
+                }
+                acc[2 * NT] = flushed ? acc[2 * NT] + l : l;
+                l = 0.f;
+                flushed = true;
+            }
         }
         if (x.h < 0)
             continue;
 
         // ---- merge the warps
+        if (flushed)
+            l += acc[2 * NT];
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         if (t == 0) {
@@ -433,7 +460,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         float *q = so + (n * 2 + c) * 32 + lane;
-                        const float val = (o[n][c] + o[n][2 + c]) * fac;
+                        const float sum = o[n][c] + o[n][2 + c];
+                        const float val = (flushed ? acc[2 * n + c] + sum : sum) * fac;
                         *q = i ? *q + val : val;
                     }
             }

@@ -9,7 +9,7 @@
 // equal runs: CTA c the places [W c / C, W (c + 1) / C), an end among a
 // unit's empty places counting as the unit's start.  (Without them a ragged
 // batch's short rows all fell to a few CTAs: 32 rows of 1 to 8000 positions,
-// 48 blocks of 32 for each of 64 heads, 420 us against 230.)  A unit inside
+// 48 blocks of 32 for each of 64 heads, 420 us against 188.)  A unit inside
 // one run is finished by its CTA; a unit cut by a run's end leaves a piece
 // (max m, sum l, weighted values o, per row) in a record, and the last of its
 // CTAs to arrive merges the pieces in the order of the positions, so the

@@ -545,12 +545,14 @@ int dv_kv_keep(const dv_kv_desc *desc, const dv_kv_cache *cache, int batch, int 
  *   as they were.  A position that a token does not see cannot change its
  *   result, whatever it holds; a value row that it sees and that holds a NaN
  *   or an infinity makes the result non-finite.
- *   u_h, n_u_h, max_u_h: device list of KV heads to compute, as
+ *   u_h, n_u_h, max_u_h: device list of distinct KV heads to compute, as
  *   dv_sparse_attn's (NULL, NULL, 0: every head; max_u_h <= n_kv_heads).
  * tokens = 1 is decode attention with one length a row.  Scores, weights and
  * sums are binary32 to its last bits for every cache type: on tensor cores
- * queries and weights are split into two binary16 parts.  One launch; the
- * order of every sum is fixed by the shapes and lengths.
+ * queries and weights are split into two binary16 parts, and no more than
+ * 128 of their steps, which cut sums off, come between binary32 additions.
+ * One launch; the order of every sum is fixed by the shapes, the lengths and
+ * the device.
  */
 int dv_tree_attn(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_rows *q, int batch,
                  int tokens, const int32_t *lens, const int32_t *n_tok, const uint64_t *mask,

@@ -630,6 +630,55 @@ def test_cold_calls_equal_warm_ones(dv, variant, dtype):
         assert all(torch.equal(out[3], o) for o in out)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "i8"])
+@pytest.mark.parametrize("T", [2, 9, 64])
+@pytest.mark.parametrize("rise", [0.0, 200.0], ids=["flat", "rising"])
+def test_tree_attn_very_long_rows(dv, variant, dtype, T, rise):
+    """100000 positions, so many heads that a CTA attends whole rows: sums of thousands of steps.
+
+    Values lie in [1, 2), so a sum cut off at every step shows as a bias.  At most 64 tiles of 64
+    (two streams of 32 tiles of 4 steps, or 64 steps) are summed by tensor cores, each step off by
+    less than 2^-23 of the sum: 128 of them; sums of up to 64 further roundings; the quotient.
+    (3000 steps of a row summed without a limit would lose 3000 x 2^-23 / 6.)  Scores that rise by
+    200 move the reference point from chunk to chunk; a score has the rounding of its 64 products'
+    sum, 2^-21 of its size, and a weight that times log2(e)."""
+    Hkv, D, cap = 160, 64, 100100
+    desc = dv.make_kv_desc(Hkv, Hkv, D, cap, DT[dtype])
+    g = torch.Generator(device="cuda").manual_seed(T)
+    cache = dv.KvCache(desc, 1)
+    n = cap - T - 3
+    pos = torch.arange(cap, device="cuda") / n
+    if dtype == "f16":
+        cache.k.normal_(generator=g).mul_(0.25)
+        cache.k[..., 0] = pos
+        cache.v.uniform_(1, 2, generator=g)
+    else:
+        cache.k.random_(-100, 101, generator=g)
+        cache.k[..., 0] = (100 * pos).round().clamp(max=100).to(torch.int8)
+        cache.v.random_(64, 128, generator=g)
+        cache.k_scale.fill_(2.0 ** -8)
+        cache.v_scale.fill_(2.0 ** -6)
+    ws = dv.KvWorkspace(desc, 1, T)
+    q = torch.randn(1, T, Hkv, D, generator=g, device="cuda")
+    top = cache.k[0, 0, n - 1, 0].double() * (1 if dtype == "f16" else 2.0 ** -8)
+    q[..., 0] = rise * D ** 0.5 / top.item()
+    out = torch.zeros(1, T, Hkv, D, device="cuda")
+    dv.dv_tree_attn(cache, q, i32([n]), out, ws)
+    assert dv.dv_check(ws) == 0
+    j = torch.arange(n + T, device="cuda")
+    seen = j[None] <= n + torch.arange(T, device="cuda")[:, None]
+    for h in (0, 77, Hkv - 1):
+        k, v = cache.k[0, h, :n + T].double(), cache.v[0, h, :n + T].double()
+        if dtype == "i8":
+            k, v = k * 2.0 ** -8, v * 2.0 ** -6
+        s = (q[0, :, h].double() @ k.T * D ** -0.5).masked_fill(~seen, -torch.inf)
+        want = s.softmax(-1) @ v
+        size = (q[0, :, h].double().abs() @ k.abs().T * D ** -0.5).max().item()
+        tol = 2 * (192 * 2.0 ** -23 + 2 * size * 2.0 ** -21)
+        err = (out[0, :, h].double() - want).abs().max().item()
+        assert err <= tol, f"off by {err:.3g}, allowed {tol:.3g}"
+
+
 def test_offsets_beyond_32_bits(dv):
     """A cache of more than 2^32 values a side: its last row and head."""
     B, Hkv, D, cap, T = 3, 8, 128, (1 << 21) - 77, 4
