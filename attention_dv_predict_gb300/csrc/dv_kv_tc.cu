@@ -9,8 +9,9 @@
 // 64-position tile of 128 dimensions take 619 tensor cycles (measured alone:
 // 384 and 256), mma.sync 2048.  64-token trees of 32 rows at the 175B shape,
 // 2048 positions: binary16 576 us, where the cache's bytes alone take 519;
-// 8 bits 724 us, where those take 282 and the tensor products 660, bound by
-// the products and by the hand-overs between the roles.
+// 8 bits 724 us, where those take 282 and the tensor products 220: there the
+// 16 softmax and 8 conversion warps bound it, which fill 0.6 of the issue slots
+// and wait for one another's hand-overs in the rest.
 //
 // Warps of a CTA (one CTA per SM):
 //   0-15      softmax: two streams that take turns at the tiles, each with its
