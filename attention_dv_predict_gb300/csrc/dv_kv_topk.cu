@@ -13,7 +13,9 @@
 // of the 8-bit keys at blocks of 64) are read once with 16-byte loads and
 // multiplied four codes at a time (dp4a); the scores stay in shared memory
 // as order-preserving keys, and four 8-bit digits of a radix selection find
-// the k-th.
+// the k-th.  32 rows of up to 8000 positions in blocks of 32, 64 heads: 25 us,
+// 512 blocks in one CTA 12 us, both bound by the passes' barriers (one warp a
+// row without any took 32 and 45 us for the former).
 #include "dv_kv.cuh"
 
 namespace dv {
