@@ -679,6 +679,41 @@ def test_tree_attn_very_long_rows(dv, variant, dtype, T, rise):
         assert err <= tol, f"off by {err:.3g}, allowed {tol:.3g}"
 
 
+@pytest.mark.parametrize("dtype", ["f16", "i8"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tree_attn_many_long_rows(dv, variant, dtype, D):
+    """Several whole rows of more than 64 tiles in every CTA's run, cut ones between them; rows of
+    other batch entries end in other tiles, one is empty.  Tolerance as above."""
+    B, Hkv, T, cap = 5, 128, 9, 5200
+    desc = dv.make_kv_desc(Hkv, Hkv, D, cap, DT[dtype])
+    g = torch.Generator(device="cuda").manual_seed(D)
+    cache = dv.KvCache(desc, B)
+    for t in (cache.k, cache.v):
+        t.random_(-100, 101, generator=g)
+    if dtype == "i8":
+        cache.k_scale.fill_(2.0 ** -6)
+        cache.v_scale.fill_(2.0 ** -6)
+    else:
+        cache.k.mul_(2.0 ** -6)
+        cache.v.mul_(2.0 ** -6)
+    lens = [cap - T, 4999, 4096, 0, 4160 - T]
+    ws = dv.KvWorkspace(desc, B, T)
+    q = torch.randn(B, T, Hkv, D, generator=g, device="cuda")
+    out = torch.full((B, T, Hkv, D), 7.0, device="cuda")
+    dv.dv_tree_attn(cache, q, i32(lens), out, ws)
+    assert dv.dv_check(ws) == 0
+    unit = 2.0 ** -6 if dtype == "i8" else 1.0
+    for b, n in enumerate(lens):
+        k, v = (t[b, :, :n + T].double() * unit for t in (cache.k, cache.v))
+        s = torch.einsum("thd,hpd->htp", q[b].double(), k) * D ** -0.5
+        size = torch.einsum("thd,hpd->htp", q[b].double().abs(), k.abs()).max().item() * D ** -0.5
+        j, t = torch.arange(n + T, device="cuda"), torch.arange(T, device="cuda")
+        want = s.masked_fill(j > n + t[:, None], -torch.inf).softmax(-1) @ v
+        tol = 2 * (192 * 2.0 ** -23 + 2 * size * 2.0 ** -21)
+        err = (out[b].double().transpose(0, 1) - want).abs().max().item()
+        assert err <= tol, f"row {b} off by {err:.3g}, allowed {tol:.3g}"
+
+
 def test_offsets_beyond_32_bits(dv):
     """A cache of more than 2^32 values a side: its last row and head."""
     B, Hkv, D, cap, T = 3, 8, 128, (1 << 21) - 77, 4
