@@ -316,17 +316,16 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
             const bool range = big <= kWeightMax && sum <= kSumMax && m != -INFINITY;
             if (!__all_sync(0xffffffffu, range)) {  // first weights, or one out of range: rare
                 const float top = quad_max(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
-                float mn = ref_from_scores(m, top);
-                weights(mn == -INFINITY ? 0.f : mn);
-                const float k = ref_shift(m == -INFINITY, quad_max(big)), g2 = ex2(-k);
-                mn += k;
+                const float m0 = ref_from_scores(m, top);
+                weights(m0 == -INFINITY ? 0.f : m0);
+                const float mn = ref_new(m, m0, quad_max(big)), g2 = pow2(m0 - mn);
                 sum *= g2;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     p[e] *= g2;
-                const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+                const float d = mn == -INFINITY ? 0.f : m - mn, f = pow2(d);
                 m = mn;
-                l *= f;
+                l = times_pow2(l, d);
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     o[i][0] *= f;
@@ -334,10 +333,12 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
                     o[i][2] *= f;
                     o[i][3] *= f;
                 }
-                if (flushed)
+                if (flushed) {
 #pragma unroll
-                    for (int i = 0; i <= 2 * NT; ++i)
+                    for (int i = 0; i < 2 * NT; ++i)
                         acc[i] = acc[i] * f;
+                    acc[2 * NT] = times_pow2(acc[2 * NT], d);
+                }
             }
             l += sum;
             unsigned hh[2], ll[2];
@@ -446,12 +447,12 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
         for (int i = 0; i < WP; ++i)
             M = fmaxf(M, s_m[i][g]);
         const float ms = M == -INFINITY ? 0.f : M;
-        const float fac = ex2(m - ms);
+        const float fac = pow2(m - ms);
         if (warp == 0 && t == 0) {
             float L = 0.f;
 #pragma unroll
             for (int i = 0; i < WP; ++i)
-                L += s_l[i][g] * ex2(s_m[i][g] - ms);
+                L += times_pow2(s_l[i][g], s_m[i][g] - ms);
             u_m[g] = M;
             u_l[g] = L;
         }

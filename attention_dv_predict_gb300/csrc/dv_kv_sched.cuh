@@ -225,6 +225,13 @@ DV_DEV int block_pos(const KvAttnArgs &a, const Unit &x, int i)
     return p < x.len ? p : -1;
 }
 
+// l 2^d, also where l is large and 2^d below binary32's range (the references of
+// pieces whose value scales lie far apart).
+DV_DEV float sum_shift(float l, float d)
+{
+    return l * exp2f(fmaxf(d, -120.f)) * exp2f(fminf(d + 120.f, 0.f));
+}
+
 // o / l by the reciprocal (one more rounding); 0 where nothing was seen.
 DV_DEV float4 row_result(const float4 &o, float l)
 {
@@ -337,7 +344,7 @@ struct Finish {
                     const float *p = piece(k) + RM * D + row;
                     const float m = __ldcg(p), l = __ldcg(p + RM);
                     const float mn = fmaxf(M, m), ms = mn == -INFINITY ? 0.f : mn;
-                    L = L * exp2f(M - ms) + l * exp2f(m - ms);
+                    L = sum_shift(L, M - ms) + sum_shift(l, m - ms);
                     M = mn;
                     if (k < 32)
                         mine = m;
@@ -347,7 +354,7 @@ struct Finish {
                 for (int o = 16; o > 0; o >>= 1)
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 const float ms = top == -INFINITY ? 0.f : top;
-                L = warp_sum(L * exp2f(M - ms));
+                L = warp_sum(sum_shift(L, M - ms));
                 if (lane < kMergePieces)
                     wgt[lane][row] = exp2f(mine - ms);
                 if (lane == 0) {

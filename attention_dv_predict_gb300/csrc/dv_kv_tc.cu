@@ -786,21 +786,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     row_max(big, false);
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const float k2 = ref_shift(m[r] == -INFINITY, big[r]);
-                        const float g2 = ex2(-k2);
-                        mn[r] += k2;
+                        const float m0 = mn[r];
+                        mn[r] = ref_new(m[r], m0, big[r]);
+                        const float g2 = pow2(m0 - mn[r]);
                         sum[r] *= g2;
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             mul2(v[4 * j + 2 * r], v[4 * j + 2 * r + 1], g2, g2);
-                        f[r] = mn[r] == -INFINITY ? 1.f : ex2(m[r] - mn[r]);
+                        const float d = mn[r] == -INFINITY ? 0.f : m[r] - mn[r];
+                        f[r] = pow2(d);
+                        l[r] = times_pow2(l[r], d);
                         m[r] = mn[r];
                     }
                 }
                 unsigned ph[8], pl[8];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    l[r] = fmaf(l[r], f[r], sum[r]);
+                    l[r] += sum[r];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float p = v[4 * j + 2 * r], q = v[4 * j + 2 * r + 1];
@@ -879,7 +881,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int r = 0; r < 2; ++r) {
                 const int row = 16 * ww + g + 8 * r;
                 const float M = fmaxf(s_m[0][row], s_m[1][row]);
-                fac[r] = ex2(m[r] - (M == -INFINITY ? 0.f : M));
+                fac[r] = pow2(m[r] - (M == -INFINITY ? 0.f : M));
             }
             auto load_o = [&](int col, float (&o)[NE]) {
                 float lo[NE];
@@ -929,15 +931,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     continue;
                 float M = fmaxf(s_m[0][row], s_m[1][row]);
                 const float ms = M == -INFINITY ? 0.f : M;
-                float L = (s_l[0][row] + s_l[1][row]) * ex2(s_m[0][row] - ms) +
-                          (s_l[2][row] + s_l[3][row]) * ex2(s_m[1][row] - ms);
+                float L = times_pow2(s_l[0][row] + s_l[1][row], s_m[0][row] - ms) +
+                          times_pow2(s_l[2][row] + s_l[3][row], s_m[1][row] - ms);
                 float *const part = rec + row * D + c0 + sx * QC + 2 * t4;
                 if (!first) {  // what the part's chunks before have left there
                     const float mo = c_m[buf ^ 1][row], top = fmaxf(M, mo);
                     const float ts = top == -INFINITY ? 0.f : top;
-                    const float fn = ex2(M - ts), fo = ex2(mo - ts);
+                    const float fn = pow2(M - ts), fo = pow2(mo - ts);
+                    L = times_pow2(c_l[buf ^ 1][row], mo - ts) + times_pow2(L, M - ts);
                     M = top;
-                    L = fmaf(c_l[buf ^ 1][row], fo, L * fn);
 #pragma unroll
                     for (int j = 0; j < QC / 8; ++j) {
                         const float2 y = __ldcg(reinterpret_cast<const float2 *>(part + 8 * j));

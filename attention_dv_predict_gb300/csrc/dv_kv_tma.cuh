@@ -162,22 +162,38 @@ DV_DEV void fma2(float &a, float &b, float c, float d)  // a c + d, b c + d
 // A softmax row's reference point.  Weights are w_p = 2^(s_p - m) v_p (s: the
 // score in units of log2, v: the value row's scale, 1 in binary16 caches) and
 // l = sum 2^(s_p - m), o = sum w_p value_p, so m cancels from o / l and may be
-// anything that keeps w in binary16's range.  It is set so that a row's first
-// largest weight is between 1 and 2^14, and only raised when one exceeds
-// that: the low parts' last place, 2^-24, stays under the weights' sum times
-// binary32's, and no step needs a row's maximum.  m = -inf: nothing seen yet.
+// anything that keeps w in binary16's range.  It is set by a row's first
+// weights and moves when a weight or a sum leaves its range: the largest weight
+// is then taken to between 2^6 and 2^7, whatever v is.  So the low parts' last
+// place, 2^-24, is 2^-30 of the largest weight for value rows of any size down
+// to scales of 2^-60, where the shift ends (it keeps l finite: 2^66 a position),
+// and no step needs a row's maximum.  (First weights taken to 2^12, nearer to
+// the end of the range, moved more often: 64-token trees of 32 x 96 heads x
+// 2048 8-bit positions 737 us against 687.)  m is a whole number, so that every
+// change of reference scales by a power of two, without an error.  m = -inf:
+// nothing seen yet.
 constexpr float kWeightMax = 16384.f;
-constexpr float kWeightMin = 1.f;  // a row's first weights are shifted if all are smaller
 constexpr float kSumMax = 0x1p100f;  // 2^(s - m) itself must stay finite where v is tiny
-// The new reference for the scores' maximum top (over a row) before weights
-// are known, and its correction from the weights' maximum big under it.
-DV_DEV float ref_from_scores(float m, float top) { return fmaxf(m, top - 6.f); }
-DV_DEV float ref_shift(bool first, float big)
+constexpr float kShiftMin = -60.f;
+// A reference for the scores' maximum top (over a row) before weights are
+// known, and the one to use by the weights' maximum big under it.  Neither is
+// below the reference m before.
+DV_DEV float ref_from_scores(float m, float top) { return fmaxf(m, floorf(top) - 6.f); }
+DV_DEV float ref_new(float m, float m0, float big)
 {
-    if (!(big > 0.f) || !(big <= 3.402823466e38f))
-        return 0.f;
-    const float k = (float)((int)(__float_as_uint(big) >> 23) - 127 - 12);
-    return first ? fmaxf(k, -90.f) : fmaxf(k, 0.f);
+    if (!(big <= 3.402823466e38f))  // (the row's result is not finite)
+        return m0;
+    const int e = (int)(__float_as_uint(big) >> 23) - 127;
+    return fmaxf(m, m0 + fmaxf((float)(e - 6), kShiftMin));
+}
+// 2^d for a whole number d <= 127; 0 below 2^-126 and for NaN (two references
+// of rows that see nothing, or whose result is not finite anyway).
+DV_DEV float pow2(float d) { return d >= -126.f ? __int_as_float(((int)d + 127) << 23) : 0.f; }
+// x 2^d, also where x is large and 2^d below 2^-126: the sums l of rows whose
+// value scales lie far apart (zero rows have 2^-126).
+DV_DEV float times_pow2(float x, float d)
+{
+    return x * pow2(fmaxf(d, -126.f)) * pow2(fminf(d + 126.f, 0.f));
 }
 
 // Four values of a query row, already scaled for the softmax, as binary16 high

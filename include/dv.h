@@ -548,11 +548,16 @@ int dv_kv_keep(const dv_kv_desc *desc, const dv_kv_cache *cache, int batch, int 
  *   u_h, n_u_h, max_u_h: device list of distinct KV heads to compute, as
  *   dv_sparse_attn's (NULL, NULL, 0: every head; max_u_h <= n_kv_heads).
  * tokens = 1 is decode attention with one length a row.  Scores, weights and
- * sums are binary32 to its last bits for every cache type: on tensor cores
- * queries and weights are split into two binary16 parts, and no more than
- * 128 of their steps, which cut sums off, come between binary32 additions.
- * One launch; the order of every sum is fixed by the shapes, the lengths and
- * the device.
+ * sums are held in binary32 for every cache type.  The tensor-core kernels
+ * (binary16 and 8-bit rows of 64 or 128 values) come near a binary32
+ * evaluation, not to its last bit: a query element is two binary16 parts
+ * (exact to 2^-22 of itself, or 2^-38 of its row's largest), a weight (with its
+ * value row's scale) two parts (2^-22 of itself, or 2^-30 of the row's largest),
+ * 2^x has a relative error of up to 2^-22, and up to 128 steps that cut the sum
+ * off (2^-23 each) come between binary32 additions.  This holds for
+ * 8-bit value rows with scales from 2^-60 to 2^100, and rows of zeros among
+ * them; smaller ones lose bits.  One launch; the order of every sum is fixed by
+ * the shapes, the lengths and the device.
  */
 int dv_tree_attn(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_rows *q, int batch,
                  int tokens, const int32_t *lens, const int32_t *n_tok, const uint64_t *mask,

@@ -1,0 +1,118 @@
+"""Attention over a KV cache where its numbers can go wrong, on the GPU: value rows of any size,
+scores that rise, rows that must not depend on one another, NaN and infinities."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import kv_ref
+from test_gpu_kv import Case, close, dv, i32, mask_tensor, random_tree, skip_same, variant  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def half_ulp(x):
+    return 2.0 ** (math.floor(math.log2(x)) - 24)
+
+
+def sized_cache(c, pattern, e, rise, seed):
+    """Fill an 8-bit Case: scores rise by `rise` (units of log2) over the first quarter of the
+    positions for a query of 1 in dimension 0, value scales lie in [2^-e-1, 2^-e), zero rows as
+    dv_kv_append stores them by `pattern`.  Returns keys' dimension 0 and values in 64 bits."""
+    g = np.random.default_rng(seed)
+    shape = (c.B, c.Hkv, c.cap)
+    ramp = np.clip(np.arange(c.cap) / (c.cap / 4), 0, 1) * 200 - 100
+    k0 = np.clip(np.rint(ramp + g.integers(-6, 7, shape)), -127, 127).astype(np.int8)
+    codes = g.integers(64, 128, shape + (c.D,)).astype(np.int8)
+    scale = (g.uniform(0.5, 1, shape) * 2.0 ** -e).astype(np.float32)
+    zero = {"none": np.zeros(c.cap, bool), "first": np.arange(c.cap) < 100,
+            "between": np.arange(c.cap) // 64 % 2 == 0}[pattern]
+    codes[:, :, zero] = 0
+    scale[:, :, zero] = 2.0 ** -126
+    c.cache.k.zero_()
+    c.cache.k[..., 0] = torch.from_numpy(k0).cuda()
+    c.cache.k_scale.fill_(rise / 200)
+    c.cache.v.copy_(torch.from_numpy(codes))
+    c.cache.v_scale.copy_(torch.from_numpy(scale))
+    return (k0 * float(np.float32(rise / 200)), codes * scale[..., None].astype(np.float64))
+
+
+def sized_tolerance(e, rise, steps):
+    """Relative to sum p |v|.  A score, one product, is off by at most 2^-21 of its size (its
+    query's two parts 2^-22, the softmax scale, the product with it, the key's scale and the sum
+    of the parts 2^-24 each).  Its weight's exponent, the score less a reference that takes the
+    values' size too, is below |e| + 2 * rise + 16 and rounded once; ex2.approx, the weight's two
+    parts and the value's scale add 2^-21.  That counts in the numerator and in the sum.  Every
+    step of a tensor-core sum cuts off up to 2^-23."""
+    w = math.log(2) * (rise / 2 * 2.0 ** -21 + half_ulp(abs(e) + 2 * rise + 16)) + 2.0 ** -21
+    return 2 * w + steps * 2.0 ** -23
+
+
+SIZES = [("none", e) for e in (0, 7, 14, 20, 30, 60)] + \
+        [("first", e) for e in (-90, 0, 30)] + [("between", e) for e in (-90, -30, 8, 50)]
+
+
+@pytest.mark.parametrize("pattern,e", SIZES)
+@pytest.mark.parametrize("T,D,cap", [(3, 128, 1000), (3, 64, 6000), (12, 64, 1000),
+                                     (40, 128, 1000), (12, 128, 9000)])
+def test_tree_attn_values_of_any_size(dv, variant, T, D, cap, pattern, e):
+    """Results are as exact for values of 2^-60 or 2^90 as for values of 1, also where scores rise
+    from tile to tile and where the first rows, or every other tile's, are zeros."""
+    skip_same(variant, "i8", D, T)
+    rise = 12.0
+    c = Case(dv, 2, 3, 1, D, 16, "i8", tokens=T)
+    c = big(c, dv, cap, T)
+    k0, v = sized_cache(c, pattern, e, rise, e + 1000)
+    lens = [cap - T, cap // 2 + 5]
+    q = torch.zeros(2, T, 3, D, device="cuda")
+    q[..., 0] = 1.0
+    out = torch.zeros_like(q)
+    dv.dv_tree_attn(c.cache, q, i32(lens), out, c.ws, scale=math.log(2))
+    c.ok()
+    got = out.double().cpu().numpy()
+    ln2 = float(np.float32(math.log(2)))
+    tol = sized_tolerance(e, rise, 64 if cap <= 4096 else 224)
+    for b in range(2):
+        for t in (0, T - 1):
+            n = lens[b] + t + 1
+            s = ln2 * k0[b, :, :n]
+            p = np.exp(s - s.max(-1, keepdims=True))
+            want = np.einsum("hp,hpd->hd", p / p.sum(-1, keepdims=True), v[b, :, :n])
+            err = np.abs(got[b, t] - want).max() / want.max()
+            assert err <= tol, f"row {b} token {t}: off by {err:.3g} of its size, allowed {tol:.3g}"
+
+
+def big(c, dv, cap, tokens, block=0):
+    """c with a cache of `cap` positions that only the device holds."""
+    c.cap = cap
+    c.desc = dv.make_kv_desc(c.H, c.Hkv, c.D, cap, dv.DV_I8, block)
+    c.cache = dv.KvCache(c.desc, c.B)
+    c.ws = dv.KvWorkspace(c.desc, c.B, tokens)
+    return c
+
+
+@pytest.mark.parametrize("pattern,e", SIZES)
+@pytest.mark.parametrize("D,cap", [(128, 1000), (64, 6000)])
+def test_block_attn_values_of_any_size(dv, pattern, e, D, cap):
+    rise = 12.0
+    c = big(Case(dv, 2, 3, 1, D, 16, "i8"), dv, cap, 1, 16)
+    k0, v = sized_cache(c, pattern, e, rise, e + 2000)
+    lens = [cap, cap // 2 + 5]
+    q = torch.zeros(2, 3, D, device="cuda")
+    q[..., 0] = 1.0
+    out = torch.zeros_like(q)
+    idx = torch.arange(cap // 16, dtype=torch.int32, device="cuda").repeat(2, 3, 1)
+    idx[1, :, (lens[1] + 15) // 16:] = -1
+    dv.dv_block_attn(c.cache, q, i32(lens), idx, out, c.ws, scale=math.log(2))
+    c.ok()
+    got = out.double().cpu().numpy()
+    tol = sized_tolerance(e, rise, 64 if cap <= 4096 else 224)
+    for b in range(2):
+        n = min(lens[b], cap // 16 * 16)
+        s = float(np.float32(math.log(2))) * k0[b, :, :n]
+        p = np.exp(s - s.max(-1, keepdims=True))
+        want = np.einsum("hp,hpd->hd", p / p.sum(-1, keepdims=True), v[b, :, :n])
+        err = np.abs(got[b] - want).max() / want.max()
+        assert err <= tol, f"row {b}: off by {err:.3g} of its size, allowed {tol:.3g}"
