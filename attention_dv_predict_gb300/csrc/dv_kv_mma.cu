@@ -315,10 +315,14 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
             weights(m == -INFINITY ? 0.f : m);
             const bool range = big <= kWeightMax && sum <= kSumMax && m != -INFINITY;
             if (!__all_sync(0xffffffffu, range)) {  // first weights, or one out of range: rare
+                // (a row's reference moves for its own sake only, so that no row's
+                // bits depend on what another one sees)
+                const bool move = quad_max(range ? 0.f : 1.f) != 0.f;
                 const float top = quad_max(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
-                const float m0 = ref_from_scores(m, top);
+                const float m0 = move ? ref_from_scores(m, top) : m;
                 weights(m0 == -INFINITY ? 0.f : m0);
-                const float mn = ref_new(m, m0, quad_max(big)), g2 = pow2(m0 - mn);
+                big = quad_max(big);
+                const float mn = move ? ref_new(m, m0, big) : m, g2 = move ? pow2(m0 - mn) : 1.f;
                 sum *= g2;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)

@@ -223,7 +223,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     __shared__ Unit s_unit[2];
     __shared__ int s_tile0[2], s_n[2];  // first tile; tiles (0: the run is over)
     __shared__ int s_ends[2];           // bit 0: the part's first chunk, bit 1: its last
-    __shared__ float s_max[2][2][RM];  // rare: a row's maximum over both halves
+    __shared__ float s_max[2][2][RM];  // rare: a row's maximum over both halves,
+    __shared__ bool s_out[2][2][RM];   // and whether a weight of it is out of range
     __shared__ unsigned s_bad[2][2];  // binary16 edge tiles: positions not finite
     __shared__ __align__(8) uint64_t b_raw_full[I8 ? C::NSR : 1], b_raw_empty[I8 ? C::NSR : 1],
         b_sc_full[C::NSC], b_k_full[NK], b_k_empty[NK], b_v_full[NV], b_v_empty[NV], b_s_full[C::NS],
@@ -756,6 +757,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     moved |= !(big[r] <= kWeightMax && sum[r] <= kSumMax) || m[r] == -INFINITY;
                 moved = stream_any(sx, moved);
                 if (moved) {  // a row's first weights, or one out of range: rare
+                    // (a row's reference moves for its own sake only, so that no row's
+                    // bits depend on what another one sees)
+                    bool move[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const bool out =
+                            !(big[r] <= kWeightMax && sum[r] <= kSumMax) || m[r] == -INFINITY;
+                        move[r] = quad_max(out ? 1.f : 0.f) != 0.f;
+                        if (t4 == 0)
+                            s_out[sx][hx][16 * ww + g + 8 * r] = move[r];
+                    }
                     scores();
                     float mn[2], ms[2];
                     // a row's maximum over both halves, by way of shared memory
@@ -768,8 +780,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         }
                         stream_any(sx, false);
 #pragma unroll
-                        for (int r = 0; r < 2; ++r)
-                            x[r] = fmaxf(x[r], s_max[sx][hx ^ 1][16 * ww + g + 8 * r]);
+                        for (int r = 0; r < 2; ++r) {
+                            const int row = 16 * ww + g + 8 * r;
+                            x[r] = fmaxf(x[r], s_max[sx][hx ^ 1][row]);
+                            if (scaled)
+                                move[r] |= s_out[sx][hx ^ 1][row];
+                        }
                         stream_any(sx, false);
                     };
                     float top[2] = {-INFINITY, -INFINITY};
@@ -779,7 +795,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     row_max(top, true);
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        mn[r] = ref_from_scores(m[r], top[r]);
+                        mn[r] = move[r] ? ref_from_scores(m[r], top[r]) : m[r];
                         ms[r] = mn[r] == -INFINITY ? 0.f : mn[r];
                     }
                     weights(ms[0], ms[1], sum, big);
@@ -787,8 +803,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const float m0 = mn[r];
-                        mn[r] = ref_new(m[r], m0, big[r]);
-                        const float g2 = pow2(m0 - mn[r]);
+                        mn[r] = move[r] ? ref_new(m[r], m0, big[r]) : m[r];
+                        const float g2 = move[r] ? pow2(m0 - mn[r]) : 1.f;
                         sum[r] *= g2;
 #pragma unroll
                         for (int j = 0; j < 4; ++j)

@@ -172,7 +172,7 @@ DV_DEV void fma2(float &a, float &b, float c, float d)  // a c + d, b c + d
 // 2048 8-bit positions 737 us against 687.)  m is a whole number, so that every
 // change of reference scales by a power of two, without an error.  m = -inf:
 // nothing seen yet.
-constexpr float kWeightMax = 16384.f;
+constexpr float kWeightMax = 65504.f;  // the largest binary16
 constexpr float kSumMax = 0x1p100f;  // 2^(s - m) itself must stay finite where v is tiny
 constexpr float kShiftMin = -60.f;
 // A reference for the scores' maximum top (over a row) before weights are

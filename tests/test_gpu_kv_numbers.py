@@ -116,3 +116,49 @@ def test_block_attn_values_of_any_size(dv, pattern, e, D, cap):
         want = np.einsum("hp,hpd->hd", p / p.sum(-1, keepdims=True), v[b, :, :n])
         err = np.abs(got[b] - want).max() / want.max()
         assert err <= tol, f"row {b}: off by {err:.3g} of its size, allowed {tol:.3g}"
+
+
+@pytest.mark.parametrize("dtype", ["f16", "i8", "f32"])
+@pytest.mark.parametrize("what", ["nan", "inf", "huge", "queries"])
+@pytest.mark.parametrize("T,cap", [(6, 200), (6, 9000), (24, 200), (40, 9000)])
+def test_rows_do_not_depend_on_one_another(dv, variant, dtype, what, T, cap):
+    """To the bit: what a token does not see (behind the last token, and a drafted token that only
+    itself sees), and other tokens' queries, do not show in its result."""
+    if dtype == "f32" and cap > 200:
+        pytest.skip("one form at any capacity")
+    skip_same(variant, dtype, 64, T)
+    B, Hkv, D = 2, 2, 64
+    c = Case(dv, B, Hkv, 1, D, cap, dtype, tokens=T, seed=5)
+    lens, n_tok, own = [cap - 70, 13], [T - 1, T], 2
+    mask = [random_tree(c.rng, T) for _ in range(B)]
+    for b in range(B):
+        mask[b] = [m & ~(1 << own) for m in mask[b]]
+        mask[b][own] = (1 << T) - 1
+    q = torch.from_numpy(c.normal(B, T, Hkv, D)).cuda()
+
+    def run():
+        out = torch.zeros(B, T, Hkv, D, device="cuda")
+        dv.dv_tree_attn(c.cache, q, i32(lens), out, c.ws, mask=mask_tensor(mask),
+                        n_tok=i32(n_tok))
+        c.ok()
+        return out
+
+    clean = run()
+    if what == "queries":
+        q[:, own] *= 300
+    else:
+        x = {"nan": np.nan, "inf": np.inf, "huge": 3e4 if dtype == "f16" else 1e30}[what]
+        for b in range(B):
+            for p in [lens[b] + own] + list(range(lens[b] + n_tok[b], cap)):
+                for t in ("k", "v"):
+                    if dtype == "i8":
+                        c.ref.scale[t][b, :, p] = x
+                    else:
+                        c.ref.raw[t][b, :, p] = x
+        c.upload()
+    got = run()
+    for b in range(B):
+        for t in range(n_tok[b]):
+            if t != own:
+                assert torch.equal(got[b, t], clean[b, t]), (b, t)
+    assert not torch.equal(got[:, own], clean[:, own])
