@@ -988,6 +988,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             if (end)
                 fin.done(a, run, x);
+            __syncwarp();  // every lane has read what lies in the buffer
             if (lane == 0)
                 bar_arrive(smem_addr(&b_q_free[buf]));
         }

@@ -162,3 +162,56 @@ def test_rows_do_not_depend_on_one_another(dv, variant, dtype, what, T, cap):
             if t != own:
                 assert torch.equal(got[b, t], clean[b, t]), (b, t)
     assert not torch.equal(got[:, own], clean[:, own])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "i8"])
+@pytest.mark.parametrize("T,D", [(3, 64), (12, 64), (12, 128)])
+def test_long_rows_repeat_and_meet_poison(dv, variant, dtype, T, D):
+    """So many long rows that a CTA attends several whole ones in chunks: the same bits from cold
+    and warm calls, and with NaN or infinities where no token looks; one that is seen reaches its
+    own head alone."""
+    skip_same(variant, dtype, D, T)
+    Hkv, cap = 160, 9000
+    desc = dv.make_kv_desc(Hkv, Hkv, D, cap, 1 if dtype == "f16" else 2)
+    cache, ws = dv.KvCache(desc, 1), dv.KvWorkspace(desc, 1, T)
+    g = torch.Generator(device="cuda").manual_seed(T + D)
+    for t in (cache.k, cache.v):
+        t.random_(-100, 101, generator=g)
+    if dtype == "i8":
+        cache.k_scale.uniform_(0.01, 0.02, generator=g)
+        cache.v_scale.uniform_(0.01, 0.02, generator=g)
+    else:
+        cache.k.mul_(2.0 ** -6)
+        cache.v.mul_(2.0 ** -6)
+    n = cap - T - 130
+    mask = torch.full((1, T), (1 << T) - 1, dtype=torch.int64, device="cuda")
+    mask &= ~2  # no token sees drafted token 1
+    q = torch.randn(1, T, Hkv, D, generator=g, device="cuda")
+    flush = torch.empty(1 << 28, dtype=torch.int8, device="cuda")
+
+    def run():
+        out = torch.zeros(1, T, Hkv, D, device="cuda")
+        flush.fill_(1)
+        dv.dv_tree_attn(cache, q, i32([n]), out, ws, mask=mask)
+        assert dv.dv_check(ws) == 0
+        return out
+
+    def put(h, p, x):
+        for t in (cache.k, cache.v) if dtype == "f16" else (cache.k_scale, cache.v_scale):
+            t[0, h, p] = x
+
+    clean = run()
+    for _ in range(4):
+        assert torch.equal(run(), clean)
+    for x in (float("nan"), float("inf")):
+        for p in (n + 1, slice(n + T, cap)):
+            put(slice(None), p, x)
+        assert torch.equal(run(), clean)
+        put(77, 5000, x)
+        out = run()
+        assert not torch.isfinite(out[0, :, 77]).any()
+        out[:, :, 77] = clean[:, :, 77]
+        assert torch.equal(out, clean)
+        put(77, 5000, 1.0)
+        clean[:, :, 77] = run()[:, :, 77]
+    assert torch.isfinite(clean).all()
