@@ -198,8 +198,8 @@ struct Store<DV_I8> {
 // rounded to a multiple of g = n 2^(e - 24), and sums of n such multiples
 // are whole numbers below 2^24 times g.  Then mean = (sum / g) 2^(e - 24),
 // quantised as a row.  The rounding is below 2^-17 of the block's largest
-// value for n = 128, far under a code.  A block with a NaN or an infinity
-// gets codes 0 and scale +inf (it is selected first).
+// value for n = 128, far under a code.  A block with a NaN or an infinity, or
+// whose mean rounds to one, gets codes 0 and scale +inf (it is selected first).
 //
 // A warp a block and no barrier: the other warps of an append go on with the
 // values meanwhile (a mean by the whole CTA, with its barriers, took 210 us
@@ -219,6 +219,7 @@ DV_DEV void store_mean(const KvCacheArgs &c, size_t row, const int (&acc)[EPC], 
     float ma = amax_of(mean);
     for (int o = 1; o < lpr; o <<= 1)
         ma = amax2(ma, __shfl_xor_sync(0xffffffffu, ma, o));
+    fine &= ma <= 3.402823466e38f;  // (2^24 units of 2^104: all keys at binary32's end)
     const float s = quant_scale(ma);
     if ((int)(threadIdx.x & 31) < lpr) {
         const float inv = quant_inv(s);

@@ -459,8 +459,8 @@ int dv_predict_topk_noalloc(const dv_layer_desc *desc, const dv_layer_weights *w
  * other n - 1 must be in the cache by then).  The mean's sum is taken over
  * the keys as stored, each rounded to a multiple of n 2^(e - 24) with 2^e the
  * power of two above the block's largest magnitude (e >= -100), so that it is
- * exact in any order.  A block with a NaN or an infinity has codes 0 and
- * scale +infinity.
+ * exact in any order.  A block with a NaN or an infinity, or whose mean rounds
+ * to one, has codes 0 and scale +infinity.
  */
 #define DV_KV_MAX_BATCH 256
 #define DV_TREE_MAX_TOKENS 64

@@ -215,3 +215,33 @@ def test_long_rows_repeat_and_meet_poison(dv, variant, dtype, T, D):
         put(77, 5000, 1.0)
         clean[:, :, 77] = run()[:, :, 77]
     assert torch.isfinite(clean).all()
+
+
+@pytest.mark.parametrize("how", ["append", "keep"])
+def test_mean_of_the_largest_keys(dv, how):
+    """Keys at binary32's end: their mean rounds to an infinity, so the block comes first, like one
+    that holds an infinity; below that it is a mean like others."""
+    B, T, D, n = 1, 48, 32, 16
+    c = Case(dv, B, 1, 1, D, 64, "f32", n)
+    x = c.normal(B, T, 1, D)
+    top = np.finfo(np.float32).max
+    x[:, :n] = top
+    x[:, n:2 * n] = np.float32(top * (1 - 2.0 ** -19))
+    dev = torch.from_numpy(x).cuda()
+    dv.dv_kv_append(c.cache, dev, dev, i32([0]), c.ws)
+    if how == "keep":
+        c.cache.k_mean.fill_(5)
+        c.cache.k_mean_scale.fill_(7.0)
+        path = torch.arange(T, dtype=torch.int32, device="cuda").reshape(1, T)
+        dv.dv_kv_keep(c.cache, i32([0]), path, i32([T]), c.ws)
+    c.ok()
+    scale = c.cache.k_mean_scale[0, 0].cpu().numpy()
+    codes = c.cache.k_mean[0, 0].cpu().numpy()
+    assert np.isinf(scale[0]) and not codes[0].any()
+    assert (codes[1] == 127).all() and abs(float(scale[1]) * 127 / top - 1) < 2.0 ** -18
+    want, s = kv_ref.quantise(x[0, 2 * n:3 * n, 0].astype(np.float64).mean(0).astype(np.float32))
+    assert np.abs(codes[2].astype(int) - want).max() <= 1 and abs(scale[2] / s - 1) < 2.0 ** -16
+    idx = torch.zeros(B, 1, 2, dtype=torch.int32, device="cuda")
+    dv.dv_block_topk(c.cache, -dev[:, 0, :, :] / top, i32([T]), idx, c.ws, n_first=0)
+    c.ok()
+    assert idx.flatten().tolist() == [0, 2]
