@@ -111,6 +111,9 @@ dv_status attn_launch(const KvAttnArgs &a, const KvPlan &p, void *stream)
 template <typename P>
 P *at(void *ws, size_t off) { return reinterpret_cast<P *>(static_cast<char *>(ws) + off); }
 
+// The softmax scale in units of log2, as the kernels take it.
+float scale2(float scale) { return scale * 1.4426950408889634f; }
+
 // Work items of a 1-D grid fit its limit.
 bool grid_ok(long long n) { return n > 0 && n <= INT_MAX; }
 
@@ -265,7 +268,7 @@ int dv_tree_attn(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_r
     if ((s = check_cache(*desc, cache, batch, &a.c)) || (s = check_rows(q, &a.q)))
         return s;
     if (tokens < 1 || tokens > DV_TREE_MAX_TOKENS || tokens > desc->kv_cap || !aligned(lens, 4) ||
-        (n_tok && !aligned(n_tok, 4)) || (mask && !aligned(mask, 8)) || !std::isfinite(scale) ||
+        (n_tok && !aligned(n_tok, 4)) || (mask && !aligned(mask, 8)) || !std::isfinite(scale2(scale)) ||
         !aligned(out, 16))
         return DV_ERR_INVALID_ARG;
     if (u_h ? !aligned(u_h, 4) || !aligned(n_u_h, 4) || max_u_h < 1 || max_u_h > desc->n_kv_heads
@@ -283,7 +286,7 @@ int dv_tree_attn(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_r
     a.H = desc->n_heads;
     a.T = tokens;
     a.r_group = (float)desc->n_kv_heads / (float)desc->n_heads;
-    a.scale = scale * 1.4426950408889634f;
+    a.scale = scale2(scale);
     a.out = out;
     a.rec = at<float>(ws, kKvRecOff);
     a.cnt = at<int>(ws, kKvCntOff);
@@ -331,7 +334,7 @@ int dv_block_attn(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_
     if ((s = check_cache(*desc, cache, batch, &a.c)) || (s = check_rows(q, &a.q)))
         return s;
     if (!desc->block || k_blocks < 1 || k_blocks > kKvMaxBlocks || !aligned(lens, 4) ||
-        !aligned(idx, 4) || !std::isfinite(scale) || !aligned(out, 16))
+        !aligned(idx, 4) || !std::isfinite(scale2(scale)) || !aligned(out, 16))
         return DV_ERR_INVALID_ARG;
     if ((s = check_ws(*desc, 1, ws, ws_bytes)))
         return s;
@@ -344,7 +347,7 @@ int dv_block_attn(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_
     a.H = desc->n_heads;
     a.T = 1;
     a.r_group = (float)desc->n_kv_heads / (float)desc->n_heads;
-    a.scale = scale * 1.4426950408889634f;
+    a.scale = scale2(scale);
     a.out = out;
     a.rec = at<float>(ws, kKvRecOff);
     a.cnt = at<int>(ws, kKvCntOff);

@@ -541,10 +541,11 @@ int dv_kv_keep(const dv_kv_desc *desc, const dv_kv_cache *cache, int batch, int 
  *   out [B, tokens, n_heads, D] binary32:
  *     out[b, t, h] = sum_p softmax_p(scale q . k_p) v_p
  *   over positions p < lens[b] and the drafted ones it sees; zeros where it
- *   sees none.  Tokens t >= n_tok[b] and heads that are not listed are left
- *   as they were.  A position that a token does not see cannot change its
- *   result, whatever it holds, nor can another token's query; a value row that
- *   it sees and that holds a NaN or an infinity makes the result non-finite.
+ *   sees none (scale log2(e) must be finite).  Tokens t >= n_tok[b] and heads
+ *   that are not listed are left as they were.  A position that a token does
+ *   not see cannot change its result, whatever it holds, nor can another token's
+ *   query; a value row that it sees and that holds a NaN or an infinity makes
+ *   the result non-finite.
  *   u_h, n_u_h, max_u_h: device list of distinct KV heads to compute, as
  *   dv_sparse_attn's (NULL, NULL, 0: every head; max_u_h <= n_kv_heads).
  * tokens = 1 is decode attention with one length a row.  Scores, weights and
