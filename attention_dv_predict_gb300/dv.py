@@ -513,6 +513,12 @@ def _kv_dev(cache: KvCache, ws: KvWorkspace, stream):
     return stream.cuda_stream
 
 
+def _kv_dim(name: str, t: torch.Tensor, ndim: int, dim: int) -> int:
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions")
+    return t.shape[dim]
+
+
 def _kv_tensor(name: str, t: Optional[torch.Tensor], cache: KvCache, shape, dtype):
     if t is None:
         return None
@@ -540,7 +546,7 @@ def _kv_rows(name: str, t: torch.Tensor, cache: KvCache, shape) -> KvRows:
 def dv_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, lens: torch.Tensor,
                  ws: KvWorkspace, n_tok: Optional[torch.Tensor] = None, stream=None):
     """Write k, v [B, T, Hkv, D] (any strides over the first three) at positions lens[b] + t."""
-    d, B, T = cache.desc, cache.batch, k.shape[1]
+    d, B, T = cache.desc, cache.batch, _kv_dim("k", k, 4, 1)
     st = _kv_dev(cache, ws, stream)
     shape = (B, T, d.n_kv_heads, d.head_dim)
     _check("dv_kv_append", _lib.dv_kv_append(
@@ -553,7 +559,7 @@ def dv_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, lens: torch.T
 def dv_kv_read(cache: KvCache, start: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor,
                ws: KvWorkspace, stream=None):
     """Positions start[b] .. start[b] + T - 1 into k_out, v_out [B, Hkv, T, D] (float32/float16)."""
-    d, B, T = cache.desc, cache.batch, k_out.shape[2]
+    d, B, T = cache.desc, cache.batch, _kv_dim("k_out", k_out, 4, 2)
     st = _kv_dev(cache, ws, stream)
     if k_out.dtype not in _ROW_DTYPE:
         raise ValueError("k_out must be float32 or float16")
@@ -567,7 +573,7 @@ def dv_kv_read(cache: KvCache, start: torch.Tensor, k_out: torch.Tensor, v_out: 
 def dv_kv_keep(cache: KvCache, lens: torch.Tensor, path: torch.Tensor, n_keep: torch.Tensor,
                ws: KvWorkspace, stream=None):
     """Move position lens[b] + path[b, i] to lens[b] + i for i < n_keep[b] (path [B, T] ascending)."""
-    B, T = cache.batch, path.shape[1]
+    B, T = cache.batch, _kv_dim("path", path, 2, 1)
     st = _kv_dev(cache, ws, stream)
     _check("dv_kv_keep", _lib.dv_kv_keep(
         *cache._refs, B, T, _kv_tensor("lens", lens, cache, (B,), torch.int32),
@@ -583,7 +589,7 @@ def dv_tree_attn(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, out: torch
     """Attention of q [B, T, H, D] over the cache; mask [B, T] int64 (bit j: sees drafted token j).
 
     scale: head_dim ** -0.5 by default.  u_h, n_u_h: a device list of KV heads and its length."""
-    d, B, T = cache.desc, cache.batch, q.shape[1]
+    d, B, T = cache.desc, cache.batch, _kv_dim("q", q, 4, 1)
     st = _kv_dev(cache, ws, stream)
     shape = (B, T, d.n_heads, d.head_dim)
     if (u_h is None) != (n_u_h is None):
@@ -608,7 +614,7 @@ def dv_set_tree_kernel(variant: int) -> None:
 def dv_block_topk(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, idx: torch.Tensor,
                   ws: KvWorkspace, n_first: int = 1, n_last: int = 1, stream=None):
     """The idx.shape[2] blocks each query of q [B, H, D] attends to, into idx [B, H, k] (-1 behind)."""
-    d, B, k = cache.desc, cache.batch, idx.shape[2]
+    d, B, k = cache.desc, cache.batch, _kv_dim("idx", idx, 3, 2)
     st = _kv_dev(cache, ws, stream)
     _check("dv_block_topk", _lib.dv_block_topk(
         *cache._refs, C.byref(_kv_rows("q", q, cache, (B, d.n_heads, d.head_dim))), B,
@@ -619,7 +625,7 @@ def dv_block_topk(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, idx: torc
 def dv_block_attn(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, idx: torch.Tensor,
                   out: torch.Tensor, ws: KvWorkspace, scale: Optional[float] = None, stream=None):
     """Attention of q [B, H, D] over the blocks listed in idx [B, H, k], into out [B, H, D]."""
-    d, B, k = cache.desc, cache.batch, idx.shape[2]
+    d, B, k = cache.desc, cache.batch, _kv_dim("idx", idx, 3, 2)
     st = _kv_dev(cache, ws, stream)
     shape = (B, d.n_heads, d.head_dim)
     _check("dv_block_attn", _lib.dv_block_attn(

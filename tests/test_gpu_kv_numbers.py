@@ -245,3 +245,18 @@ def test_mean_of_the_largest_keys(dv, how):
     dv.dv_block_topk(c.cache, -dev[:, 0, :, :] / top, i32([T]), idx, c.ws, n_first=0)
     c.ok()
     assert idx.flatten().tolist() == [0, 2]
+
+
+def test_wrappers_refuse_tensors_of_other_ranks(dv):
+    """Too few dimensions are a ValueError too."""
+    c = Case(dv, 2, 2, 1, 32, 50, "i8", 16)
+    lens, x, o = i32([0, 0]), torch.zeros(2, 2, device="cuda"), torch.zeros(2, device="cuda")
+    for call in (lambda: dv.dv_kv_append(c.cache, o, o, lens, c.ws),
+                 lambda: dv.dv_kv_read(c.cache, lens, x, x, c.ws),
+                 lambda: dv.dv_kv_keep(c.cache, lens, lens, lens, c.ws),
+                 lambda: dv.dv_tree_attn(c.cache, o, lens, o, c.ws),
+                 lambda: dv.dv_block_topk(c.cache, x, lens, lens, c.ws),
+                 lambda: dv.dv_block_attn(c.cache, x, lens, lens, x, c.ws)):
+        with pytest.raises(ValueError):
+            call()
+    c.same_cache()
