@@ -247,6 +247,87 @@ def test_mean_of_the_largest_keys(dv, how):
     assert idx.flatten().tolist() == [0, 2]
 
 
+@pytest.mark.parametrize("dtype,D", [("f32", 32), ("f16", 64), ("f16", 32)])
+@pytest.mark.parametrize("T", [2, 12])
+def test_infinite_keys(dv, variant, dtype, D, T):
+    """A key with an infinity that a token sees: its score is an infinity or not a number.  The
+    result is NaN, or as if the token did not see it (a score of -infinity); other heads and
+    tokens that do not see it keep their bits."""
+    skip_same(variant, dtype, D, T)
+    B, H, cap = 1, 3, 300
+    c = Case(dv, B, H, 1, D, cap, dtype, tokens=T, seed=1)
+    n = 200
+    q = torch.from_numpy(c.normal(B, T, H, D)).cuda()
+    mask = [[((1 << T) - 1) & ~2] * T]  # drafted token 1 is not seen
+    mask[0][T - 1] |= 2                 # but by the last one
+
+    def run():
+        out = torch.zeros(B, T, H, D, device="cuda")
+        dv.dv_tree_attn(c.cache, q, i32([n]), out, c.ws, mask=mask_tensor(mask))
+        c.ok()
+        return out
+
+    clean = run()
+    c.cache.k[0, 0, n + 1, 3] = float("inf")
+    out = run()
+    assert torch.equal(out[:, :T - 1], clean[:, :T - 1])
+    assert torch.equal(out[:, :, 1:], clean[:, :, 1:])
+    mask[0][T - 1] &= ~2
+    unseen = run()[0, T - 1, 0]
+    got = out[0, T - 1, 0]
+    assert torch.isnan(got).all() or torch.allclose(got, unseen, rtol=1e-5, atol=1e-6)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "i8", "f32"])
+@pytest.mark.parametrize("D,cap", [(64, 700), (128, 9000)])
+def test_block_attn_meets_poison(dv, dtype, D, cap):
+    """NaN and infinities in blocks that are not listed, and behind the last position of a listed
+    one, do not show; a listed one reaches its own head alone."""
+    if dtype == "f32" and cap > 700:
+        pytest.skip("one form at any capacity")
+    H, n = 3, 32
+    c = Case(dv, 1, H, 1, D, cap, dtype, n, seed=2)
+    L = cap - 75
+    nb = -(-L // n)
+    listed = [j for j in range(nb) if j % 5 != 1]
+    assert nb - 1 in listed
+    idx = torch.full((1, H, nb), -1, dtype=torch.int32, device="cuda")
+    idx[:, :, :len(listed)] = torch.tensor(listed, dtype=torch.int32, device="cuda")
+    q = torch.from_numpy(c.normal(1, H, D)).cuda()
+
+    def run():
+        out = torch.zeros(1, H, D, device="cuda")
+        dv.dv_block_attn(c.cache, q, i32([L]), idx, out, c.ws)
+        c.ok()
+        return out
+
+    clean = run()
+    sides = (c.cache.k_scale, c.cache.v_scale) if dtype == "i8" else (c.cache.k, c.cache.v)
+    for x in (float("nan"), float("inf")):
+        for t in sides:
+            for j in range(1, nb, 5):
+                t[:, :, j * n:(j + 1) * n] = x
+            t[:, :, L:] = x
+        assert torch.equal(run(), clean)
+    sides[1][0, 1, 2 * n + 5] = float("nan")
+    out = run()
+    assert not torch.isfinite(out[0, 1]).any()
+    assert torch.equal(out[0, [0, 2]], clean[0, [0, 2]])
+
+
+@pytest.mark.parametrize("dtype,B,Hkv,T", [("f16", 6, 4, 12), ("f16", 6, 8, 20), ("i8", 6, 4, 12),
+                                           ("i8", 8, 8, 40)])
+def test_short_rows_in_a_large_cache(dv, dtype, B, Hkv, T):
+    """Capacity of more than 4096 positions, rows of a hundred: the rules choose the kernel."""
+    c = Case(dv, B, Hkv, 1, 64, 6000, dtype, tokens=T, seed=T)
+    lens = [0, 1, 63, 64, 100, 17, 129, 5][:B]
+    q = c.normal(B, T, Hkv, 64)
+    out = torch.zeros(q.shape, device="cuda")
+    dv.dv_tree_attn(c.cache, torch.from_numpy(q).cuda(), i32(lens), out, c.ws)
+    c.ok()
+    close(out, *kv_ref.tree(c.ref, q, lens, [T] * B, None, 0.125))
+
+
 def test_wrappers_refuse_tensors_of_other_ranks(dv):
     """Too few dimensions are a ValueError too."""
     c = Case(dv, 2, 2, 1, 32, 50, "i8", 16)
