@@ -439,7 +439,9 @@ int dv_predict_topk_noalloc(const dv_layer_desc *desc, const dv_layer_weights *w
  * The conventions at the top of this file hold; the workspace is one of
  * dv_kv_workspace_size() bytes (not one of the layer calls'), zeroed once
  * with dv_workspace_init() and read by dv_check().  It may be shared by calls
- * of any shapes that fit it, one after another.
+ * of any shapes that fit it, one after another; calls, or graphs that hold
+ * them, that may run at the same time need a workspace each (dv_tree_attn and
+ * dv_block_attn keep pieces and counters in it).
  *
  * Device-side checks: a batch row whose length, token count, path or list of
  * blocks is out of range is skipped, its outputs and cache rows are left as
@@ -544,8 +546,9 @@ int dv_kv_keep(const dv_kv_desc *desc, const dv_kv_cache *cache, int batch, int 
  *   sees none (scale log2(e) must be finite).  Tokens t >= n_tok[b] and heads
  *   that are not listed are left as they were.  A position that a token does
  *   not see cannot change its result, whatever it holds, nor can another token's
- *   query; a value row that it sees and that holds a NaN or an infinity makes
- *   the result non-finite.
+ *   query; a value row that it sees and that holds a NaN or an infinity, or a
+ *   key row with a NaN, makes the result non-finite.  A key row with an infinity
+ *   does so too, or counts as unseen (a score of -infinity).
  *   u_h, n_u_h, max_u_h: device list of distinct KV heads to compute, as
  *   dv_sparse_attn's (NULL, NULL, 0: every head; max_u_h <= n_kv_heads).
  * tokens = 1 is decode attention with one length a row.  Scores, weights and
