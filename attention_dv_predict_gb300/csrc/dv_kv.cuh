@@ -127,18 +127,6 @@ DV_DEV float ld_row(const KvRowsArgs &r, long long i)
                  : static_cast<const float *>(r.p)[i];
 }
 
-// Four consecutive values of a row given by the caller (16-byte aligned for
-// binary32, 8-byte for binary16).
-DV_DEV float4 ld_row4(const KvRowsArgs &r, long long i)
-{
-    if (!r.f16)
-        return *reinterpret_cast<const float4 *>(static_cast<const float *>(r.p) + i);
-    const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const __half *>(r.p) + i);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-
 // ---------------------------------------------------------------------------
 DV_DEV float block_amax(float v, float *scratch)
 {

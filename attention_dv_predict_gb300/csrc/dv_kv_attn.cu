@@ -11,9 +11,9 @@
 //
 // Four passes' rows (two of 8 bits: registers) are loaded together and their
 // dot products reduced side by side: one token of 8 x 96 heads over 2049
-// binary32 positions of 128 values takes 316 us, 0.75 of the bytes' rate (a
+// binary32 positions of 128 values takes 279 us, 0.85 of the bytes' rate (a
 // pass at a time 1068).  More query rows are bound by the arithmetic and the
-// shuffles of the CUDA cores: 64 tokens of one batch row 1331 us.
+// shuffles of the CUDA cores: 64 tokens of one batch row 1174 us.
 #include "dv_kv_sched.cuh"
 
 namespace dv {
@@ -23,36 +23,29 @@ constexpr int kGenThreads = 128;
 constexpr int kGenWarps = kGenThreads / 32;
 constexpr int RM = kKvGenRows;
 
-template <typename T>
-struct Cached;
-template <>
-struct Cached<float> {
-    static constexpr int EPC = 4;
-    DV_DEV static void unpack(const uint4 &v, float (&f)[4]) { Elem<float>::unpack(v, f); }
-};
-template <>
-struct Cached<__half> {
-    static constexpr int EPC = 8;
-    DV_DEV static void unpack(const uint4 &v, float (&f)[8]) { Elem<__half>::unpack(v, f); }
-};
-template <>
-struct Cached<int8_t> {
-    static constexpr int EPC = 16;
-    DV_DEV static void unpack(const uint4 &v, float (&f)[16])
-    {
+// 16 bytes of a row as numbers.  (8-bit codes one by one: by pairs of binary16, as
+// Store does it, one token of 8 x 32 heads over 2049 rows of 256 takes 244 us
+// instead of 204.)
+template <int DT>
+DV_DEV void unpack(const uint4 &v, float (&f)[Store<DT>::EPC])
+{
+    if constexpr (DT == DV_I8) {
         const unsigned u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             f[i] = (float)(int8_t)(u[i / 4] >> (8 * (i % 4)));
+    } else {
+        Store<DT>::unpack(v, f);
     }
-};
+}
 
 DV_DEV float safe(float m) { return m == -INFINITY ? 0.f : m; }
 
-template <typename T, bool BLOCK>
+template <int DT, bool BLOCK>
 __global__ void __launch_bounds__(kGenThreads) k_kv_attn(const KvAttnArgs a)
 {
-    constexpr int EPC = Cached<T>::EPC;
+    using T = typename Store<DT>::T;
+    constexpr int EPC = Store<DT>::EPC;
     __shared__ SchedSmem sm;
     __shared__ __align__(16) float qs[RM][256];
     __shared__ __align__(16) float wo[kGenWarps][RM][256];
@@ -117,7 +110,7 @@ __global__ void __launch_bounds__(kGenThreads) k_kv_attn(const KvAttnArgs a)
                     if (p[u] >= 0) {
                         kv[u] = __ldcg(reinterpret_cast<const uint4 *>(K + (base + p[u]) * D) + dc);
                         vv[u] = __ldcg(reinterpret_cast<const uint4 *>(V + (base + p[u]) * D) + dc);
-                        if (a.c.dtype == DV_I8) {
+                        if (DT == DV_I8) {
                             ksc[u] = __ldcg(a.c.ks + base + p[u]);
                             vsc[u] = __ldcg(a.c.vs + base + p[u]);
                         }
@@ -132,7 +125,7 @@ __global__ void __launch_bounds__(kGenThreads) k_kv_attn(const KvAttnArgs a)
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         float kf[EPC];
-                        Cached<T>::unpack(kv[u], kf);
+                        unpack<DT>(kv[u], kf);
                         dot[u] = 0.f;
 #pragma unroll
                         for (int e = 0; e < EPC; e += 4) {
@@ -152,7 +145,7 @@ __global__ void __launch_bounds__(kGenThreads) k_kv_attn(const KvAttnArgs a)
                         const int j = p[u] - x.len;
                         if (p[u] >= 0 && (j < 0 || ((bits[r] >> j) & 1))) {
                             float vf[EPC];
-                            Cached<T>::unpack(vv[u], vf);
+                            unpack<DT>(vv[u], vf);
                             const float y = dot[u] * ksc[u];
                             const float mn = fmaxf(m[r], y), ms = safe(mn);
                             const float sc = exp2f(m[r] - ms);
@@ -218,15 +211,15 @@ __global__ void __launch_bounds__(kGenThreads) k_kv_attn(const KvAttnArgs a)
     fin.end(a, run, sm, um, ul, wgt);
 }
 
-template <typename T>
+template <int DT>
 cudaError_t launch_gen(const KvAttnArgs &a, int grid, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kGenThreads);
     cfg.stream = st;
-    return a.idx ? cudaLaunchKernelEx(&cfg, k_kv_attn<T, true>, a)
-                 : cudaLaunchKernelEx(&cfg, k_kv_attn<T, false>, a);
+    return a.idx ? cudaLaunchKernelEx(&cfg, k_kv_attn<DT, true>, a)
+                 : cudaLaunchKernelEx(&cfg, k_kv_attn<DT, false>, a);
 }
 
 }  // namespace
@@ -269,10 +262,10 @@ cudaError_t launch_kv_attn(const KvAttnArgs &a, const KvPlan &p, int nsm, cudaSt
                                                 : launch_kv_tc(a, nsm, st);
     const int grid = nsm * 4 < kKvMaxCtas ? nsm * 4 : kKvMaxCtas;
     if (a.c.dtype == DV_I8)
-        return launch_gen<int8_t>(a, grid, st);
+        return launch_gen<DV_I8>(a, grid, st);
     if (a.c.dtype == DV_F16)
-        return launch_gen<__half>(a, grid, st);
-    return launch_gen<float>(a, grid, st);
+        return launch_gen<DV_F16>(a, grid, st);
+    return launch_gen<DV_F32>(a, grid, st);
 }
 
 }  // namespace dv

@@ -515,8 +515,8 @@ cudaError_t launch_cfg(const KvAttnArgs &a, int nsm, cudaStream_t st)
 template <bool I8, int D>
 cudaError_t launch_d(const KvAttnArgs &a, int nsm, cudaStream_t st)
 {
-    // rings of 48 to 96 KB; 8-bit rows need the third CTA's warps more
-    constexpr int NST = 3 * (128 / D), MINB = (I8 || D == 64) ? 3 : 2;
+    // rings of 48 KB (8 bits) and 96 KB: room for a third CTA per SM, and for two
+    constexpr int NST = 3 * (128 / D), MINB = I8 ? 3 : 2;
     // Units of at most FLUSH tiles have no use for the code that adds the
     // outputs up in between: 32 rows of 2049 8-bit positions of 96 heads take
     // 310 us without it, 361 with it (binary16: 475 both).  Where it is needed, at

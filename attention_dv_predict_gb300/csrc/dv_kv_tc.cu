@@ -116,13 +116,11 @@ template <int N>
 DV_DEV void tm_ld(unsigned addr, float (&v)[N])
 {
     static_assert(N == 16 || N == 8, "32 or 16 columns");
-    if constexpr (N == 0)
-        ;
-    else if constexpr (N == 16)
+    if constexpr (N == 16)
         asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
                      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
                      : "r"(addr));
-    else if constexpr (N == 8)
+    else
         asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                      : "r"(addr));
@@ -130,13 +128,12 @@ DV_DEV void tm_ld(unsigned addr, float (&v)[N])
 template <int N>
 DV_DEV void tm_st(unsigned addr, const float (&v)[N])
 {
-    if constexpr (N == 0)
-        ;
-    else if constexpr (N == 16)
+    static_assert(N == 16 || N == 8, "32 or 16 columns");
+    if constexpr (N == 16)
         asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
                      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
                      : "memory");
-    else if constexpr (N == 8)
+    else
         asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
                      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                      : "memory");
@@ -145,14 +142,13 @@ DV_DEV void tm_st(unsigned addr, const float (&v)[N])
 template <int N>
 DV_DEV void tm_wait_ld(float (&v)[N])
 {
-    if constexpr (N == 0)
-        ;
-    else if constexpr (N == 16)
+    static_assert(N == 16 || N == 8, "32 or 16 columns");
+    if constexpr (N == 16)
         asm volatile("tcgen05.wait::ld.sync.aligned;"
                      : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
                      :
                      : "memory");
-    else if constexpr (N == 8)
+    else
         asm volatile("tcgen05.wait::ld.sync.aligned;"
                      : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7])
                      :

@@ -45,20 +45,6 @@ DV_DEV bool bar_wait(unsigned bar, unsigned parity)
     return false;
 }
 
-// Whether it is complete now.
-DV_DEV bool bar_test(unsigned bar, unsigned parity)
-{
-    unsigned ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // Box at (byte x of the rows, position, (row, head)) of a cache side.
 DV_DEV void tma_load(unsigned dst, const CUtensorMap *map, int x, int pos, int bh, unsigned bar)
 {
