@@ -2,6 +2,9 @@
 scores that rise, rows that must not depend on one another, NaN and infinities."""
 
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -119,7 +122,7 @@ def test_block_attn_values_of_any_size(dv, pattern, e, D, cap):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "i8", "f32"])
-@pytest.mark.parametrize("what", ["nan", "inf", "huge", "queries"])
+@pytest.mark.parametrize("what", ["nan", "inf", "huge", "queries", "nan queries"])
 @pytest.mark.parametrize("T,cap", [(6, 200), (6, 9000), (24, 200), (40, 9000)])
 def test_rows_do_not_depend_on_one_another(dv, variant, dtype, what, T, cap):
     """To the bit: what a token does not see (behind the last token, and a drafted token that only
@@ -146,6 +149,8 @@ def test_rows_do_not_depend_on_one_another(dv, variant, dtype, what, T, cap):
     clean = run()
     if what == "queries":
         q[:, own] *= 300
+    elif what == "nan queries":
+        q[:, own, :, 7] = float("nan")
     else:
         x = {"nan": np.nan, "inf": np.inf, "huge": 3e4 if dtype == "f16" else 1e30}[what]
         for b in range(B):
@@ -341,3 +346,70 @@ def test_wrappers_refuse_tensors_of_other_ranks(dv):
         with pytest.raises(ValueError):
             call()
     c.same_cache()
+
+
+def test_two_calls_at_once(dv, variant):
+    """Calls on two streams, a workspace each, on one cache."""
+    c = Case(dv, 4, 4, 1, 128, 3000, "i8", 64, tokens=20)
+    lens = i32([2900, 2100, 50, 1500])
+    s = [torch.cuda.Stream() for _ in range(2)]
+    ws = [dv.KvWorkspace(c.desc, 4, 20) for _ in range(2)]
+    q = [torch.from_numpy(c.normal(4, 20, 4, 128)).cuda() for _ in range(2)]
+    want = [torch.zeros_like(q[0]) for _ in range(2)]
+    for i in range(2):
+        dv.dv_tree_attn(c.cache, q[i], lens, want[i], ws[i])
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(s[i]):
+                out = torch.zeros_like(q[i])
+                dv.dv_tree_attn(c.cache, q[i], lens, out, ws[i])
+                outs.append((i, out))
+    torch.cuda.synchronize()
+    assert all(dv.dv_check(w) == 0 for w in ws)
+    assert all(torch.equal(o, want[i]) for i, o in outs)
+
+
+FIRST_CALLS = """
+import torch
+from attention_dv_predict_gb300 import dv
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+for dt, D in ((0, 32), (1, 64), (2, 128)):
+    desc = dv.make_kv_desc(4, 4, D, 200, dt, 16)
+    c, ws = dv.KvCache(desc, 2), dv.KvWorkspace(desc, 2, 16)
+    x = torch.randn(2, 12, 4, D, device="cuda")
+    lens, n = i32([60, 5]), i32([12, 12])
+    path = torch.arange(12, dtype=torch.int32, device="cuda").repeat(2, 1)
+    k, v = (torch.zeros(2, 4, 12, D, device="cuda") for _ in range(2))
+    out, one = torch.zeros_like(x), torch.zeros(2, 4, D, device="cuda")
+    idx = torch.zeros(2, 4, 2, dtype=torch.int32, device="cuda")
+    def step():
+        dv.dv_kv_append(c, x, x, lens, ws)
+        dv.dv_tree_attn(c, x, lens, out, ws)
+        dv.dv_kv_keep(c, lens, path, n, ws)
+        dv.dv_kv_read(c, lens, k, v, ws)
+        dv.dv_block_topk(c, x[:, 0], lens, idx, ws)
+        dv.dv_block_attn(c, x[:, 0], lens, idx, one, ws)
+    for kernel in (1, 2):
+        dv.dv_set_tree_kernel(kernel)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        g.replay()
+        got = [t.clone() for t in (out, one, k, v, idx)]
+        step()
+        assert all(torch.equal(a, b) for a, b in zip(got, (out, one, k, v, idx)))
+        assert dv.dv_check(ws) == 0 and bool(out.any())
+print("captured")
+"""
+
+
+def test_first_calls_are_captured():
+    """A process whose first call of every operator is recorded into a graph."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "captured", r.stderr[-2000:]
