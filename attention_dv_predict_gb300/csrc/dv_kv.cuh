@@ -79,7 +79,7 @@ DV_DEV float code_at_half(float x, float s, float t)
 // quotient within 2^-18: both round to the same whole number unless x inv is
 // 2^-15 from a half (one value in 16000), where code_at_half decides.
 // A division per value made a 2048-token append of the 175B-shaped batch of 8
-// compute-bound (965 us; now 619, 479 of them its bytes' own).
+// compute-bound (with the read back 965 us; now 619, 479 of them the bytes' own).
 constexpr float kMagic = 12582912.f;
 DV_DEV float quant_inv(float s)  // (s lies in [2^-126, 2^121]: no subnormals)
 {

@@ -238,13 +238,14 @@ KvPlan kv_plan(int dtype, int D, int rows)
 
 // Whether units of 8 rows, which read the cache once for every 8, are the
 // faster ones for more than 8 rows.  Measured (us, units of 8 / of 64): 768
-// heads of 2112 positions of 128 values, 8 bits: 16 rows 183 / 218, 24 rows
-// 266 / 222, 40 rows 433 / 231; binary16: 12 rows 255 / 152; 120 heads of 17
-// tiles at most, 8 bits: 12 rows 23 / 37, 40 rows 30 / 44; binary16: 23 / 35,
-// 33 / 45.  So a tile of 64 positions takes the units of 8 about 3.6 (8-bit)
+// heads of 2112 positions of 128 values, 8 bits: 16 rows 169 / 173, 24 rows
+// 244 / 177, 40 rows 395 / 185; binary16: 12 rows 256 / 147; 120 heads of 17
+// tiles at most, 8 bits: 12 rows 24 / 38, 40 rows 37 / 47; binary16: 26 / 35,
+// 42 / 45.  So a tile of 64 positions takes the units of 8 about 3.6 (8-bit)
 // or 5.0 ns a pass over it and the units of 64 7.4 or 4.9 ns, and these take
 // about 15 us longer to start and to end.  The lengths are known on the device only:
-// the capacity stands for them.
+// the capacity stands for them.  What a unit costs beside its tiles is not in the
+// rule: 1024 heads of 2 tiles, binary16, 12 rows: 51 / 77, and it takes the 77.
 static bool kv_small_units(const KvAttnArgs &a)
 {
     if (const int v = g_tree_variant.load())

@@ -2,12 +2,12 @@
 // or 8-bit cache (single tokens, small trees, selected blocks) on tensor
 // cores (sm_103a).
 //
-// The arithmetic is binary32 to its last bits although the products are
-// mma.sync m16n8k16 with binary16 operands: cached keys and values are exact
-// in binary16 (8-bit codes are whole numbers; their scales multiply the
-// scores and the weights), and queries and softmax weights are split into
-// binary16 high and low parts, each scaled by a power of two so that the low
-// part keeps its bits.  The two parts of 8 rows fill the 16 rows of an MMA
+// The arithmetic is near binary32's although the products are mma.sync m16n8k16
+// with binary16 operands: cached keys and values are exact in binary16 (8-bit
+// codes are whole numbers; their scales multiply the scores and the weights),
+// and queries and softmax weights are split into binary16 high and low parts,
+// each scaled by a power of two so that the low part keeps its bits (22 of the
+// number, dv_kv_tma.cuh).  The two parts of 8 rows fill the 16 rows of an MMA
 // (rows 0-7 high, 8-15 low), and their results are added.
 //
 // Four warps take 16 positions each of a tile of 64, every warp from a ring
@@ -16,8 +16,9 @@
 // between warps until a unit ends.  What bounds it is the cache's bytes; an
 // 8-bit value costs about 0.7 instructions to become binary16, which is why
 // a warp's 16 rows are filled with both parts instead of two products.  One
-// token of 32 x 96 heads over 2049 positions: binary16 475 us, the bytes' own
-// time; 8 bits 310 us of 245, bound by those instructions and their latencies.
+// token of 32 x 96 heads over 2049 positions: binary16 473 us, the bytes' own
+// time; 8 bits 309 us of 245: 0.53 of the issue slots and 0.58 of the DRAM
+// throughput are in use, the rest is those instructions' latencies.
 //
 // Rows are swizzled by the copy, and dimensions are dealt to the fragments so
 // that a thread reads 16 contiguous bytes of a cached row at a time: the k
@@ -519,8 +520,9 @@ cudaError_t launch_d(const KvAttnArgs &a, int nsm, cudaStream_t st)
     constexpr int NST = 3 * (128 / D), MINB = I8 ? 3 : 2;
     // Units of at most FLUSH tiles have no use for the code that adds the
     // outputs up in between: 32 rows of 2049 8-bit positions of 96 heads take
-    // 310 us without it, 361 with it (binary16: 475 both).  Where it is needed, at
-    // 8000 positions of 8 rows: 329 us.
+    // 309 us without it, 360 with it (binary16: 473 and 476).  Where it is needed, at
+    // 8000 positions of 8 rows: 329 us.  (The lengths are not known here: the capacity
+    // stands for them.)
     using L = Cfg<I8, D, NST, MINB, true>;
     using S = Cfg<I8, D, NST, MINB, false>;
     const long long listed = a.idx ? (long long)a.k * a.c.block : a.c.cap;

@@ -4,14 +4,15 @@
 // A unit's 64 query rows fill an M = 128 tile with their binary16 high and
 // low parts: TMEM lanes 32 w .. 32 w + 15 hold the high parts of rows 16 w ..
 // 16 w + 15, the next 16 lanes their low parts, so the sum of the two lane
-// halves is the score to binary32's last bits, and the weights, split the
-// same way, give the value product the same accuracy.  Both products of a
-// 64-position tile of 128 dimensions take 619 tensor cycles (measured alone:
-// 384 and 256), mma.sync 2048.  64-token trees of 32 rows at the 175B shape,
-// 2048 positions: binary16 576 us, where the cache's bytes alone take 519;
-// 8 bits 724 us, where those take 282 and the tensor products 220: there the
-// 16 softmax and 8 conversion warps bound it, which fill 0.6 of the issue slots
-// and wait for one another's hand-overs in the rest.
+// halves has 22 of the query's bits, and the weights, split the same way, give
+// the value product the same accuracy.  Both products of a 64-position tile of
+// 128 dimensions take 619 tensor cycles (measured alone: 384 and 256), mma.sync
+// 2048.  64-token trees of 32 rows at the 175B shape, 2048 cached positions:
+// binary16 573 us, where the cache's bytes alone take 519; 8 bits 675 us,
+// where those take 282 and the tensor products 220.  No unit is full there (0.60
+// of the issue slots, 0.32 of the DRAM throughput, 0.30 of the tensor pipe): the
+// 16 softmax and 8 conversion warps wait for loads of tensor memory and for one
+// another's hand-overs.  Their 72 registers a thread spill 64 bytes of stores.
 //
 // Warps of a CTA (one CTA per SM):
 //   0-15      softmax: two streams that take turns at the tiles, each with its
@@ -28,9 +29,13 @@
 // MN-major operand of Q = softmax weights (A from tensor memory) x V.
 // Hand-overs are mbarriers; every wait has a limit (DV_ERR_TIMEOUT).
 //
-// A row's reference point only moves when a weight leaves binary16's range
-// (dv_kv_tma.cuh), so the output in tensor memory is rarely rescaled and a
-// tile's softmax needs no reduction over the row.
+// A row's reference point only moves when a weight of its own leaves binary16's
+// range (dv_kv_tma.cuh), so the output in tensor memory is rarely rescaled and a
+// tile's softmax needs no reduction over the row.  Scores that rise steadily
+// move their rows one after another: 64 tokens of 8 x 96 heads over 2048 8-bit
+// positions take 198 us, 252 where the scores rise by 15 and 329 where by 60
+// (binary16: 179, 195, 225).  Taking rows that are halfway to the range's end
+// every fourth tile made that 240 and 310, but the 675 us above 760.
 #include "dv_kv_tma.cuh"
 
 namespace dv {
@@ -1027,9 +1032,10 @@ template <bool I8, int D>
 cudaError_t launch_i8(const KvAttnArgs &a, int nsm, cudaStream_t st)
 {
     // A cache that holds no part of two chunks is attended without their code:
-    // 724 us against 767 for 64-token trees over 32 x 96 heads x 2048 8-bit
-    // positions (binary16: 576 both ways).  At 8000 positions of 8 rows, where
-    // they are needed, they cost 534 -> 585 us.
+    // 670 us against 730 for 64-token trees over 32 x 96 heads x 2048 cached 8-bit
+    // positions (binary16: 567 and 572).  At 8000 positions of 8 rows, where they
+    // are needed: 560 us.  (The lengths are not known here: the capacity stands
+    // for them.)
     using L = TcCfg<I8, D, true>;
     return a.c.cap > L::CHUNK * L::TP ? launch_tc<L>(a, nsm, st)
                                       : launch_tc<TcCfg<I8, D, false>>(a, nsm, st);
