@@ -155,9 +155,9 @@ DV_DEV void fma2(float &a, float &b, float c, float d)  // a c + d, b c + d
 // to scales of 2^-60, where the shift ends (it keeps l finite: 2^66 a position),
 // and no step needs a row's maximum.  (First weights taken to 2^12, nearer to
 // the end of the range, moved more often: 64-token trees of 32 x 96 heads x
-// 2048 8-bit positions 737 us against 687, rows moving together.)  m is a whole number, so that every
-// change of reference scales by a power of two, without an error.  m = -inf:
-// nothing seen yet.
+// 2048 8-bit positions 737 us against 687, rows moving together.)  m is a whole
+// number, so that every change of reference scales by a power of two, without
+// an error.  m = -inf: nothing seen yet.
 constexpr float kWeightMax = 65504.f;  // the largest binary16
 constexpr float kSumMax = 0x1p100f;  // 2^(s - m) itself must stay finite where v is tiny
 constexpr float kShiftMin = -60.f;

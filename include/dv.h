@@ -502,7 +502,8 @@ size_t dv_kv_workspace_size(const dv_kv_desc *desc, int batch, int tokens);
  * dv_kv_append -- write new keys and values, quantised for a DV_I8 cache.
  *   k, v: rows (b, t, h) of one type, t < tokens, h < n_kv_heads; token t of row b goes
  *   to position lens[b] + t, for t < n_tok[b] (n_tok [B], NULL: tokens).
- *   lens [B] device, lens[b] + n_tok[b] <= kv_cap; it is not advanced.
+ *   lens [B] device, lens[b] + n_tok[b] <= kv_cap; it is not advanced.  k and
+ *   v must not overlap the cache.
  * Rounding to binary16 is to nearest (a value above 65504 becomes infinite).
  */
 int dv_kv_append(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_rows *k,
