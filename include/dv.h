@@ -561,8 +561,9 @@ int dv_kv_keep(const dv_kv_desc *desc, const dv_kv_cache *cache, int batch, int 
  * 2^x has a relative error of up to 2^-22, and up to 128 steps that cut the sum
  * off (2^-23 each) come between binary32 additions.  This holds for
  * 8-bit value rows with scales from 2^-60 to 2^100, and rows of zeros among
- * them; smaller ones lose bits.  One launch; the order of every sum is fixed by
- * the shapes, the lengths and the device.
+ * them, and key rows with scales up to 2^98; smaller values lose bits, larger
+ * numbers overflow.  One launch; the order of every sum is fixed by the shapes,
+ * the lengths and the device.
  */
 int dv_tree_attn(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_rows *q, int batch,
                  int tokens, const int32_t *lens, const int32_t *n_tok, const uint64_t *mask,
