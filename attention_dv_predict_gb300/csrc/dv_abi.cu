@@ -1037,6 +1037,7 @@ const char *dv_status_string(int status)
     case DV_ERR_DEVICE_INDEX: return "a kernel met an index outside its range";
     case DV_ERR_SCRATCH_LIMIT:
         return "shape and batch need more scratch than dv_predict_topk_noalloc holds";
+    case DV_ERR_PAGES: return "the pool has too few free pages";
     default: return "unknown status";
     }
 }

@@ -26,12 +26,15 @@ _lib = C.CDLL(LIB_PATH)
 
 DV_OK, DV_ERR_INVALID_ARG, DV_ERR_UNSUPPORTED, DV_ERR_CUDA = 0, 1, 2, 3
 DV_ERR_TIMEOUT, DV_ERR_WORKSPACE, DV_ERR_DEVICE_INDEX, DV_ERR_SCRATCH_LIMIT = 4, 5, 6, 7
+DV_ERR_PAGES = 8
 DV_F32, DV_F16, DV_I8 = 0, 1, 2
 DV_LAYERNORM, DV_RMSNORM = 0, 1
 DV_MLP_RELU, DV_MLP_SWIGLU = 0, 1
 DV_MAX_BATCH = 32
 DV_KV_MAX_BATCH = 256
 DV_TREE_MAX_TOKENS = 64
+DV_SEQ_MAX_BATCH = 1024
+DV_ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "ramp": 3, "ramp_index": 4}
 
 WEIGHT_FIELDS = ("ln1_g", "ln1_b", "w_qkv", "b_qkv", "w_oT", "b_o", "ln2_g", "ln2_b",
                  "w1", "b1", "w2T", "b2", "pred_h", "pred_a", "pred_b")
@@ -67,6 +70,21 @@ class KvRows(C.Structure):
                 ("stride_t", C.c_int64), ("stride_h", C.c_int64)]
 
 
+class SeqDesc(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("n_heads", "n_kv_heads", "head_dim", "dtype", "page",
+                                         "n_pages")]
+
+
+class PagePoolPointers(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p)]
+
+
+class RopeParams(C.Structure):
+    _fields_ = [("steps", C.c_void_p), ("rot_dim", C.c_int32), ("interleaved", C.c_int32),
+                ("mscale", C.c_float), ("norm", C.c_int32), ("eps", C.c_float),
+                ("q_gain", C.c_void_p), ("k_gain", C.c_void_p)]
+
+
 _P = C.c_void_p
 _I = C.c_int
 _SZ = C.c_size_t
@@ -76,6 +94,9 @@ _S = C.POINTER(Selection)
 _KD = C.POINTER(KvDesc)
 _KC = C.POINTER(KvCachePointers)
 _KR = C.POINTER(KvRows)
+_QD = C.POINTER(SeqDesc)
+_QP = C.POINTER(PagePoolPointers)
+_DB = C.c_double
 
 _SIGS = {
     "dv_status_string": ([_I], C.c_char_p),
@@ -115,6 +136,14 @@ _SIGS = {
                      _I),
     "dv_block_topk": ([_KD, _KC, _KR, _I, _P, _I, _I, _I, _P, _P, _SZ, _P], _I),
     "dv_block_attn": ([_KD, _KC, _KR, _I, _P, _P, _I, C.c_float, _P, _P, _SZ, _P], _I),
+    "dv_seq_workspace_size": ([_QD], _SZ),
+    "dv_page_release": ([_QD, _I, _P, _P, _I, _P, _P, _P, _P, _P, _SZ, _P], _I),
+    "dv_page_take": ([_QD, _I, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P, _SZ, _P], _I),
+    "dv_rope_steps": ([_I, _DB, _I, _DB, _DB, _DB, _DB, _P], _I),
+    "dv_qk_rope": ([_QD, C.POINTER(RopeParams), _I, _P, _KR, _KR, _KR, _KR, _KR, _QP, _P, _P, _SZ,
+                    _P], _I),
+    "dv_prompt_attn": ([_QD, _I, _I, _I, _KR, _KR, _KR, _P, C.c_float, _P, _P, _SZ, _P], _I),
+    "dv_paged_attn": ([_QD, _QP, _I, _I, _I, _KR, _P, _P, _P, _I, C.c_float, _P, _P, _SZ, _P], _I),
 }
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -634,3 +663,255 @@ def dv_block_attn(cache: KvCache, q: torch.Tensor, lens: torch.Tensor, idx: torc
         _kv_tensor("idx", idx, cache, (B, d.n_heads, k), torch.int32), k,
         d.head_dim ** -0.5 if scale is None else scale,
         _kv_tensor("out", out, cache, shape, torch.float32), ws.ptr, ws.nbytes, st))
+
+
+# ---------------------------------------------------------------------------
+# Packed sequences and paged caches.
+
+
+def make_seq_desc(n_heads, n_kv_heads, head_dim, dtype, page=0, n_pages=0) -> SeqDesc:
+    return SeqDesc(n_heads, n_kv_heads, head_dim, dtype, page, n_pages)
+
+
+def seq_workspace_size(desc: SeqDesc) -> int:
+    return int(_lib.dv_seq_workspace_size(C.byref(desc)))
+
+
+class SeqWorkspace(Workspace):
+    """Device workspace of the operators over packed sequences, zeroed once; any batch and length."""
+
+    def __init__(self, desc: SeqDesc, device=None, stream=None):
+        n = seq_workspace_size(desc)
+        if n == 0:
+            raise DvError("dv_seq_workspace_size", DV_ERR_INVALID_ARG)
+        self.buf = torch.empty(n + 256, dtype=torch.uint8, device=device or "cuda")
+        self.device = self.buf.device
+        self.device_index = self.buf.get_device()
+        off = (-self.buf.data_ptr()) % 256
+        self.ptr = self.buf.data_ptr() + off
+        self.nbytes = n
+        with torch.cuda.device(self.device):
+            _check("dv_workspace_init", _lib.dv_workspace_init(C.c_void_p(self.ptr), n,
+                                                                _stream(stream)))
+
+
+class _SeqTensors:
+    """Tensors of given shapes and types on one device, as attributes (``tensors``: these)."""
+
+    def _take(self, want, device, tensors, made):
+        if tensors is None:
+            tensors = made(device or "cuda")
+        if set(tensors) != set(want):
+            raise ValueError(f"the tensors are {sorted(want)}, got {sorted(tensors)}")
+        first = next(iter(tensors.values()))
+        self.device, self.device_index = first.device, first.get_device()
+        for n, (shape, dt) in want.items():
+            t = tensors[n]
+            if (tuple(t.shape) != shape or t.dtype != dt or not t.is_cuda
+                    or not t.is_contiguous() or t.device != self.device):
+                raise ValueError(f"{n} must be a contiguous CUDA tensor {shape} of {dt} on one "
+                                 "device")
+            setattr(self, n, t)
+
+
+class PagedCache(_SeqTensors):
+    """A pool of pages, ``k`` and ``v`` [n_pages, Hkv, page, D], plus the C struct pointing at
+    them.  ``tensors``: use these instead of allocating (zeroed) ones."""
+
+    def __init__(self, desc: SeqDesc, device=None, tensors: Optional[Dict[str, torch.Tensor]] = None):
+        if seq_workspace_size(desc) == 0 or not desc.page:
+            raise DvError("dv_seq_workspace_size", DV_ERR_INVALID_ARG)
+        self.desc = desc
+        shape = (desc.n_pages, desc.n_kv_heads, desc.page, desc.head_dim)
+        dt = _TORCH_DTYPE[desc.dtype]
+        self._take({"k": (shape, dt), "v": (shape, dt)}, device, tensors,
+                   lambda dev: {n: torch.zeros(shape, dtype=dt, device=dev) for n in ("k", "v")})
+        self.c = PagePoolPointers(self.k.data_ptr(), self.v.data_ptr())
+
+
+class PageTables(_SeqTensors):
+    """Block tables of ``batch`` requests (``tables`` [batch, max_pages]) and the stack of free
+    pages (``free`` [n_pages], ``n_free`` [1]), int32; all pages free at first.  ``tensors``: use
+    these."""
+
+    def __init__(self, desc: SeqDesc, batch: int, max_pages: int, device=None,
+                 tensors: Optional[Dict[str, torch.Tensor]] = None):
+        if seq_workspace_size(desc) == 0 or not desc.page:
+            raise DvError("dv_seq_workspace_size", DV_ERR_INVALID_ARG)
+        self.desc, self.batch, self.max_pages = desc, batch, max_pages
+        n, i32 = desc.n_pages, torch.int32
+        self._take({"tables": ((batch, max_pages), i32), "free": ((n,), i32),
+                    "n_free": ((1,), i32)}, device, tensors, lambda dev: {
+                        "tables": torch.full((batch, max_pages), -1, dtype=i32, device=dev),
+                        "free": torch.arange(n - 1, -1, -1, dtype=i32, device=dev),
+                        "n_free": torch.full((1,), n, dtype=i32, device=dev)})
+
+
+class Rope:
+    """Per-head norms and position rotation as dv_qk_rope takes them.
+
+    rot_dim: the first values of a head that turn (0: none).  scaling: "none", "linear", "base",
+    "ramp" or "ramp_index" (dv.h); mscale: a factor of sines and cosines.  q_gain, k_gain:
+    float32 [head_dim], or None for no norm.  steps: these angles (int64 [rot_dim / 2], units of
+    2^-64 turns a position) instead of those of theta and scaling."""
+
+    def __init__(self, head_dim: int, rot_dim: int, interleaved: bool = False,
+                 theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                 orig_len: float = 0.0, low: float = 1.0, high: float = 32.0, mscale: float = 1.0,
+                 norm: int = DV_RMSNORM, eps: float = 1e-6, q_gain: Optional[torch.Tensor] = None,
+                 k_gain: Optional[torch.Tensor] = None, steps: Optional[torch.Tensor] = None,
+                 device=None):
+        self.head_dim, self.rot_dim = head_dim, rot_dim
+        gains = [t for t in (q_gain, k_gain) if t is not None]
+        dev = torch.device(device) if device is not None else gains[0].device if gains else \
+            torch.device("cuda", torch.cuda.current_device())
+        if steps is None and rot_dim:
+            host = (C.c_uint64 * max(1, rot_dim // 2))()
+            _check("dv_rope_steps", _lib.dv_rope_steps(
+                rot_dim, theta, DV_ROPE_SCALING[scaling], factor, orig_len, low, high, host))
+            steps = torch.tensor([v - (1 << 64) if v >> 63 else v for v in host],
+                                 dtype=torch.int64).to(dev)
+        self.steps, self.q_gain, self.k_gain = steps, q_gain, k_gain
+        for n, t, shape, dt in (("steps", steps, (rot_dim // 2,), torch.int64),
+                                ("q_gain", q_gain, (head_dim,), torch.float32),
+                                ("k_gain", k_gain, (head_dim,), torch.float32)):
+            if t is not None and (tuple(t.shape) != shape or t.dtype != dt or not t.is_cuda
+                                  or not t.is_contiguous() or t.device != dev):
+                raise ValueError(f"{n} must be a contiguous CUDA tensor {shape} of {dt} on one "
+                                 "device")
+        self.device_index = dev.index
+        ptr = [None if t is None else t.data_ptr() for t in (steps, q_gain, k_gain)]
+        self.c = RopeParams(ptr[0], rot_dim, int(interleaved), mscale, norm, eps, ptr[1], ptr[2])
+
+
+def _seq_dev(ws: SeqWorkspace, stream, *others) -> int:
+    """The stream of a call; its device must be the workspace's, the others' and the current one."""
+    dev = ws.device_index
+    for o in others:
+        if o is not None and o.device_index != dev:
+            raise ValueError("the workspace is on another device")
+    if torch.cuda.current_device() != dev:
+        raise ValueError("the workspace is not on the current device (torch.cuda.device)")
+    if stream is None:
+        return _raw_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError("the stream is not of the workspace's device")
+    return stream.cuda_stream
+
+
+def _seq_tensor(name: str, t: torch.Tensor, ws: SeqWorkspace, shape, dtype=torch.int32):
+    if (t.dtype != dtype or t.shape != shape or not t.is_contiguous()
+            or t.get_device() != ws.device_index):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on the "
+                         "workspace's device")
+    return t.data_ptr()
+
+
+def _seq_rows(name: str, t: torch.Tensor, ws: SeqWorkspace, shape):
+    dt = _ROW_DTYPE.get(t.dtype)
+    if dt is None or t.shape != shape or t.get_device() != ws.device_index or t.stride(2) != 1:
+        raise ValueError(f"{name} must be a float32 or float16 tensor {shape} on the workspace's "
+                         "device, contiguous in its last dimension")
+    s = t.stride()
+    # (a dimension of one row is never stepped over: its stride says nothing)
+    return C.byref(KvRows(t.data_ptr(), dt, 0, s[0] if shape[0] > 1 else 0,
+                          s[1] if shape[1] > 1 else 0))
+
+
+def dv_page_release(pt: PageTables, lens: torch.Tensor, done: torch.Tensor, ws: SeqWorkspace,
+                    n_free_out: Optional[torch.Tensor] = None, stream=None):
+    """Push the pages of the requests with done[b] != 0 (lens, done [B] int32) on the stack.
+
+    n_free_out: where the new count goes (pt.n_free by default)."""
+    st = _seq_dev(ws, stream, pt)
+    B, out = pt.batch, pt.n_free if n_free_out is None else n_free_out
+    _check("dv_page_release", _lib.dv_page_release(
+        C.byref(pt.desc), B, _seq_tensor("lens", lens, ws, (B,)),
+        _seq_tensor("done", done, ws, (B,)), pt.max_pages, pt.tables.data_ptr(),
+        pt.free.data_ptr(), pt.n_free.data_ptr(), _seq_tensor("n_free_out", out, ws, (1,)),
+        ws.ptr, ws.nbytes, st))
+
+
+def dv_page_take(pt: PageTables, lens: torch.Tensor, n_tok: torch.Tensor, cu: torch.Tensor,
+                 pos: torch.Tensor, slots: torch.Tensor, ws: SeqWorkspace,
+                 n_free: Optional[torch.Tensor] = None,
+                 n_free_out: Optional[torch.Tensor] = None, stream=None):
+    """Pages for n_tok[b] new tokens behind lens[b]; cu [B + 1], pos and slots [max_tokens] int32.
+
+    n_free, n_free_out: the count before and after (pt.n_free by default)."""
+    st = _seq_dev(ws, stream, pt)
+    B, T = pt.batch, _kv_dim("pos", pos, 1, 0)
+    before = pt.n_free if n_free is None else n_free
+    after = pt.n_free if n_free_out is None else n_free_out
+    _check("dv_page_take", _lib.dv_page_take(
+        C.byref(pt.desc), B, _seq_tensor("lens", lens, ws, (B,)),
+        _seq_tensor("n_tok", n_tok, ws, (B,)), pt.max_pages, pt.tables.data_ptr(),
+        pt.free.data_ptr(), _seq_tensor("n_free", before, ws, (1,)),
+        _seq_tensor("n_free_out", after, ws, (1,)), _seq_tensor("cu", cu, ws, (B + 1,)),
+        _seq_tensor("pos", pos, ws, (T,)), _seq_tensor("slots", slots, ws, (T,)), T, ws.ptr,
+        ws.nbytes, st))
+
+
+def dv_qk_rope(rope: Rope, q: torch.Tensor, k: torch.Tensor, pos: torch.Tensor, ws: SeqWorkspace,
+               q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+               v: Optional[torch.Tensor] = None, cache: Optional[PagedCache] = None,
+               slots: Optional[torch.Tensor] = None, desc: Optional[SeqDesc] = None, stream=None):
+    """Normalise and rotate q [T, H, D] and k [T, Hkv, D] at positions pos [T] (int32).
+
+    q_out (q itself by default) and k_out get the rows; with a cache, k and v [T, Hkv, D] go to
+    slots [T] of it, and k_out may be left out (without one: k itself by default)."""
+    st = _seq_dev(ws, stream, rope, cache)
+    T, H, D = (_kv_dim("q", q, 3, i) for i in range(3))
+    Hkv = _kv_dim("k", k, 3, 1)
+    if desc is None:
+        desc = cache.desc if cache is not None else make_seq_desc(H, Hkv, D, DV_F32 if D <= 128
+                                                                  else DV_F16)
+    if D != rope.head_dim or (H, Hkv, D) != (desc.n_heads, desc.n_kv_heads, desc.head_dim):
+        raise ValueError("q, k, the rotation and the descriptor differ in heads or head size")
+    if (cache is None) != (slots is None) or (v is not None and cache is None):
+        raise ValueError("a cache, slots and v go together")
+    q_out = q if q_out is None else q_out
+    if k_out is None and cache is None:
+        k_out = k
+    _check("dv_qk_rope", _lib.dv_qk_rope(
+        C.byref(desc), C.byref(rope.c), T, _seq_tensor("pos", pos, ws, (T,)),
+        _seq_rows("q", q, ws, (T, H, D)), _seq_rows("k", k, ws, (T, Hkv, D)),
+        None if v is None else _seq_rows("v", v, ws, (T, Hkv, D)),
+        _seq_rows("q_out", q_out, ws, (T, H, D)),
+        None if k_out is None else _seq_rows("k_out", k_out, ws, (T, Hkv, D)),
+        None if cache is None else C.byref(cache.c),
+        None if slots is None else _seq_tensor("slots", slots, ws, (T,)), ws.ptr, ws.nbytes, st))
+
+
+def dv_prompt_attn(desc: SeqDesc, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                   cu: torch.Tensor, out: torch.Tensor, ws: SeqWorkspace,
+                   max_tok: Optional[int] = None, scale: Optional[float] = None, stream=None):
+    """Causal attention of packed prompts: q, out [T, H, D], k, v [T, Hkv, D], cu [B + 1] (int32).
+
+    max_tok: the most tokens of a request (T by default); scale: head_dim ** -0.5 by default."""
+    st = _seq_dev(ws, stream)
+    T, B = _kv_dim("q", q, 3, 0), _kv_dim("cu", cu, 1, 0) - 1
+    shape, kv = (T, desc.n_heads, desc.head_dim), (T, desc.n_kv_heads, desc.head_dim)
+    _check("dv_prompt_attn", _lib.dv_prompt_attn(
+        C.byref(desc), B, T, T if max_tok is None else max_tok, _seq_rows("q", q, ws, shape),
+        _seq_rows("k", k, ws, kv), _seq_rows("v", v, ws, kv), _seq_tensor("cu", cu, ws, (B + 1,)),
+        desc.head_dim ** -0.5 if scale is None else scale,
+        _seq_tensor("out", out, ws, shape, _TORCH_DTYPE[desc.dtype]), ws.ptr, ws.nbytes, st))
+
+
+def dv_paged_attn(cache: PagedCache, q: torch.Tensor, cu: torch.Tensor, lens: torch.Tensor,
+                  tables: torch.Tensor, out: torch.Tensor, ws: SeqWorkspace,
+                  max_tok: Optional[int] = None, scale: Optional[float] = None, stream=None):
+    """Causal attention of new tokens q [T, H, D] over their requests' pages, into out [T, H, D].
+
+    cu [B + 1], lens [B], tables [B, max_pages] int32; max_tok, scale as dv_prompt_attn's."""
+    d = cache.desc
+    st = _seq_dev(ws, stream, cache)
+    T, B, P = _kv_dim("q", q, 3, 0), _kv_dim("cu", cu, 1, 0) - 1, _kv_dim("tables", tables, 2, 1)
+    shape = (T, d.n_heads, d.head_dim)
+    _check("dv_paged_attn", _lib.dv_paged_attn(
+        C.byref(d), C.byref(cache.c), B, T, T if max_tok is None else max_tok,
+        _seq_rows("q", q, ws, shape), _seq_tensor("cu", cu, ws, (B + 1,)),
+        _seq_tensor("lens", lens, ws, (B,)), _seq_tensor("tables", tables, ws, (B, P)), P,
+        d.head_dim ** -0.5 if scale is None else scale,
+        _seq_tensor("out", out, ws, shape, _TORCH_DTYPE[d.dtype]), ws.ptr, ws.nbytes, st))

@@ -70,7 +70,8 @@ typedef enum {
     DV_ERR_TIMEOUT = 4,      /* a bounded device-side wait gave up */
     DV_ERR_WORKSPACE = 5,    /* workspace missing, misaligned or too small */
     DV_ERR_DEVICE_INDEX = 6, /* a kernel met an index outside its range (skipped) */
-    DV_ERR_SCRATCH_LIMIT = 7 /* dv_predict_topk_noalloc: shape needs more than its scratch */
+    DV_ERR_SCRATCH_LIMIT = 7, /* dv_predict_topk_noalloc: shape needs more than its scratch */
+    DV_ERR_PAGES = 8         /* dv_page_take: the pool has too few free pages */
 } dv_status;
 
 /* DV_I8 is a storage type of the KV-cache operators (dv_kv_desc) alone. */
@@ -609,6 +610,174 @@ int dv_block_topk(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_
 int dv_block_attn(const dv_kv_desc *desc, const dv_kv_cache *cache, const dv_kv_rows *q, int batch,
                   const int32_t *lens, const int32_t *idx, int k_blocks, float scale, float *out,
                   void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Packed sequences and paged caches: what a serving step does with prompts and
+ * with requests that share one pool of pages.  The new tokens of B requests lie
+ * one behind the other, request b's at rows cu[b] .. cu[b + 1] - 1 (cu [B + 1],
+ * device), any number of them from none to a whole prompt; request b has
+ * lens[b] cached positions before them.  They are an addition of this library;
+ * the DejaVu pages have no counterpart.
+ *
+ * The conventions at the top of this file hold; the workspace is one of
+ * dv_seq_workspace_size() bytes, zeroed once with dv_workspace_init() and read
+ * by dv_check().  It serves calls of any batch and length, one after another;
+ * calls, or graphs that hold them, that may run at the same time need one each.
+ * Query heads share KV heads in groups of n_heads / n_kv_heads.
+ *
+ * Device-side checks: a request whose offsets, length or token count are out of
+ * range is skipped, what it would write is left as it was, and
+ * DV_ERR_DEVICE_INDEX is recorded in the status word.  A page number out of
+ * range in a block table is recorded too: dv_page_take gives its tokens slot
+ * -1, dv_paged_attn reads its positions as zeros.
+ *
+ * Pool: k, v [n_pages, Hkv, page, D] in desc.dtype: position p of request b and
+ * head h is row p % page of (tables[b][p / page], h).  Block tables: tables [B,
+ * max_pages] page numbers, of which the first ceil(length / page) of a row
+ * count; max_pages x page <= 2^30.  Slot of a token: page number x page + row.
+ */
+#define DV_SEQ_MAX_BATCH 1024
+
+typedef struct {
+    int32_t n_heads;    /* query heads: a multiple of n_kv_heads, at most 256 */
+    int32_t n_kv_heads;
+    int32_t head_dim;   /* power of two, 8 to 256, at most 512 bytes */
+    int32_t dtype;      /* DV_F32 or DV_F16 */
+    int32_t page;       /* positions a page: 16, 32, 64 or 128; 0: no pool (dv_qk_rope to rows,
+                         * dv_prompt_attn) */
+    int32_t n_pages;    /* pages of the pool, n_pages x page <= 2^30 (0 without a pool) */
+} dv_seq_desc;
+
+typedef struct {
+    void *k, *v;
+} dv_page_pool;
+
+/* Bytes of workspace of the calls below.  0 if invalid. */
+size_t dv_seq_workspace_size(const dv_seq_desc *desc);
+
+/*
+ * dv_page_release -- give back the pages of requests that have finished.
+ *   free_pages [n_pages] device: a stack of page numbers, n_free[0] of them.
+ *   done [B]: of requests with done[b] != 0 the pages of their first lens[b]
+ *   positions are pushed, in the order of the requests and positions;
+ *   n_free_out[0] (may be n_free) gets the new count.  tables and lens stay as
+ *   they are.  A request with a page number out of range, or whose pages would
+ *   not fit the stack, is skipped and recorded (DV_ERR_DEVICE_INDEX).
+ */
+int dv_page_release(const dv_seq_desc *desc, int batch, const int32_t *lens, const int32_t *done,
+                    int max_pages, const int32_t *tables, int32_t *free_pages,
+                    const int32_t *n_free, int32_t *n_free_out, void *ws, size_t ws_bytes,
+                    void *stream);
+
+/*
+ * dv_page_take -- block tables and slots for n_tok[b] new tokens a request.
+ *   Request b needs ceil((lens[b] + n_tok[b]) / page) - ceil(lens[b] / page) new
+ *   pages; they are popped from the stack (free_pages, n_free as above) in the
+ *   order of the requests and written behind the first ceil(lens[b] / page)
+ *   entries of its table; n_free_out[0] (may be n_free) gets the new count.
+ *   lens is not advanced.
+ *   cu [B + 1]: offsets of the packed tokens; pos [max_tokens], slots
+ *   [max_tokens]: each token's position and slot, -1 behind the last one.
+ *   A request that the stack has too few pages for, those before it served,
+ *   takes none: its tokens keep their places with slot -1, and DV_ERR_PAGES is
+ *   recorded.  A request out of range (lens[b] + n_tok[b] > max_pages x page)
+ *   counts as one of no tokens.  Offsets stop at max_tokens (recorded).
+ */
+int dv_page_take(const dv_seq_desc *desc, int batch, const int32_t *lens, const int32_t *n_tok,
+                 int max_pages, int32_t *tables, const int32_t *free_pages, const int32_t *n_free,
+                 int32_t *n_free_out, int32_t *cu, int32_t *pos, int32_t *slots, int max_tokens,
+                 void *ws, size_t ws_bytes, void *stream);
+
+/* How positions are scaled for contexts longer than the trained one.  With f_i
+ * = theta^(-2 i / rot_dim) the angle of pair i per position:
+ *   DV_ROPE_NONE    f_i
+ *   DV_ROPE_LINEAR  f_i / factor
+ *   DV_ROPE_BASE    f_i of theta factor^(rot_dim / (rot_dim - 2))
+ *   DV_ROPE_RAMP    f_i (w + (1 - w) / factor), w rising from 0 to 1 as the
+ *                   turns over the trained length, orig_len f_i / 2 pi, rise
+ *                   from low to high
+ *   DV_ROPE_RAMP_INDEX  the same with w falling from 1 to 0 as i rises from
+ *                   floor(dim(high)) to ceil(dim(low)) (held within 0 ..
+ *                   rot_dim - 1), dim(r) = rot_dim ln(orig_len / 2 pi r) / (2 ln
+ *                   theta): the pair that makes r turns */
+typedef enum {
+    DV_ROPE_NONE = 0,
+    DV_ROPE_LINEAR = 1,
+    DV_ROPE_BASE = 2,
+    DV_ROPE_RAMP = 3,
+    DV_ROPE_RAMP_INDEX = 4
+} dv_rope_scaling;
+
+/* The angles as the kernel takes them, turns per position in units of 2^-64:
+ * steps (HOST) [rot_dim / 2], to be copied to the device once.  An angle is the
+ * product with the position modulo 2^64, so it is as exact at position 2^30 as
+ * at the first.  theta > 1, 1 <= factor, orig_len, low < high where used. */
+int dv_rope_steps(int rot_dim, double theta, int scaling, double factor, double orig_len,
+                  double low, double high, uint64_t *steps);
+
+typedef struct {
+    const uint64_t *steps;  /* [rot_dim / 2] device (any angles of at most half a turn a position) */
+    int32_t rot_dim;        /* even, 0 (no rotation) to head_dim: the first rot_dim values turn */
+    int32_t interleaved;    /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2 i, 2 i + 1) */
+    float mscale;           /* factor of sines and cosines (1 unless the scaling has one) */
+    int32_t norm;           /* dv_norm, over a head's D values, where there are gains */
+    float eps;              /* > 0 */
+    const float *q_gain, *k_gain;  /* [head_dim] device; NULL: queries (keys) as they are */
+} dv_rope;
+
+/*
+ * dv_qk_rope -- normalise and rotate the queries and keys of packed tokens, and
+ * store keys and values in the pool, in one pass.
+ *   q, k, v: rows (t, h) (stride_b is not used), t < tokens; v NULL: no values.
+ *   pos [tokens] device: positions; a token with a negative one is skipped.
+ *   x' = x / sqrt(mean(x^2) + eps) gain (DV_LAYERNORM: of x less its mean), then
+ *   each pair turns by its angle: (a, b) -> (a cos - b sin, b cos + a sin).
+ *   q_out: rows of the queries; may be q itself (same place, type, strides).
+ *   k_out: rows of the keys, or NULL; may be k.  pool, slots [tokens]: where keys
+ *   and values go (NULL: nowhere); a negative slot takes nothing, one out of
+ *   range neither (recorded).  v goes to the pool alone, as it is.
+ * Outputs otherwise overlap nothing.  Arithmetic is binary32, angles are exact
+ * to 2^-31 of a turn; a row is rounded once, when it is stored.
+ */
+int dv_qk_rope(const dv_seq_desc *desc, const dv_rope *rope, int tokens, const int32_t *pos,
+               const dv_kv_rows *q, const dv_kv_rows *k, const dv_kv_rows *v,
+               const dv_kv_rows *q_out, const dv_kv_rows *k_out, const dv_page_pool *pool,
+               const int32_t *slots, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * dv_prompt_attn -- causal attention of packed prompts over themselves.
+ *   q, k, v: rows (t, h) of desc.dtype, t < tokens (strides of rows that differ
+ *   are at least D).  cu [batch + 1]: request b has rows cu[b] .. cu[b + 1] - 1,
+ *   0 <= cu[b] <= cu[b + 1] <= tokens, at most max_tok of them.
+ *   out [tokens, n_heads, D] of desc.dtype:
+ *     out[cu[b] + i, h] = sum_{j <= i} softmax_j(scale q_i . k_j) v_j
+ *   Rows of no request are left as they were.  scale log2(e): a positive normal
+ *   number.
+ * A row's result depends on the rows it sees alone, whatever others hold; a
+ * value row that it sees and that holds a NaN or an infinity, or a key row with
+ * a NaN, makes the result non-finite (every value of it, or that dimension's).
+ * Scores, weights, sums and outputs are held in binary32, and a result is rounded
+ * once.  The order of every sum is fixed by the shapes, the
+ * lengths and the device.
+ */
+int dv_prompt_attn(const dv_seq_desc *desc, int batch, int tokens, int max_tok,
+                   const dv_kv_rows *q, const dv_kv_rows *k, const dv_kv_rows *v,
+                   const int32_t *cu, float scale, void *out, void *ws, size_t ws_bytes,
+                   void *stream);
+
+/*
+ * dv_paged_attn -- causal attention of every request's new tokens over its
+ * pages.  Their own keys and values are in the pool already, at positions
+ * lens[b] + i (dv_qk_rope); one token a request is decode attention.
+ *   q: rows (t, h) of desc.dtype; cu, max_tok, scale, out as dv_prompt_attn's;
+ *   lens [batch], tables [batch, max_pages]; lens[b] + count <= max_pages x page.
+ *     out[cu[b] + i, h] = sum_{p <= lens[b] + i} softmax_p(scale q_i . k_p) v_p
+ * Arithmetic and what cannot change a result as dv_prompt_attn's.
+ */
+int dv_paged_attn(const dv_seq_desc *desc, const dv_page_pool *pool, int batch, int tokens,
+                  int max_tok, const dv_kv_rows *q, const int32_t *cu, const int32_t *lens,
+                  const int32_t *tables, int max_pages, float scale, void *out, void *ws,
+                  size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }
