@@ -8,7 +8,8 @@
 namespace dv {
 
 constexpr int kSeqMaxCtas = 608;   // attention CTAs on CUDA cores (four per SM of 152)
-constexpr int kSeqGenRows = 32;    // their query rows a unit
+constexpr int kSeqTcCtas = 152;    // tensor-core attention CTAs (one per SM)
+constexpr int kSeqGenRows = 32;    // the CUDA-core kernel's query rows a unit
 constexpr int kSeqGenTile = 64;    // and cached positions a tile
 
 // Workspace: the status word's line, counters (zero at rest), then records of
@@ -76,5 +77,7 @@ cudaError_t launch_page_take(const SeqTakeArgs &a, cudaStream_t st);
 cudaError_t launch_qk_rope(const SeqRopeArgs &a, cudaStream_t st);
 cudaError_t launch_seq_attn(const SeqAttnArgs &a, int nsm, cudaStream_t st);
 size_t seq_attn_record_bytes(int D);
+cudaError_t launch_seq_tc(const SeqAttnArgs &a, int nsm, cudaStream_t st);
+size_t seq_tc_record_bytes(int D);
 
 }  // namespace dv

@@ -29,14 +29,21 @@ dv_status check_desc(const dv_seq_desc *D)
         return DV_ERR_UNSUPPORTED;
     if (D->page && D->page != 16 && D->page != 32 && D->page != 64 && D->page != 128)
         return DV_ERR_UNSUPPORTED;
-    if ((long long)D->n_pages * D->page > 1 << 30)
+    // (page numbers times heads are a 32-bit coordinate of the copies)
+    if ((long long)D->n_pages * D->page > 1 << 30 ||
+        (long long)D->n_pages * D->n_kv_heads > INT_MAX)
         return DV_ERR_UNSUPPORTED;
     return DV_OK;
 }
 
+// Binary16 rows of 64 and 128 values run on tensor cores.
+bool on_tc(int f16, int D) { return f16 && (D == 64 || D == 128); }
+
 size_t seq_ws_bytes(const dv_seq_desc &D)
 {
-    return (kSeqRecOff + seq_attn_record_bytes(D.head_dim) + 255) / 256 * 256;
+    const size_t rec = on_tc(D.dtype == DV_F16, D.head_dim) ? seq_tc_record_bytes(D.head_dim)
+                                                            : seq_attn_record_bytes(D.head_dim);
+    return (kSeqRecOff + rec + 255) / 256 * 256;
 }
 
 dv_status check_ws(const dv_seq_desc &D, void *ws, size_t ws_bytes)
@@ -128,8 +135,8 @@ dv_status attn_launch(SeqAttnArgs &a, void *stream)
     if (cuda_failed(cudaGetDevice(&dev)) ||
         cuda_failed(cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev)))
         return DV_ERR_CUDA;
-    seq_group(a, kSeqGenRows);
-    return cuda_status(launch_seq_attn(a, nsm, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(on_tc(a.f16, a.D) ? launch_seq_tc(a, nsm, st) : launch_seq_attn(a, nsm, st));
 }
 
 double dim_of_turns(double turns, int rot, double theta, double orig)

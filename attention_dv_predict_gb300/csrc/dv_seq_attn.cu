@@ -218,8 +218,9 @@ __global__ void __launch_bounds__(256) k_seq_attn(const SeqAttnArgs a)
 }
 
 template <typename T, int D>
-cudaError_t launch_gen(const SeqAttnArgs &a, int nsm, cudaStream_t st)
+cudaError_t launch_gen(SeqAttnArgs a, int nsm, cudaStream_t st)
 {
+    seq_group(a, RM);
     auto kern = k_seq_attn<T, D>;
     constexpr size_t smem = GenSmem<T, D>::BYTES;
     static DeviceOnce once;

@@ -1,0 +1,912 @@
+// dv_seq_tc.cu -- causal attention of packed sequences on tcgen05 (sm_103a):
+// binary16 rows of 64 or 128 values, packed or in pages.
+//
+// A unit's query rows fill one or two M = 128 tiles.  Two streams of softmax,
+// four warps each with a row a thread, keep the tensor cores busy in turn:
+// while one weighs a tile of 128 positions, the other's products run.  A unit
+// of two tiles (a pair: prompts, chunks) gives each stream its own rows and the
+// same positions; a unit of one (decode, a chunk's end) gives both the same
+// rows and every other tile of positions, and they are merged when it ends.
+// Scores lie in tensor memory, the weights (binary16) take their place as the
+// A operand of the value product, and the outputs are summed there in binary32.
+//
+// Warps of a CTA (one CTA per SM):
+//   0-3, 4-7  softmax of stream 0, 1
+//   8         copies of keys and values: a ring of 128-position tiles; of a paged
+//             cache a lane a page, the page numbers a tile ahead
+//   9         the products (one thread issues them)
+//   10        copies of queries
+//   11        takes NaN and infinities out of value rows that some row of the
+//             unit does not see (only the last tiles hold any)
+// Hand-overs are mbarriers; every wait has a limit (DV_ERR_TIMEOUT).
+//
+// A row's reference point m stands in for its running maximum: weights are
+// 2^(s - m) with m a whole number 6 below the first tile's maximum, and m moves
+// (for this row alone) when a weight would pass 2^15, near the end of binary16's
+// range.  So the outputs are rarely rescaled, and a tile is read from tensor
+// memory once, its maximum formed beside the weights.
+#include <cudaTypedefs.h>
+
+#include "dv_kv_tma.cuh"
+#include "dv_seq_sched.cuh"
+
+namespace dv {
+namespace {
+
+struct SeqMaps {
+    CUtensorMap q, k, v;
+};
+
+template <int D_>
+struct SeqTcCfg {
+    static constexpr int D = D_, TP = 128, RM = 128;
+    static constexpr int TILE = TP * D * 2;              // a tile of keys, values or queries
+    static constexpr int HALF = TP * 128;                // 64 dimensions of it
+    static constexpr int NST = D == 128 ? 5 : 10;        // ring stages
+    static constexpr int THREADS = 384;
+    static constexpr int OFF_KV = 2 * TILE, OFF_CTL = OFF_KV + NST * TILE;
+    static constexpr int T_S = 0, T_O = 256, T_COLS = 512;  // tensor-memory columns
+    static constexpr int REC = 2 * RM * D + 4 * RM;      // floats of a piece's record
+    using Sched = SeqSched<TP, true, 3, 8>;
+};
+
+// Control block behind the ring.
+struct SeqCtl {
+    SeqSmem sched;
+    uint64_t full[10], empty[10], s_full[2], p_full[2], o_full[2], q_full[2];
+    uint64_t q_free[2];          // a unit's score products are done
+    uint64_t x_free[2];          // a unit of one tile no longer uses the queries' place
+    uint64_t v_req[4], v_ok[4];  // edge tiles, by their number modulo 4
+    uint64_t end;
+    float m[2][128], l[2][128];  // exchange of a unit of one tile
+    unsigned bad[4][4];          // positions of an edge tile that were not finite
+    int last[2];
+    unsigned tmem;
+};
+
+DV_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+DV_DEV void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+DV_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Shared-memory matrix descriptor, 128-byte swizzle: 8-row groups 1024 bytes
+// apart; lbo: bytes between 64-element blocks of an MN-major operand.
+DV_DEV uint64_t tc_desc(unsigned saddr, unsigned lbo)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// kind::f16, f32 accumulate, M = 128, N columns; tb: B is MN-major.
+__host__ __device__ constexpr uint32_t tc_idesc(int N, bool tb)
+{
+    return (1u << 4) | (tb ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(128 >> 4) << 24);
+}
+DV_DEV void tc_mma_ss(unsigned d, uint64_t ad, uint64_t bd, uint32_t idesc, bool acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"((int)acc)
+        : "memory");
+}
+DV_DEV void tc_mma_ts(unsigned d, unsigned a, uint64_t bd, uint32_t idesc, bool acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bd), "r"(idesc), "r"((int)acc)
+        : "memory");
+}
+DV_DEV void tc_commit(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+            smem_addr(bar))
+        : "memory");
+}
+// 32 columns of a thread's lane of tensor memory.
+DV_DEV void tm_ld(unsigned addr, float (&v)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+                 "%30, %31}, [%32];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                   "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]),
+                   "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
+                   "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+                   "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]),
+                   "=f"(v[30]), "=f"(v[31])
+                 : "r"(addr));
+}
+// The loads into v have landed (v passes through, so that no use moves before it).
+DV_DEV void tm_wait_ld(float (&v)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                   "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                   "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]),
+                   "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                   "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                   "+f"(v[30]), "+f"(v[31])
+                 :
+                 : "memory");
+}
+DV_DEV void tm_st(unsigned addr, const float (&v)[32])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+                 "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, "
+                 "%31, %32};" ::"r"(addr),
+                 "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]),
+                 "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]),
+                 "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]),
+                 "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]),
+                 "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+                 : "memory");
+}
+// Binary16 pairs r[0 .. 31] to 32 columns.
+DV_DEV void tm_st_pairs(unsigned addr, const unsigned *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+                 "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, "
+                 "%31, %32};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+                 "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+                 "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+                 "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+                 : "memory");
+}
+DV_DEV void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+DV_DEV bool elect_one()
+{
+    unsigned p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(p));
+    return p != 0;
+}
+DV_DEV float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+template <int N>
+DV_DEV void group_sync(int bar)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(N) : "memory");
+}
+
+// A role's waits: after one has run out the others no longer wait (the
+// results are lost, the status says so, every loop still ends).
+struct SeqWaiter {
+    int *status;
+    bool dead = false;
+    DV_DEV void operator()(uint64_t *bar, unsigned parity)
+    {
+        if (!dead && !bar_wait(smem_addr(bar), parity & 1)) {
+            dead = true;
+            set_status(status, DV_ERR_TIMEOUT);
+        }
+    }
+};
+
+// A piece's tiles as both streams see them, and its operands' places in the
+// ring (counted from the piece's first): of a pair keys and values in turn, of
+// a single tile a tile's keys before the values of the one before.
+template <class C>
+struct Plan {
+    int n, n0;       // tiles; of them, a pair's first 128 rows' own
+    int edge;        // first tile (of the piece) that some row does not see whole
+    bool pair;
+    DV_DEV Plan(const SeqAttnArgs &a, const typename C::Sched::Piece &x)
+    {
+        pair = x.pair;
+        n = x.k1 - x.k0;
+        n0 = pair ? min(max(((x.pos + (1 << a.tlog) + C::TP - 1) >> 7) - x.k0, 0), n) : n;
+        edge = min(max(((x.pos + 1) >> 7) - x.k0, 0), n);
+    }
+    DV_DEV unsigned k_at(int t) const { return pair ? 2 * t : max(2 * t - 1, 0); }
+    DV_DEV unsigned v_at(int t) const { return pair ? 2 * t + 1 : min(2 * t + 2, 2 * n - 1); }
+    DV_DEV int of_stream(int w) const { return pair ? (w ? n : n0) : (n + 1 - w) >> 1; }
+};
+
+// 32 scores as weights under the reference m: v becomes pairs of binary16.
+// d (EDGE): the last seen column.
+template <bool EDGE>
+DV_DEV void weigh(float (&v)[32], int d, float scale, float m, float &top, float (&sum)[2],
+                  unsigned *pr)
+{
+    if (EDGE) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            v[i] = i <= d ? v[i] : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+        top = max3(top, v[i], v[i + 1]);
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        fma2(v[i], v[i + 1], scale, -m);
+        v[i] = ex2(v[i]);
+        v[i + 1] = ex2(v[i + 1]);
+        add2(sum[0], sum[1], v[i], v[i + 1]);
+        pr[i / 2] = h2(v[i], v[i + 1]);
+    }
+}
+
+constexpr float kSeqShift = 6.f;   // the first tile's largest weight is 2^6 to 2^7
+constexpr float kSeqLimit = 15.f;  // a weight above 2^15 moves the reference
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+    k_seq_tc(const SeqAttnArgs a, const __grid_constant__ SeqMaps maps, int q_tokens)
+{
+    constexpr int D = C::D, TP = C::TP, RM = C::RM, NST = C::NST;
+    using Sched = typename C::Sched;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    SeqCtl &ctl = *reinterpret_cast<SeqCtl *>(smem + C::OFF_CTL);
+    const unsigned sbase = smem_addr(smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(&ctl.tmem)),
+                     "r"(C::T_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        auto init = [](uint64_t &b, int n) { bar_init(smem_addr(&b), n); };
+        for (int i = 0; i < NST; ++i) {
+            init(ctl.full[i], 1);
+            init(ctl.empty[i], 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            init(ctl.s_full[w], 1);
+            init(ctl.p_full[w], 4);
+            init(ctl.o_full[w], 1);
+            init(ctl.q_full[w], 1);
+            init(ctl.q_free[w], 1);
+            init(ctl.x_free[w], 4);
+        }
+        for (int i = 0; i < 4; ++i) {
+            init(ctl.v_req[i], 1);
+            init(ctl.v_ok[i], 1);
+        }
+        init(ctl.end, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tc_fence_before();
+    const SeqRun run = Sched::init(a, ctl.sched);  // (barriers)
+    tc_fence_after();
+    const unsigned tmem = ctl.tmem;
+    SeqWaiter wait{a.status};
+    typename Sched::Walk walk(a, run);
+    typename Sched::Piece x = {};
+
+    if (warp == 8) {
+        // ---- keys and values
+        unsigned i = 0;  // ring entries so far
+        const int np = a.pk ? TP / a.page : 1;  // pages of a tile (lane: its page)
+        const int none = a.pk ? a.n_pages * a.Hkv : 0;
+        // where this lane's page of tile t lies: the row (head) of the pool, or
+        // one behind the pool, which reads as zeros
+        auto page_of = [&](int t) {
+            const int p = t * TP + lane * a.page;
+            if (lane >= np || p >= x.pos + x.ntok)
+                return none;
+            const int pg = __ldg(a.tables + (long long)x.b * a.width + p / a.page);
+            if ((unsigned)pg >= (unsigned)a.n_pages) {
+                set_status(a.status, DV_ERR_DEVICE_INDEX);
+                return none;
+            }
+            return pg * a.Hkv + x.hkv;
+        };
+        auto load = [&](const CUtensorMap *map, int t, int z) {
+            const unsigned st = i % NST, full = smem_addr(&ctl.full[st]);
+            if (i >= NST)
+                wait(&ctl.empty[st], i / NST - 1);
+            ++i;
+            if (wait.dead)
+                return;
+            if (lane == 0)
+                bar_expect(full, C::TILE);
+            __syncwarp();
+            const unsigned dst = sbase + C::OFF_KV + st * C::TILE;
+            if (lane < np) {
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    if (a.pk)
+                        tma_load(dst + c * C::HALF + lane * a.page * 128, map, 64 * c, 0, z, full);
+                    else
+                        tma_load(dst + c * C::HALF, map, 64 * c, x.tok - x.pos + t * TP, x.hkv,
+                                 full);
+                }
+            }
+        };
+        while (walk.next(x)) {
+            const int lag = x.pair ? 0 : 1;
+            int z = 0, zn = a.pk ? page_of(x.k0) : 0, zv = 0;
+            for (int t = x.k0; t < x.k1 + lag; ++t) {
+                zv = z;
+                z = zn;
+                if (a.pk && t + 1 < x.k1)
+                    zn = page_of(t + 1);
+                if (t < x.k1)
+                    load(&maps.k, t, z);
+                if (t - lag >= x.k0)
+                    load(&maps.v, t - lag, lag ? zv : z);
+            }
+        }
+        // no copy may outlive the CTA
+        for (unsigned k = i < NST ? 0 : i - NST; k < i && !wait.dead; ++k)
+            bar_wait(smem_addr(&ctl.full[k % NST]), (k / NST) & 1);
+        if (wait.dead)
+            for (int k = 0; k < NST; ++k) {  // (either phase: what was issued lands in time)
+                bar_wait(smem_addr(&ctl.full[k]), 0);
+                bar_wait(smem_addr(&ctl.full[k]), 1);
+            }
+    } else if (warp == 10) {
+        // ---- queries
+        unsigned u = 0, pairs = 0, singles = 0;
+        const unsigned bytes = (unsigned)(a.group * q_tokens) * 128 * (D / 64);
+        while (walk.next(x)) {
+            for (int w = 0; w < 2; ++w) {
+                if (u > 0)
+                    wait(&ctl.q_free[w], u - 1);
+                if (singles > 0)
+                    wait(&ctl.x_free[w], singles - 1);
+                if (lane == 0 && !wait.dead && (w == 0 || x.pair)) {
+                    const unsigned full = smem_addr(&ctl.q_full[w]);
+                    bar_expect(full, bytes);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load(sbase + w * C::TILE + c * C::HALF, &maps.q, 64 * c, x.h0,
+                                 x.tok + (w << a.tlog), full);
+                }
+                __syncwarp();
+            }
+            ++u;
+            pairs += x.pair;
+            singles += !x.pair;
+        }
+        if (u > 0)
+            bar_wait(smem_addr(&ctl.q_full[0]), (u - 1) & 1);
+        if (pairs > 0)
+            bar_wait(smem_addr(&ctl.q_full[1]), (pairs - 1) & 1);
+    } else if (warp == 9) {
+        // ---- products.  The warp runs its loop together, so that descriptors
+        // stay in uniform registers, and one thread issues.
+        constexpr uint32_t ID_S = tc_idesc(TP, false), ID_O = tc_idesc(D, true);
+        constexpr unsigned STAGE = C::TILE >> 4;
+        const uint64_t dq = tc_desc(sbase, 16), dk = tc_desc(sbase + C::OFF_KV, 16),
+                       dv = tc_desc(sbase + C::OFF_KV, C::HALF);
+        const bool one = elect_one();
+        unsigned base = 0, units = 0, pairs = 0, edges = 0, np[2] = {0, 0};
+        while (walk.next(x)) {
+            const Plan<C> pl(a, x);
+            const int n = pl.n;
+            wait(&ctl.q_full[0], units);
+            auto keys = [&](int t) {  // tile t's keys are there
+                const unsigned i = base + pl.k_at(t);
+                wait(&ctl.full[i % NST], i / NST);
+                if (one && t >= pl.edge)
+                    bar_arrive(smem_addr(&ctl.v_req[(edges + t - pl.edge) & 3]));
+                tc_fence_after();
+            };
+            auto scores = [&](int w, int t, bool last) {
+                const unsigned st = (base + pl.k_at(t)) % NST;
+                const uint64_t q = dq + (pl.pair && w ? STAGE : 0u), k = dk + st * STAGE;
+                if (one && !wait.dead) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        tc_mma_ss(tmem + C::T_S + w * 128, q + (kk / 4) * (C::HALF >> 4) + (kk % 4) * 2,
+                                  k + (kk / 4) * (C::HALF >> 4) + (kk % 4) * 2, ID_S, kk > 0);
+                    tc_commit(&ctl.s_full[w]);
+                    if (last)
+                        tc_commit(&ctl.empty[st]);
+                }
+                __syncwarp();
+            };
+            auto values = [&](int w, int t, bool acc, bool end, bool last) {
+                const unsigned i = base + pl.v_at(t), st = i % NST;
+                wait(&ctl.full[st], i / NST);
+                if (t >= pl.edge) {
+                    const unsigned e = edges + t - pl.edge;
+                    wait(&ctl.v_ok[e & 3], e >> 2);
+                }
+                wait(&ctl.p_full[w], np[w]++);
+                tc_fence_after();
+                const uint64_t v = dv + st * STAGE;
+                if (one && !wait.dead) {
+#pragma unroll
+                    for (int kk = 0; kk < TP / 16; ++kk)
+                        tc_mma_ts(tmem + C::T_O + w * 128, tmem + C::T_S + w * 128 + kk * 8,
+                                  v + kk * (16 * 128 >> 4), ID_O, acc || kk > 0);
+                    if (last)
+                        tc_commit(&ctl.empty[st]);
+                    if (end)
+                        tc_commit(&ctl.o_full[w]);
+                }
+                __syncwarp();
+            };
+            auto free_q = [&](int w) {
+                if (one && !wait.dead)
+                    tc_commit(&ctl.q_free[w]);
+            };
+            if (pl.pair) {
+                const int n0 = pl.n0;
+                keys(0);
+                if (n0 > 0)
+                    scores(0, 0, false);
+                if (n0 <= 1)
+                    free_q(0);
+                wait(&ctl.q_full[1], pairs);
+                tc_fence_after();
+                scores(1, 0, true);
+                if (n == 1)
+                    free_q(1);
+                for (int t = 0; t < n; ++t) {
+                    if (t < n0)
+                        values(0, t, t > 0, t == n0 - 1, false);
+                    if (t + 1 < n) {
+                        keys(t + 1);
+                        if (t + 1 < n0)
+                            scores(0, t + 1, false);
+                        if (t + 1 == n0 - 1)
+                            free_q(0);
+                    }
+                    values(1, t, t > 0, t == n - 1, true);
+                    if (t + 1 < n)
+                        scores(1, t + 1, true);
+                    if (t + 1 == n - 1)
+                        free_q(1);
+                }
+            } else {
+                for (int t = 0; t < 2 && t < n; ++t) {
+                    keys(t);
+                    scores(t, t, true);
+                }
+                for (int t = 0; t < n; ++t) {
+                    values(t & 1, t, t > 1, t + 2 >= n, true);
+                    if (t + 2 < n) {
+                        keys(t + 2);
+                        scores(t & 1, t + 2, true);
+                    }
+                }
+                free_q(0);
+                free_q(1);
+            }
+            base += 2 * n;
+            edges += n - pl.edge;
+            ++units;
+            pairs += pl.pair;
+        }
+        // every product is done before tensor memory goes
+        if (one)
+            tc_commit(&ctl.end);
+        __syncwarp();
+        bar_wait(smem_addr(&ctl.end), 0);
+    } else if (warp == 11) {
+        // ---- value rows that some row does not see
+        unsigned base = 0, edges = 0;
+        while (walk.next(x)) {
+            const Plan<C> pl(a, x);
+            for (int t = pl.edge; t < pl.n; ++t, ++edges) {
+                // (asked for when the tile's keys are there: what the ring's stage held
+                // before its values has been waited for by then, so a parity tells the
+                // phases apart)
+                wait(&ctl.v_req[edges & 3], edges >> 2);
+                const unsigned i = base + pl.v_at(t), st = i % NST;
+                wait(&ctl.full[st], i / NST);
+                unsigned *const bad = ctl.bad[edges & 3];
+                if (lane < 4)
+                    bad[lane] = 0u;
+                __syncwarp();
+                // rows up to the first token's position are seen by all
+                const int r0 = max(0, x.pos + 1 - (x.k0 + t) * TP);
+                const unsigned at = sbase + C::OFF_KV + st * C::TILE;
+#pragma unroll 1
+                for (int c = 0; c < D / 64; ++c)
+#pragma unroll 4
+                    for (int j = r0 * 8 + lane; j < TP * 8; j += 32) {
+                        const unsigned p = at + c * C::HALF + j * 16;
+                        const uint4 y = lds16(p);
+                        // an exponent field of ones carries into its half's top bit
+                        unsigned z = ((y.x & 0x7c007c00u) + 0x04000400u) |
+                                     ((y.y & 0x7c007c00u) + 0x04000400u) |
+                                     ((y.z & 0x7c007c00u) + 0x04000400u) |
+                                     ((y.w & 0x7c007c00u) + 0x04000400u);
+                        if (z & 0x80008000u) {
+                            sts16(p, 0u, 0u, 0u, 0u);
+                            atomicOr(bad + (j >> 8), 1u << ((j >> 3) & 31));
+                        }
+                    }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(smem_addr(&ctl.v_ok[edges & 3]));
+            }
+            base += 2 * pl.n;
+        }
+    } else {
+        // ---- softmax of stream w: a thread a row
+        const int w = warp >> 2, row = tid & 127, rtok = row / a.group, rhead = row % a.group;
+        const unsigned lanes = (unsigned)(32 * (warp & 3)) << 16;
+        const unsigned tS = tmem + lanes + C::T_S + w * 128, tO = tmem + lanes + C::T_O + w * 128;
+        const float scale = a.scale;
+        unsigned tiles = 0, edges = 0, ends = 0;
+        while (walk.next(x)) {
+            const Plan<C> pl(a, x);
+            const int n = pl.of_stream(w);
+            const int tok0 = pl.pair && w ? 1 << a.tlog : 0;  // this stream's first token
+            const int ntok = pl.pair && !w ? 1 << a.tlog : x.ntok - tok0;
+            const bool on = rtok < ntok;
+            const bool busy = __any_sync(0xffffffffu, on);  // the warp has a row
+            const int lim = x.pos + tok0 + rtok;
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < n; ++j, ++tiles) {
+                const int t = pl.pair ? j : 2 * j + w;
+                wait(&ctl.s_full[w], tiles);
+                if (busy) {
+                    tc_fence_after();
+                    const bool edge = t >= pl.edge;
+                    const bool cut = x.pos + tok0 < (x.k0 + t + 1) * TP - 1;  // for some row
+                    const int d = lim - (x.k0 + t) * TP;
+                    float top, sum[2], v[2][32];
+                    unsigned pr[64];
+                    auto pass = [&](float ms, auto edged) {
+                        constexpr bool E = decltype(edged)::value;
+                        top = -INFINITY;
+                        sum[0] = sum[1] = 0.f;
+                        tm_ld(tS, v[0]);
+                        tm_wait_ld(v[0]);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if (c < 3)
+                                tm_ld(tS + 32 * (c + 1), v[(c + 1) & 1]);
+                            weigh<E>(v[c & 1], d - 32 * c, scale, ms, top, sum, pr + 16 * c);
+                            if (c < 3)
+                                tm_wait_ld(v[(c + 1) & 1]);
+                        }
+                    };
+                    auto both = [&](float ms) {
+                        if (cut)
+                            pass(ms, std::true_type{});
+                        else
+                            pass(ms, std::false_type{});
+                    };
+                    if (j == 0) {  // a first reference, by the tile's maximum
+                        top = -INFINITY;
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            tm_ld(tS + 32 * c, v[0]);
+                            tm_wait_ld(v[0]);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                top = fmaxf(top, !cut || 32 * c + i <= d ? v[0][i] : -INFINITY);
+                        }
+                        m = floorf(top * scale) - kSeqShift;
+                    }
+                    both(m == -INFINITY ? 0.f : m);
+                    const float high = top * scale;
+                    const bool need = m == -INFINITY ? high > -INFINITY : high - m > kSeqLimit;
+                    if (__any_sync(0xffffffffu, need)) {
+                        // (the tile before's value product is done: this tile's scores
+                        // came after it)
+                        const float mn = need ? floorf(high) - kSeqShift : m;
+                        const float f = need ? pow2(m - mn) : 1.f;
+                        m = mn;
+                        l *= f;
+                        if (j > 0) {
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                tm_ld(tO + c, v[0]);
+                                tm_wait_ld(v[0]);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    v[0][i] *= f;
+                                tm_st(tO + c, v[0]);
+                            }
+                        }
+                        both(m == -INFINITY ? 0.f : m);
+                    }
+                    l += sum[0] + sum[1];
+                    if (edge) {  // a row that sees what was taken out is not finite
+                        const unsigned e = edges + t - pl.edge;
+                        wait(&ctl.v_ok[e & 3], e >> 2);
+                        const unsigned *bad = ctl.bad[e & 3];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int s = d - 32 * k;
+                            const unsigned seen = s < 0 ? 0u : s >= 31 ? ~0u : (2u << s) - 1;
+                            if (bad[k] & seen)
+                                l = __int_as_float(0x7fc00000);
+                        }
+                    }
+                    tm_st_pairs(tS, pr);
+                    tm_st_pairs(tS + 32, pr + 32);
+                    tm_wait_st();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(smem_addr(&ctl.p_full[w]));
+            }
+            edges += pl.n - pl.edge;
+
+            // ---- the piece's end
+            const bool whole = x.c0 == x.c1;
+            __half *const out = static_cast<__half *>(a.out) +
+                                ((long long)(x.tok + tok0 + rtok) * a.H + x.h0 + rhead) * D;
+            float *const rec = a.rec + (size_t)Sched::slot(run.c, x.c0) * C::REC;
+            float *const rec_m = rec + 2 * RM * D + w * 2 * RM, *const rec_l = rec_m + RM;
+            if (n > 0) {
+                wait(&ctl.o_full[w], ends++);
+                tc_fence_after();
+            }
+            auto st8h = [&](int c, const float *y, float f) {  // 8 values of the result
+                uint4 u;
+                u.x = h2(y[0] * f, y[1] * f);
+                u.y = h2(y[2] * f, y[3] * f);
+                u.z = h2(y[4] * f, y[5] * f);
+                u.w = h2(y[6] * f, y[7] * f);
+                *reinterpret_cast<uint4 *>(out + c) = u;
+            };
+            // four values of row r's piece, columns 4 c ..
+            auto rec_at = [&](float *base, int r, int c) {
+                return reinterpret_cast<float4 *>(base) + c * (2 * RM) + r;
+            };
+            const int r0 = pl.pair ? w * RM : 0;  // the record's rows of this stream
+            if (pl.pair) {
+                if (busy) {
+                    const float f = l == 0.f ? 0.f : __frcp_rn(l);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float y[32];
+                        if (n > 0) {
+                            tm_ld(tO + c, y);
+                            tm_wait_ld(y);
+                        }
+                        if (whole) {
+                            if (on)
+#pragma unroll
+                                for (int i = 0; i < 32; i += 8)
+                                    st8h(c + i, y + i, f);
+                        } else if (on && n > 0) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                __stcg(rec_at(rec, r0 + row, (c + i) / 4),
+                                       make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]));
+                        }
+                    }
+                    tc_fence_before();
+                }
+            } else {
+                // Stream w finishes columns w D / 2 .. of all rows; the other
+                // stream's share of them comes through the queries' place, whose
+                // products are done when both streams' are.
+                constexpr int HC = D / 2;
+                group_sync<256>(1);  // (both have left the unit before, too)
+                ctl.m[w][row] = m;
+                ctl.l[w][row] = l;
+                float4 *const give = reinterpret_cast<float4 *>(smem + (w ^ 1) * C::TILE) + row;
+                const float4 *const get = reinterpret_cast<float4 *>(smem + w * C::TILE) + row;
+                if (busy && n > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < HC; c += 32) {
+                        float y[32];
+                        tm_ld(tO + (w ^ 1) * HC + c, y);
+                        tm_wait_ld(y);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            give[(c + i) / 4 * RM] = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+                    }
+                }
+                group_sync<256>(1);
+                if (busy) {
+                    const float mo = ctl.m[w ^ 1][row], M = fmaxf(m, mo);
+                    const float ms = M == -INFINITY ? 0.f : M;
+                    const float fw = pow2(m - ms), fo = pow2(mo - ms);
+                    const bool other = pl.of_stream(w ^ 1) > 0;
+                    l = l * fw + ctl.l[w ^ 1][row] * fo;
+                    m = M;
+                    const float f = l == 0.f ? 0.f : __frcp_rn(l);
+#pragma unroll 1
+                    for (int c = 0; c < HC; c += 32) {
+                        float y[32];
+                        if (n > 0) {
+                            tm_ld(tO + w * HC + c, y);
+                            tm_wait_ld(y);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (other)
+                                g = get[(c + i) / 4 * RM];
+                            y[i] = n > 0 ? fmaf(y[i], fw, g.x * fo) : g.x * fo;
+                            y[i + 1] = n > 0 ? fmaf(y[i + 1], fw, g.y * fo) : g.y * fo;
+                            y[i + 2] = n > 0 ? fmaf(y[i + 2], fw, g.z * fo) : g.z * fo;
+                            y[i + 3] = n > 0 ? fmaf(y[i + 3], fw, g.w * fo) : g.w * fo;
+                        }
+                        if (on) {
+                            if (whole) {
+#pragma unroll
+                                for (int i = 0; i < 32; i += 8)
+                                    st8h(w * HC + c + i, y + i, f);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 32; i += 4)
+                                    __stcg(rec_at(rec, row, (w * HC + c + i) / 4),
+                                           make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]));
+                            }
+                        }
+                    }
+                    tc_fence_before();
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(smem_addr(&ctl.x_free[w]));
+            }
+            if (whole)
+                continue;
+            if (on) {
+                // (a stream without a tile of this piece has left no outputs)
+                __stcg(rec_m + row, m);
+                __stcg(rec_l + row, l);
+            }
+            __threadfence();
+            group_sync<128>(2 + w);
+            if (row == 0) {
+                int *cnt = a.cnt + 2 * x.c0 + w;
+                const int was = atomicAdd(cnt, 1);
+                ctl.last[w] = was == x.c1 - x.c0;
+                if (ctl.last[w])
+                    *cnt = 0;
+                __threadfence();
+            }
+            group_sync<128>(2 + w);
+            if (!ctl.last[w])
+                continue;
+            // ---- merge: rows x groups of four columns over the stream's threads
+            const int rows = min(ntok * a.group, RM);
+            const int cg = pl.pair ? D / 4 : D / 8, cg0 = pl.pair ? 0 : w * (D / 8);
+#pragma unroll 1
+            for (int k = row; k < rows * cg; k += 128) {
+                const int r = k % rows, c = cg0 + k / rows;
+                float M = -INFINITY, L = 0.f;
+                for (int p = x.c0; p <= x.c1; ++p)
+                    M = fmaxf(M, ld_cg(a.rec + (size_t)Sched::slot(p, x.c0) * C::REC + 2 * RM * D +
+                                       w * 2 * RM + r));
+                const float ms = M == -INFINITY ? 0.f : M;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int p = x.c0; p <= x.c1; ++p) {
+                    float *q = a.rec + (size_t)Sched::slot(p, x.c0) * C::REC;
+                    const float mp = ld_cg(q + 2 * RM * D + w * 2 * RM + r);
+                    const float lp = ld_cg(q + 2 * RM * D + w * 2 * RM + RM + r);
+                    const float4 y = __ldcg(rec_at(q, r0 + r, c));
+                    if (mp == -INFINITY && lp == 0.f)
+                        continue;
+                    const float f = pow2(mp - ms);
+                    L = fmaf(lp, f, L);
+                    o.x = fmaf(y.x, f, o.x);
+                    o.y = fmaf(y.y, f, o.y);
+                    o.z = fmaf(y.z, f, o.z);
+                    o.w = fmaf(y.w, f, o.w);
+                }
+                const float f = L == 0.f ? 0.f : __frcp_rn(L);
+                __half *to = static_cast<__half *>(a.out) +
+                             ((long long)(x.tok + tok0 + r / a.group) * a.H + x.h0 + r % a.group) * D +
+                             4 * c;
+                *reinterpret_cast<uint2 *>(to) = make_uint2(h2(o.x * f, o.y * f), h2(o.z * f, o.w * f));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(C::T_COLS)
+                     : "memory");
+    }
+}
+
+// Tensor maps of binary16 rows, encoded by the driver's function (resolved
+// through the runtime: the library does not link the driver library).
+struct SeqMapEncoder {
+    PFN_cuTensorMapEncodeTiled_v12000 encode;
+    SeqMapEncoder()
+    {
+        static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+            void *f = nullptr;
+            cudaDriverEntryPointQueryResult q;
+            const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                                             cudaEnableDefault, &q) == cudaSuccess &&
+                            q == cudaDriverEntryPointSuccess;
+            return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ok ? f : nullptr);
+        }();
+        encode = fn;
+    }
+    // Three dimensions, the strides of the outer two in elements; swizzled rows
+    // of 128 bytes.
+    cudaError_t operator()(CUtensorMap *m, const void *p, const unsigned (&dims)[3],
+                           const long long (&strides)[2], const unsigned (&box)[3]) const
+    {
+        if (!encode)
+            return cudaErrorNotSupported;
+        const cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
+        const cuuint64_t s[2] = {(cuuint64_t)strides[0] * 2, (cuuint64_t)strides[1] * 2};
+        const cuuint32_t b[3] = {box[0], box[1], box[2]}, one[3] = {1, 1, 1};
+        return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(p), d, s, b, one,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+                   ? cudaSuccess
+                   : cudaErrorInvalidValue;
+    }
+};
+
+template <class C>
+cudaError_t launch_tc(SeqAttnArgs a, int nsm, cudaStream_t st)
+{
+    auto kern = k_seq_tc<C>;
+    constexpr size_t smem = C::OFF_CTL + sizeof(SeqCtl);
+    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+    static DeviceOnce once;
+    cudaError_t e = once.run([&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    });
+    if (e != cudaSuccess)
+        return e;
+    seq_group(a, C::RM);
+    int q_tokens = 1;  // of a copy: no more than a request can have
+    while (q_tokens < a.max_tok && q_tokens < 1 << a.tlog)
+        q_tokens *= 2;
+    const SeqMapEncoder enc;
+    SeqMaps maps;
+    constexpr unsigned D = C::D;
+    // queries (dimension, head, token), boxes of a unit's heads and tokens
+    if ((e = enc(&maps.q, a.q.p, {D, (unsigned)a.H, (unsigned)a.T},
+                 {a.H > 1 ? a.q.sh : D, a.T > 1 ? a.q.st : D},
+                 {64, (unsigned)a.group, (unsigned)q_tokens})))
+        return e;
+    for (int i = 0; i < 2; ++i) {
+        CUtensorMap *m = i ? &maps.v : &maps.k;
+        const SeqRowsArgs &r = i ? a.v : a.k;
+        if (a.pk)  // (dimension, row of a page, page and head)
+            e = enc(m, i ? a.pv : a.pk, {D, (unsigned)a.page, (unsigned)(a.n_pages * a.Hkv)},
+                    {D, (long long)D * a.page}, {64, (unsigned)a.page, 1});
+        else  // (dimension, token, head)
+            e = enc(m, r.p, {D, (unsigned)a.T, (unsigned)a.Hkv},
+                    {a.T > 1 ? r.st : D, a.Hkv > 1 ? r.sh : D}, {64, C::TP, 1});
+        if (e)
+            return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(nsm < kSeqTcCtas ? nsm : kSeqTcCtas);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    return cudaLaunchKernelEx(&cfg, kern, a, maps, q_tokens);
+}
+
+}  // namespace
+
+cudaError_t launch_seq_tc(const SeqAttnArgs &a, int nsm, cudaStream_t st)
+{
+    return a.D == 128 ? launch_tc<SeqTcCfg<128>>(a, nsm, st) : launch_tc<SeqTcCfg<64>>(a, nsm, st);
+}
+
+size_t seq_tc_record_bytes(int D)
+{
+    return 2 * (size_t)kSeqTcCtas * (D == 128 ? SeqTcCfg<128>::REC : SeqTcCfg<64>::REC) * 4;
+}
+
+}  // namespace dv
