@@ -48,9 +48,10 @@ __global__ void __launch_bounds__(256) k_seq_attn(const SeqAttnArgs a)
     float *const sq = smem, *const sk = sq + RM * LD, *const sv = sk + TP * LD, *const sp = sv + TP * LD;
     const int tid = threadIdx.x, r = tid >> 3, j8 = tid & 7;
     const SeqRun run = Sched::init(a, ss);
-    Sched::Walk walk(a, run);
+    Sched::Walk walk;
     Sched::Piece x;
-    while (walk.next(x)) {
+    walk.start(a, run);
+    while (walk.next(a, run, x)) {
         const int nrows = x.ntok * a.group, ctx = x.pos + x.ntok;
         __syncthreads();
         for (int i = tid; i < RM * (D / 4); i += 256) {

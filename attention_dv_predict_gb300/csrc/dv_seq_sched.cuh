@@ -119,6 +119,7 @@ struct SeqSched {
             __syncthreads();
             long long all = 0;
             before = inc - v;
+#pragma unroll 1
             for (int w = 0; w < nw; ++w) {
                 before += w < warp ? sm.part[w] : 0;
                 all += sm.part[w];
@@ -161,18 +162,17 @@ struct SeqSched {
         bool pair;      // more than 2^tlog tokens
     };
 
+    // Where a role is: the request, its group of heads and unit that come next.
     struct Walk {
-        const SeqAttnArgs &a;
-        const SeqRun &r;
         SeqRow row;
-        int b, hs;
-        long long i, u0;  // unit of the request and head, its place
+        int b, hs, i;
+        long long u0;  // the unit's place
 
-        DV_DEV Walk(const SeqAttnArgs &a_, const SeqRun &r_) : a(a_), r(r_)
+        DV_DEV void start(const SeqAttnArgs &a, const SeqRun &r)
         {
+            row = SeqRow{0, 0, 0};
             b = r.b;
-            hs = 0;
-            i = 0;
+            hs = i = 0;
             u0 = r.hi;
             if (r.lo >= r.hi)
                 return;
@@ -181,9 +181,10 @@ struct SeqSched {
             hs = (int)(at / per);
             const long long rest = at - hs * per;
             // the last whole unit, or the partial one behind them, that starts by `rest`
-            long long lo = 0, hi = units() - 1;
+            int lo = 0, hi = units(a) - 1;
+#pragma unroll 1
             while (lo < hi) {
-                const long long mid = (lo + hi + 1) / 2;
+                const int mid = (lo + hi + 1) / 2;
                 if (whole(a, row.len, mid) <= rest)
                     lo = mid;
                 else
@@ -192,15 +193,16 @@ struct SeqSched {
             i = lo;
             u0 = r.lo - (rest - whole(a, row.len, i));
         }
-        DV_DEV long long units() const
+        DV_DEV int units(const SeqAttnArgs &a) const
         {
-            return ((long long)row.n + (1 << ulog(a)) - 1) >> ulog(a);
+            return (row.n + (1 << ulog(a)) - 1) >> ulog(a);
         }
         // The next piece, false behind the last.
-        DV_DEV bool next(Piece &p)
+        DV_DEV bool next(const SeqAttnArgs &a, const SeqRun &r, Piece &p)
         {
+#pragma unroll 1
             while (u0 < r.hi) {
-                const int first = (int)(i << ulog(a));
+                const int first = i << ulog(a);
                 p.ntok = min(1 << ulog(a), row.n - first);
                 p.tok = row.t0 + first;
                 p.pos = row.len + first;
@@ -214,10 +216,11 @@ struct SeqSched {
                 p.k0 = (int)max(0ll, (r.lo - t0 + wt) >> wt);
                 p.k1 = (int)max(0ll, min((long long)p.nt, (r.hi - t0 + wt) >> wt));
                 u0 = t0 + ((long long)p.nt << wt);
-                if (++i >= units()) {
+                if (++i >= units(a)) {
                     i = 0;
                     if (++hs == a.H / a.group) {
                         hs = 0;
+#pragma unroll 1
                         do {
                             if (++b < a.B)
                                 row = seq_row(a, b, false);
@@ -230,16 +233,19 @@ struct SeqSched {
                     continue;
                 p.c0 = p.c1 = r.c;
                 if (p.k0 > 0)
-                    p.c0 = run_of(t0);
+                    p.c0 = run_of(r, t0);
                 if (p.k1 < p.nt)
-                    p.c1 = run_of(t0 + ((long long)(p.nt - 1) << wt));
+                    p.c1 = run_of(r, t0 + ((long long)(p.nt - 1) << wt));
                 return true;
             }
             return false;
         }
-        // The run that place w falls to: the last c with floor(W c / C) <= w.
-        DV_DEV int run_of(long long w) const { return (int)(((w + 1) * r.C - 1) / r.W); }
     };
+    // The run that place w falls to: the last c with floor(W c / C) <= w.
+    DV_DEV static int run_of(const SeqRun &r, long long w)
+    {
+        return (int)(((w + 1) * r.C - 1) / r.W);
+    }
     // Record of run c's piece of a unit that starts in run c0.
     DV_DEV static int slot(int c, int c0) { return 2 * c + (c == c0); }
 };

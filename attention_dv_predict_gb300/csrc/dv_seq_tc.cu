@@ -2,29 +2,36 @@
 // binary16 rows of 64 or 128 values, packed or in pages.
 //
 // A unit's query rows fill one or two M = 128 tiles.  Two streams of softmax,
-// four warps each with a row a thread, keep the tensor cores busy in turn:
-// while one weighs a tile of 128 positions, the other's products run.  A unit
-// of two tiles (a pair: prompts, chunks) gives each stream its own rows and the
-// same positions; a unit of one (decode, a chunk's end) gives both the same
-// rows and every other tile of positions, and they are merged when it ends.
-// Scores lie in tensor memory, the weights (binary16) take their place as the
-// A operand of the value product, and the outputs are summed there in binary32.
+// four warps each with a row a thread, share the tensor cores.  A unit of two
+// tiles (a pair: prompts, chunks) gives each stream its own rows and the same
+// positions; a unit of one (decode, a chunk's end) gives both the same rows and
+// every other tile of positions, and they are merged when it ends.  Scores lie
+// in tensor memory, the weights (binary16) take their place as the A operand of
+// the value product, and the outputs are summed there in binary32.
+//
+// A tile is 64 positions and a stream has two score buffers, so that the next
+// tile's scores are there when a softmax warp gets to them and the products of
+// both streams run back to back: a tile of 128 (whose scores fill tensor memory
+// with one buffer a stream) left the tensor cores waiting for every softmax.
+// Per pair tile the score products take 384 cycles each (bound by their reads
+// of shared memory) and the value products 256.
 //
 // Warps of a CTA (one CTA per SM):
 //   0-3, 4-7  softmax of stream 0, 1
-//   8         copies of keys and values: a ring of 128-position tiles; of a paged
-//             cache a lane a page, the page numbers a tile ahead
-//   9         the products (one thread issues them)
-//   10        copies of queries
-//   11        takes NaN and infinities out of value rows that some row of the
-//             unit does not see (only the last tiles hold any)
+//   8         copies of keys and values: a ring of tiles; of a paged cache a
+//             lane a page, the page numbers a tile ahead
+//   9, 10     the products of stream 0, 1 (one thread each issues them: an issue
+//             takes as long as the product before runs, and a wait for a barrier
+//             100 cycles even if it is over, so with one warp for both streams the
+//             tensor cores idled half of the time)
+//   11        copies of queries; takes NaN and infinities out of value rows that
+//             some row of the unit does not see (only its last tiles hold any)
 // Hand-overs are mbarriers; every wait has a limit (DV_ERR_TIMEOUT).
 //
 // A row's reference point m stands in for its running maximum: weights are
 // 2^(s - m) with m a whole number 6 below the first tile's maximum, and m moves
 // (for this row alone) when a weight would pass 2^15, near the end of binary16's
-// range.  So the outputs are rarely rescaled, and a tile is read from tensor
-// memory once, its maximum formed beside the weights.
+// range, so the outputs are rarely rescaled.
 #include <cudaTypedefs.h>
 
 #include "dv_kv_tma.cuh"
@@ -37,31 +44,38 @@ struct SeqMaps {
     CUtensorMap q, k, v;
 };
 
+using TcSched = SeqSched<64, true, 6, 16>;
+
 template <int D_>
 struct SeqTcCfg {
-    static constexpr int D = D_, TP = 128, RM = 128;
-    static constexpr int TILE = TP * D * 2;              // a tile of keys, values or queries
-    static constexpr int HALF = TP * 128;                // 64 dimensions of it
-    static constexpr int NST = D == 128 ? 5 : 10;        // ring stages
+    static constexpr int D = D_, TP = 64, RM = 128;
+    static constexpr int TILE = TP * D * 2, HALF = TP * 128;    // keys or values; 64 dimensions
+    static constexpr int QTILE = RM * D * 2, QHALF = RM * 128;  // queries of 128 rows
+    static constexpr int NST = D == 128 ? 5 : 8;               // ring stages
     static constexpr int THREADS = 384;
-    static constexpr int OFF_KV = 2 * TILE, OFF_CTL = OFF_KV + NST * TILE;
+    static constexpr int OFF_KV = 2 * QTILE, OFF_CTL = OFF_KV + NST * 2 * TILE;
     static constexpr int T_S = 0, T_O = 256, T_COLS = 512;  // tensor-memory columns
     static constexpr int REC = 2 * RM * D + 4 * RM;      // floats of a piece's record
-    using Sched = SeqSched<TP, true, 3, 8>;
+    using Sched = TcSched;
 };
 
 // Control block behind the ring.
 struct SeqCtl {
     SeqSmem sched;
-    uint64_t full[10], empty[10], s_full[2], p_full[2], o_full[2], q_full[2];
+    uint64_t full[8], empty[8], q_full[2];
+    uint64_t s_full[2][2], p_full[2][2];  // scores and weights of a stream's buffers
+    uint64_t o_full[2][2];                // the value product with a buffer's weights is done
     uint64_t q_free[2];          // a unit's score products are done
     uint64_t x_free[2];          // a unit of one tile no longer uses the queries' place
-    uint64_t v_req[4], v_ok[4];  // edge tiles, by their number modulo 4
-    uint64_t end;
+    // Edge tiles, by their number modulo 8.  (With no more ring stages than that a
+    // slot is used again only after both streams have released its tile's values.)
+    uint64_t v_req[8], v_ok[8];
+    uint64_t end[2];
     float m[2][128], l[2][128];  // exchange of a unit of one tile
-    unsigned bad[4][4];          // positions of an edge tile that were not finite
+    unsigned bad[8][2];          // positions of an edge tile that were not finite
     int last[2];
     unsigned tmem;
+    SeqRun run;
 };
 
 DV_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -105,12 +119,12 @@ DV_DEV void tc_commit(uint64_t *bar)
         : "memory");
 }
 // 32 columns of a thread's lane of tensor memory.
-DV_DEV void tm_ld(unsigned addr, float (&v)[32])
+DV_DEV void tm_ld(unsigned addr, float *v)
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-                 "%30, %31}, [%32];"
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                 "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, "
+                 "%26, %27, %28, %29, %30, %31}, [%32];"
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
                    "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]),
                    "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
@@ -120,7 +134,7 @@ DV_DEV void tm_ld(unsigned addr, float (&v)[32])
                  : "r"(addr));
 }
 // The loads into v have landed (v passes through, so that no use moves before it).
-DV_DEV void tm_wait_ld(float (&v)[32])
+DV_DEV void tm_wait_ld(float *v)
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
@@ -132,31 +146,27 @@ DV_DEV void tm_wait_ld(float (&v)[32])
                  :
                  : "memory");
 }
-DV_DEV void tm_st(unsigned addr, const float (&v)[32])
+// 16 columns, landed.
+DV_DEV void tm_ld16(unsigned addr, float *v)
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-                 "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, "
-                 "%31, %32};" ::"r"(addr),
-                 "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]),
-                 "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]),
-                 "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]),
-                 "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]),
-                 "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                 "%14, %15}, [%16];"
+                 "\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                   "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]),
+                   "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+                 : "r"(addr)
                  : "memory");
 }
-// Binary16 pairs r[0 .. 31] to 32 columns.
-DV_DEV void tm_st_pairs(unsigned addr, const unsigned *r)
+DV_DEV void tm_st16(unsigned addr, const unsigned *r)
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-                 "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, "
-                 "%31, %32};" ::"r"(addr),
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+                 "%15, %16};" ::"r"(addr),
                  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-                 "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
-                 "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-                 "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
-                 "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+                 "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+                 "r"(r[13]), "r"(r[14]), "r"(r[15])
                  : "memory");
 }
 DV_DEV void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -180,6 +190,27 @@ DV_DEV void group_sync(int bar)
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(N) : "memory");
 }
 
+// True once the phase with this parity is complete; false after 2^21 polls of
+// at most a microsecond each.
+DV_DEV bool seq_wait(uint64_t *bar, unsigned parity)
+{
+    const unsigned b = smem_addr(bar);
+#pragma unroll 1
+    for (int it = 0; it < kKvSpin; ++it) {
+        unsigned ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(b), "r"(parity & 1), "r"(1000)
+            : "memory");
+        if (ok)
+            return true;
+    }
+    return false;
+}
+
 // A role's waits: after one has run out the others no longer wait (the
 // results are lost, the status says so, every loop still ends).
 struct SeqWaiter {
@@ -187,16 +218,16 @@ struct SeqWaiter {
     bool dead = false;
     DV_DEV void operator()(uint64_t *bar, unsigned parity)
     {
-        if (!dead && !bar_wait(smem_addr(bar), parity & 1)) {
+        if (!dead && !seq_wait(bar, parity)) {
             dead = true;
             set_status(status, DV_ERR_TIMEOUT);
         }
     }
 };
 
-// A piece's tiles as both streams see them, and its operands' places in the
-// ring (counted from the piece's first): of a pair keys and values in turn, of
-// a single tile a tile's keys before the values of the one before.
+// A piece's tiles as both streams see them.  Entry e of its part of the ring
+// holds the keys of tile e and the values of tile e - 2, which are used together
+// (two tiles' scores are computed ahead): one wait for both.
 template <class C>
 struct Plan {
     int n, n0;       // tiles; of them, a pair's first 128 rows' own
@@ -206,37 +237,11 @@ struct Plan {
     {
         pair = x.pair;
         n = x.k1 - x.k0;
-        n0 = pair ? min(max(((x.pos + (1 << a.tlog) + C::TP - 1) >> 7) - x.k0, 0), n) : n;
-        edge = min(max(((x.pos + 1) >> 7) - x.k0, 0), n);
+        n0 = pair ? min(max((x.pos + (1 << a.tlog) + C::TP - 1) / C::TP - x.k0, 0), n) : n;
+        edge = min(max((x.pos + 1) / C::TP - x.k0, 0), n);
     }
-    DV_DEV unsigned k_at(int t) const { return pair ? 2 * t : max(2 * t - 1, 0); }
-    DV_DEV unsigned v_at(int t) const { return pair ? 2 * t + 1 : min(2 * t + 2, 2 * n - 1); }
     DV_DEV int of_stream(int w) const { return pair ? (w ? n : n0) : (n + 1 - w) >> 1; }
 };
-
-// 32 scores as weights under the reference m: v becomes pairs of binary16.
-// d (EDGE): the last seen column.
-template <bool EDGE>
-DV_DEV void weigh(float (&v)[32], int d, float scale, float m, float &top, float (&sum)[2],
-                  unsigned *pr)
-{
-    if (EDGE) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            v[i] = i <= d ? v[i] : -INFINITY;
-    }
-#pragma unroll
-    for (int i = 0; i < 32; i += 2)
-        top = max3(top, v[i], v[i + 1]);
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-        fma2(v[i], v[i + 1], scale, -m);
-        v[i] = ex2(v[i]);
-        v[i + 1] = ex2(v[i + 1]);
-        add2(sum[0], sum[1], v[i], v[i + 1]);
-        pr[i / 2] = h2(v[i], v[i + 1]);
-    }
-}
 
 constexpr float kSeqShift = 6.f;   // the first tile's largest weight is 2^6 to 2^7
 constexpr float kSeqLimit = 15.f;  // a weight above 2^15 moves the reference
@@ -263,40 +268,45 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         auto init = [](uint64_t &b, int n) { bar_init(smem_addr(&b), n); };
         for (int i = 0; i < NST; ++i) {
             init(ctl.full[i], 1);
-            init(ctl.empty[i], 1);
+            init(ctl.empty[i], 2);
         }
         for (int w = 0; w < 2; ++w) {
-            init(ctl.s_full[w], 1);
-            init(ctl.p_full[w], 4);
-            init(ctl.o_full[w], 1);
+            for (int b = 0; b < 2; ++b) {
+                init(ctl.s_full[w][b], 1);
+                init(ctl.p_full[w][b], 4);
+                init(ctl.o_full[w][b], 1);
+            }
             init(ctl.q_full[w], 1);
-            init(ctl.q_free[w], 1);
+            init(ctl.end[w], 1);
+            init(ctl.q_free[w], 2);
             init(ctl.x_free[w], 4);
         }
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
             init(ctl.v_req[i], 1);
             init(ctl.v_ok[i], 1);
         }
-        init(ctl.end, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tc_fence_before();
-    const SeqRun run = Sched::init(a, ctl.sched);  // (barriers)
+    const SeqRun run0 = Sched::init(a, ctl.sched);  // (barriers)
+    if (tid == 0)
+        ctl.run = run0;
+    __syncthreads();
+    const SeqRun &run = ctl.run;
     tc_fence_after();
     const unsigned tmem = ctl.tmem;
     SeqWaiter wait{a.status};
-    typename Sched::Walk walk(a, run);
     typename Sched::Piece x = {};
 
     if (warp == 8) {
         // ---- keys and values
         unsigned i = 0;  // ring entries so far
-        const int np = a.pk ? TP / a.page : 1;  // pages of a tile (lane: its page)
+        const int rows = a.pk ? min(a.page, TP) : TP, np = TP / rows;  // of a copy; copies of a tile
         const int none = a.pk ? a.n_pages * a.Hkv : 0;
-        // where this lane's page of tile t lies: the row (head) of the pool, or
+        // where this lane's page of tile t lies: the page and head in the pool, or
         // one behind the pool, which reads as zeros
         auto page_of = [&](int t) {
-            const int p = t * TP + lane * a.page;
+            const int p = t * TP + lane * rows;
             if (lane >= np || p >= x.pos + x.ntok)
                 return none;
             const int pg = __ldg(a.tables + (long long)x.b * a.width + p / a.page);
@@ -306,55 +316,65 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             return pg * a.Hkv + x.hkv;
         };
-        auto load = [&](const CUtensorMap *map, int t, int z) {
-            const unsigned st = i % NST, full = smem_addr(&ctl.full[st]);
-            if (i >= NST)
-                wait(&ctl.empty[st], i / NST - 1);
-            ++i;
-            if (wait.dead)
-                return;
-            if (lane == 0)
-                bar_expect(full, C::TILE);
-            __syncwarp();
-            const unsigned dst = sbase + C::OFF_KV + st * C::TILE;
+        auto load = [&](const CUtensorMap *map, unsigned dst, unsigned full, int t, int z) {
             if (lane < np) {
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
                     if (a.pk)
-                        tma_load(dst + c * C::HALF + lane * a.page * 128, map, 64 * c, 0, z, full);
+                        tma_load(dst + c * C::HALF + lane * rows * 128, map, 64 * c,
+                                 t * TP & (a.page - 1), z, full);
                     else
                         tma_load(dst + c * C::HALF, map, 64 * c, x.tok - x.pos + t * TP, x.hkv,
                                  full);
                 }
             }
         };
-        while (walk.next(x)) {
-            const int lag = x.pair ? 0 : 1;
-            int z = 0, zn = a.pk ? page_of(x.k0) : 0, zv = 0;
-            for (int t = x.k0; t < x.k1 + lag; ++t) {
-                zv = z;
+        typename Sched::Walk walk;
+        walk.start(a, run);
+#pragma unroll 1
+        while (walk.next(a, run, x)) {
+            int z = 0, z1 = 0, z2 = 0;  // of tile t, t - 1, t - 2
+            int zn = a.pk ? page_of(x.k0) : 0;
+#pragma unroll 1
+            for (int t = x.k0; t < x.k1 + 2; ++t, ++i) {
+                const unsigned st = i % NST, full = smem_addr(&ctl.full[st]);
+                const unsigned dst = sbase + C::OFF_KV + st * 2 * C::TILE;
+                const bool k = t < x.k1, v = t - 2 >= x.k0;
+                z2 = z1;
+                z1 = z;
                 z = zn;
                 if (a.pk && t + 1 < x.k1)
                     zn = page_of(t + 1);
-                if (t < x.k1)
-                    load(&maps.k, t, z);
-                if (t - lag >= x.k0)
-                    load(&maps.v, t - lag, lag ? zv : z);
+                if (i >= NST)
+                    wait(&ctl.empty[st], i / NST - 1);
+                if (wait.dead)
+                    continue;
+                if (lane == 0)
+                    bar_expect(full, (k + v) * C::TILE);
+                __syncwarp();
+                if (k)
+                    load(&maps.k, dst, full, t, z);
+                if (v)
+                    load(&maps.v, dst + C::TILE, full, t - 2, z2);
             }
         }
         // no copy may outlive the CTA
         for (unsigned k = i < NST ? 0 : i - NST; k < i && !wait.dead; ++k)
-            bar_wait(smem_addr(&ctl.full[k % NST]), (k / NST) & 1);
+            seq_wait(&ctl.full[k % NST], (k / NST) & 1);
         if (wait.dead)
             for (int k = 0; k < NST; ++k) {  // (either phase: what was issued lands in time)
-                bar_wait(smem_addr(&ctl.full[k]), 0);
-                bar_wait(smem_addr(&ctl.full[k]), 1);
+                seq_wait(&ctl.full[k], 0);
+                seq_wait(&ctl.full[k], 1);
             }
-    } else if (warp == 10) {
-        // ---- queries
-        unsigned u = 0, pairs = 0, singles = 0;
+    } else if (warp == 11) {
+        // ---- queries, and value rows that some row does not see
+        unsigned u = 0, pairs = 0, singles = 0, base = 0, edges = 0;
         const unsigned bytes = (unsigned)(a.group * q_tokens) * 128 * (D / 64);
-        while (walk.next(x)) {
+        typename Sched::Walk walk;
+        walk.start(a, run);
+#pragma unroll 1
+        while (walk.next(a, run, x)) {
+#pragma unroll 1
             for (int w = 0; w < 2; ++w) {
                 if (u > 0)
                     wait(&ctl.q_free[w], u - 1);
@@ -365,151 +385,27 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     bar_expect(full, bytes);
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c)
-                        tma_load(sbase + w * C::TILE + c * C::HALF, &maps.q, 64 * c, x.h0,
+                        tma_load(sbase + w * C::QTILE + c * C::QHALF, &maps.q, 64 * c, x.h0,
                                  x.tok + (w << a.tlog), full);
                 }
                 __syncwarp();
             }
-            ++u;
-            pairs += x.pair;
-            singles += !x.pair;
-        }
-        if (u > 0)
-            bar_wait(smem_addr(&ctl.q_full[0]), (u - 1) & 1);
-        if (pairs > 0)
-            bar_wait(smem_addr(&ctl.q_full[1]), (pairs - 1) & 1);
-    } else if (warp == 9) {
-        // ---- products.  The warp runs its loop together, so that descriptors
-        // stay in uniform registers, and one thread issues.
-        constexpr uint32_t ID_S = tc_idesc(TP, false), ID_O = tc_idesc(D, true);
-        constexpr unsigned STAGE = C::TILE >> 4;
-        const uint64_t dq = tc_desc(sbase, 16), dk = tc_desc(sbase + C::OFF_KV, 16),
-                       dv = tc_desc(sbase + C::OFF_KV, C::HALF);
-        const bool one = elect_one();
-        unsigned base = 0, units = 0, pairs = 0, edges = 0, np[2] = {0, 0};
-        while (walk.next(x)) {
             const Plan<C> pl(a, x);
-            const int n = pl.n;
-            wait(&ctl.q_full[0], units);
-            auto keys = [&](int t) {  // tile t's keys are there
-                const unsigned i = base + pl.k_at(t);
-                wait(&ctl.full[i % NST], i / NST);
-                if (one && t >= pl.edge)
-                    bar_arrive(smem_addr(&ctl.v_req[(edges + t - pl.edge) & 3]));
-                tc_fence_after();
-            };
-            auto scores = [&](int w, int t, bool last) {
-                const unsigned st = (base + pl.k_at(t)) % NST;
-                const uint64_t q = dq + (pl.pair && w ? STAGE : 0u), k = dk + st * STAGE;
-                if (one && !wait.dead) {
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        tc_mma_ss(tmem + C::T_S + w * 128, q + (kk / 4) * (C::HALF >> 4) + (kk % 4) * 2,
-                                  k + (kk / 4) * (C::HALF >> 4) + (kk % 4) * 2, ID_S, kk > 0);
-                    tc_commit(&ctl.s_full[w]);
-                    if (last)
-                        tc_commit(&ctl.empty[st]);
-                }
-                __syncwarp();
-            };
-            auto values = [&](int w, int t, bool acc, bool end, bool last) {
-                const unsigned i = base + pl.v_at(t), st = i % NST;
-                wait(&ctl.full[st], i / NST);
-                if (t >= pl.edge) {
-                    const unsigned e = edges + t - pl.edge;
-                    wait(&ctl.v_ok[e & 3], e >> 2);
-                }
-                wait(&ctl.p_full[w], np[w]++);
-                tc_fence_after();
-                const uint64_t v = dv + st * STAGE;
-                if (one && !wait.dead) {
-#pragma unroll
-                    for (int kk = 0; kk < TP / 16; ++kk)
-                        tc_mma_ts(tmem + C::T_O + w * 128, tmem + C::T_S + w * 128 + kk * 8,
-                                  v + kk * (16 * 128 >> 4), ID_O, acc || kk > 0);
-                    if (last)
-                        tc_commit(&ctl.empty[st]);
-                    if (end)
-                        tc_commit(&ctl.o_full[w]);
-                }
-                __syncwarp();
-            };
-            auto free_q = [&](int w) {
-                if (one && !wait.dead)
-                    tc_commit(&ctl.q_free[w]);
-            };
-            if (pl.pair) {
-                const int n0 = pl.n0;
-                keys(0);
-                if (n0 > 0)
-                    scores(0, 0, false);
-                if (n0 <= 1)
-                    free_q(0);
-                wait(&ctl.q_full[1], pairs);
-                tc_fence_after();
-                scores(1, 0, true);
-                if (n == 1)
-                    free_q(1);
-                for (int t = 0; t < n; ++t) {
-                    if (t < n0)
-                        values(0, t, t > 0, t == n0 - 1, false);
-                    if (t + 1 < n) {
-                        keys(t + 1);
-                        if (t + 1 < n0)
-                            scores(0, t + 1, false);
-                        if (t + 1 == n0 - 1)
-                            free_q(0);
-                    }
-                    values(1, t, t > 0, t == n - 1, true);
-                    if (t + 1 < n)
-                        scores(1, t + 1, true);
-                    if (t + 1 == n - 1)
-                        free_q(1);
-                }
-            } else {
-                for (int t = 0; t < 2 && t < n; ++t) {
-                    keys(t);
-                    scores(t, t, true);
-                }
-                for (int t = 0; t < n; ++t) {
-                    values(t & 1, t, t > 1, t + 2 >= n, true);
-                    if (t + 2 < n) {
-                        keys(t + 2);
-                        scores(t & 1, t + 2, true);
-                    }
-                }
-                free_q(0);
-                free_q(1);
-            }
-            base += 2 * n;
-            edges += n - pl.edge;
-            ++units;
-            pairs += pl.pair;
-        }
-        // every product is done before tensor memory goes
-        if (one)
-            tc_commit(&ctl.end);
-        __syncwarp();
-        bar_wait(smem_addr(&ctl.end), 0);
-    } else if (warp == 11) {
-        // ---- value rows that some row does not see
-        unsigned base = 0, edges = 0;
-        while (walk.next(x)) {
-            const Plan<C> pl(a, x);
+#pragma unroll 1
             for (int t = pl.edge; t < pl.n; ++t, ++edges) {
                 // (asked for when the tile's keys are there: what the ring's stage held
                 // before its values has been waited for by then, so a parity tells the
                 // phases apart)
-                wait(&ctl.v_req[edges & 3], edges >> 2);
-                const unsigned i = base + pl.v_at(t), st = i % NST;
+                wait(&ctl.v_req[edges & 7], edges >> 3);
+                const unsigned i = base + t + 2, st = i % NST;
                 wait(&ctl.full[st], i / NST);
-                unsigned *const bad = ctl.bad[edges & 3];
-                if (lane < 4)
+                unsigned *const bad = ctl.bad[edges & 7];
+                if (lane < TP / 32)
                     bad[lane] = 0u;
                 __syncwarp();
                 // rows up to the first token's position are seen by all
                 const int r0 = max(0, x.pos + 1 - (x.k0 + t) * TP);
-                const unsigned at = sbase + C::OFF_KV + st * C::TILE;
+                const unsigned at = sbase + C::OFF_KV + st * 2 * C::TILE + C::TILE;
 #pragma unroll 1
                 for (int c = 0; c < D / 64; ++c)
 #pragma unroll 4
@@ -529,18 +425,137 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    bar_arrive(smem_addr(&ctl.v_ok[edges & 3]));
+                    bar_arrive(smem_addr(&ctl.v_ok[edges & 7]));
             }
-            base += 2 * pl.n;
+            base += pl.n + 2;
+            ++u;
+            pairs += x.pair;
+            singles += !x.pair;
         }
+        if (u > 0)
+            seq_wait(&ctl.q_full[0], (u - 1) & 1);
+        if (pairs > 0)
+            seq_wait(&ctl.q_full[1], (pairs - 1) & 1);
+    } else if (warp == 9 || warp == 10) {
+        // ---- products of stream w.  The warp runs its loop together, so that
+        // descriptors stay in uniform registers, and one thread issues.  Both
+        // warps follow the whole ring, entry by entry.
+        constexpr uint32_t ID_S = tc_idesc(TP, false), ID_O = tc_idesc(D, true);
+        constexpr unsigned STAGE = 2 * C::TILE >> 4;
+        const int w = warp - 9;
+        const uint64_t dk = tc_desc(sbase + C::OFF_KV, 16),
+                       dv = tc_desc(sbase + C::OFF_KV + C::TILE, C::HALF);
+        const unsigned tS = tmem + C::T_S + w * 128, tO = tmem + C::T_O + w * 128;
+        const bool one = elect_one();
+        unsigned units = 0, pairs = 0, edges = 0;
+        unsigned ns = 0, nv = 0;  // products so far
+        unsigned rs = 0, rp = 0;  // the ring's next stage and its phase
+        typename Sched::Walk walk;
+        walk.start(a, run);
+#pragma unroll 1
+        while (walk.next(a, run, x)) {
+            const Plan<C> pl(a, x);
+            // (the same in every lane, and known to be)
+            const int n = __shfl_sync(0xffffffffu, wait.dead ? 0 : pl.n, 0),
+                      n0 = __shfl_sync(0xffffffffu, pl.n0, 0),
+                      edge = __shfl_sync(0xffffffffu, pl.edge, 0),
+                      pair = __shfl_sync(0xffffffffu, (int)pl.pair, 0);
+            const int mine = pair ? (w ? n : n0) : (n + 1 - w) >> 1;
+            int left = mine;  // score products to come
+            auto uses = [&](int t) { return pair ? w || t < n0 : (t & 1) == w; };
+            const uint64_t dq = tc_desc(sbase + (pair ? w * C::QTILE : 0), 16);
+            wait(&ctl.q_full[0], units);
+            if (pair && w)
+                wait(&ctl.q_full[1], pairs);
+            // the other stream's queries of a pair; one's own if they have no tile
+            if (one && pair)
+                bar_arrive(smem_addr(&ctl.q_free[w ^ 1]));
+            if (one && !mine) {
+                if (pair)
+                    bar_arrive(smem_addr(&ctl.q_free[w]));
+                else
+                    for (int i = 0; i < 2; ++i)
+                        bar_arrive(smem_addr(&ctl.q_free[i]));
+            }
+#pragma unroll 1
+            for (int e = 0; e < n + 2; ++e) {
+                const int t = e - 2;
+                const unsigned st = rs;
+                wait(&ctl.full[st], rp);
+                if (++rs == NST) {
+                    rs = 0;
+                    rp ^= 1;
+                }
+                const bool scores = e < n && uses(e), values = t >= 0 && uses(t);
+                if (one && e < n && e >= edge && (pair ? w == 1 : scores))
+                    bar_arrive(smem_addr(&ctl.v_req[(edges + e - edge) & 7]));
+                if (values) {
+                    if (t >= edge) {
+                        const unsigned k = edges + t - edge;
+                        wait(&ctl.v_ok[k & 7], k >> 3);
+                    }
+                    const unsigned b = nv & 1;
+                    wait(&ctl.p_full[w][b], nv++ >> 1);
+                    tc_fence_after();
+                    const uint64_t v = dv + st * STAGE;
+                    if (one) {
+#pragma unroll
+                        for (int kk = 0; kk < TP / 16; ++kk)
+                            tc_mma_ts(tO, tS + b * 64 + kk * 8, v + kk * (16 * 128 >> 4), ID_O,
+                                      t > (pair ? 0 : 1) || kk > 0);
+                        tc_commit(&ctl.o_full[w][b]);
+                    }
+                    __syncwarp();
+                }
+                if (scores) {
+                    // (the buffer's weights have been read by then: the value product
+                    // with them was issued before)
+                    const unsigned b = ns++ & 1;
+                    const uint64_t k = dk + st * STAGE;
+                    --left;
+                    tc_fence_after();
+                    if (one) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            tc_mma_ss(tS + b * 64, dq + (kk / 4) * (C::QHALF >> 4) + (kk % 4) * 2,
+                                      k + (kk / 4) * (C::HALF >> 4) + (kk % 4) * 2, ID_S, kk > 0);
+                        tc_commit(&ctl.s_full[w][b]);
+                        if (left == 0) {
+                            tc_commit(&ctl.q_free[w]);
+                            if (!pair)
+                                tc_commit(&ctl.q_free[w ^ 1]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (one) {
+                    if (scores || values)
+                        tc_commit(&ctl.empty[st]);
+                    else
+                        bar_arrive(smem_addr(&ctl.empty[st]));
+                }
+                __syncwarp();
+            }
+            edges += n - edge;
+            ++units;
+            pairs += pair;
+        }
+        // every product is done before tensor memory goes
+        if (one)
+            tc_commit(&ctl.end[w]);
+        __syncwarp();
+        seq_wait(&ctl.end[w], 0);
     } else {
         // ---- softmax of stream w: a thread a row
         const int w = warp >> 2, row = tid & 127, rtok = row / a.group, rhead = row % a.group;
         const unsigned lanes = (unsigned)(32 * (warp & 3)) << 16;
         const unsigned tS = tmem + lanes + C::T_S + w * 128, tO = tmem + lanes + C::T_O + w * 128;
         const float scale = a.scale;
-        unsigned tiles = 0, edges = 0, ends = 0;
-        while (walk.next(x)) {
+        unsigned tiles = 0, edges = 0;
+        typename Sched::Walk walk;
+        walk.start(a, run);
+#pragma unroll 1
+        while (walk.next(a, run, x)) {
             const Plan<C> pl(a, x);
             const int n = pl.of_stream(w);
             const int tok0 = pl.pair && w ? 1 << a.tlog : 0;  // this stream's first token
@@ -549,93 +564,96 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const bool busy = __any_sync(0xffffffffu, on);  // the warp has a row
             const int lim = x.pos + tok0 + rtok;
             float m = -INFINITY, l = 0.f;
+#pragma unroll 1
             for (int j = 0; j < n; ++j, ++tiles) {
                 const int t = pl.pair ? j : 2 * j + w;
-                wait(&ctl.s_full[w], tiles);
+                const unsigned buf = tiles & 1, tP = tS + buf * 64;
+                wait(&ctl.s_full[w][buf], tiles >> 1);
                 if (busy) {
                     tc_fence_after();
                     const bool edge = t >= pl.edge;
-                    const bool cut = x.pos + tok0 < (x.k0 + t + 1) * TP - 1;  // for some row
-                    const int d = lim - (x.k0 + t) * TP;
-                    float top, sum[2], v[2][32];
-                    unsigned pr[64];
-                    auto pass = [&](float ms, auto edged) {
-                        constexpr bool E = decltype(edged)::value;
-                        top = -INFINITY;
-                        sum[0] = sum[1] = 0.f;
-                        tm_ld(tS, v[0]);
-                        tm_wait_ld(v[0]);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            if (c < 3)
-                                tm_ld(tS + 32 * (c + 1), v[(c + 1) & 1]);
-                            weigh<E>(v[c & 1], d - 32 * c, scale, ms, top, sum, pr + 16 * c);
-                            if (c < 3)
-                                tm_wait_ld(v[(c + 1) & 1]);
-                        }
-                    };
-                    auto both = [&](float ms) {
-                        if (cut)
-                            pass(ms, std::true_type{});
-                        else
-                            pass(ms, std::false_type{});
-                    };
-                    if (j == 0) {  // a first reference, by the tile's maximum
-                        top = -INFINITY;
+                    const int d = lim - (x.k0 + t) * TP;  // the last seen column
+                    float sum[4];
+                    unsigned pr[TP / 2];
+                    // Once, or twice where the reference had to move (a row's first
+                    // tile, or rarely): the scores are read again then, as keeping them
+                    // spilled registers into the shared memory that the products
+                    // saturate.
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            tm_ld(tS + 32 * c, v[0]);
-                            tm_wait_ld(v[0]);
+                    for (bool again = false;; again = true) {
+                        float v[TP], tops[4];
+                        tm_ld(tP, v);
+                        tm_ld(tP + 32, v + 32);
+                        tm_wait_ld(v);
+                        tm_wait_ld(v + 32);
+                        if (x.pos + tok0 < (x.k0 + t + 1) * TP - 1) {  // some row sees not all
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                top = fmaxf(top, !cut || 32 * c + i <= d ? v[0][i] : -INFINITY);
+                            for (int i = 0; i < TP; ++i)
+                                v[i] = i <= d ? v[i] : -INFINITY;
                         }
-                        m = floorf(top * scale) - kSeqShift;
-                    }
-                    both(m == -INFINITY ? 0.f : m);
-                    const float high = top * scale;
-                    const bool need = m == -INFINITY ? high > -INFINITY : high - m > kSeqLimit;
-                    if (__any_sync(0xffffffffu, need)) {
-                        // (the tile before's value product is done: this tile's scores
-                        // came after it)
+                        const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            sum[k] = 0.f;
+                            tops[k] = -INFINITY;
+                        }
+#pragma unroll
+                        for (int i = 0; i < TP; i += 2) {
+                            float p = v[i], q = v[i + 1];
+                            tops[i / 2 % 4] = max3(tops[i / 2 % 4], p, q);
+                            fma2(p, q, scale, -ms);
+                            p = ex2(p);
+                            q = ex2(q);
+                            add2(sum[i & 2], sum[(i & 2) + 1], p, q);
+                            pr[i / 2] = h2(p, q);
+                        }
+                        const float high = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
+                        const bool need =
+                            !again && (m == -INFINITY ? high > -INFINITY : high - m > kSeqLimit);
+                        if (!__any_sync(0xffffffffu, need))
+                            break;
                         const float mn = need ? floorf(high) - kSeqShift : m;
                         const float f = need ? pow2(m - mn) : 1.f;
                         m = mn;
                         l *= f;
                         if (j > 0) {
+                            // (at rest once the product before is done; this one's is
+                            // not issued yet, so a parity tells)
+                            wait(&ctl.o_full[w][buf ^ 1], (tiles - 1) >> 1);
+                            tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                tm_ld(tO + c, v[0]);
-                                tm_wait_ld(v[0]);
+                            for (int c = 0; c < D; c += 16) {
+                                float y[16];
+                                unsigned z[16];
+                                tm_ld16(tO + c, y);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    v[0][i] *= f;
-                                tm_st(tO + c, v[0]);
+                                for (int i = 0; i < 16; ++i)
+                                    z[i] = __float_as_uint(y[i] * f);
+                                tm_st16(tO + c, z);
                             }
                         }
-                        both(m == -INFINITY ? 0.f : m);
                     }
-                    l += sum[0] + sum[1];
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tm_st16(tP, pr);
+                    tm_st16(tP + 16, pr + 16);
                     if (edge) {  // a row that sees what was taken out is not finite
                         const unsigned e = edges + t - pl.edge;
-                        wait(&ctl.v_ok[e & 3], e >> 2);
-                        const unsigned *bad = ctl.bad[e & 3];
+                        wait(&ctl.v_ok[e & 7], e >> 3);
+                        const unsigned *bad = ctl.bad[e & 7];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int k = 0; k < TP / 32; ++k) {
                             const int s = d - 32 * k;
                             const unsigned seen = s < 0 ? 0u : s >= 31 ? ~0u : (2u << s) - 1;
                             if (bad[k] & seen)
                                 l = __int_as_float(0x7fc00000);
                         }
                     }
-                    tm_st_pairs(tS, pr);
-                    tm_st_pairs(tS + 32, pr + 32);
                     tm_wait_st();
                     tc_fence_before();
                 }
                 __syncwarp();
                 if (lane == 0)
-                    bar_arrive(smem_addr(&ctl.p_full[w]));
+                    bar_arrive(smem_addr(&ctl.p_full[w][buf]));
             }
             edges += pl.n - pl.edge;
 
@@ -646,7 +664,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             float *const rec = a.rec + (size_t)Sched::slot(run.c, x.c0) * C::REC;
             float *const rec_m = rec + 2 * RM * D + w * 2 * RM, *const rec_l = rec_m + RM;
             if (n > 0) {
-                wait(&ctl.o_full[w], ends++);
+                wait(&ctl.o_full[w][(tiles - 1) & 1], (tiles - 1) >> 1);
                 tc_fence_after();
             }
             auto st8h = [&](int c, const float *y, float f) {  // 8 values of the result
@@ -666,20 +684,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (busy) {
                     const float f = l == 0.f ? 0.f : __frcp_rn(l);
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        float y[32];
-                        if (n > 0) {
-                            tm_ld(tO + c, y);
-                            tm_wait_ld(y);
-                        }
+                    for (int c = 0; c < D; c += 16) {
+                        float y[16];
+                        if (n > 0)
+                            tm_ld16(tO + c, y);
                         if (whole) {
                             if (on)
 #pragma unroll
-                                for (int i = 0; i < 32; i += 8)
+                                for (int i = 0; i < 16; i += 8)
                                     st8h(c + i, y + i, f);
                         } else if (on && n > 0) {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4)
+                            for (int i = 0; i < 16; i += 4)
                                 __stcg(rec_at(rec, r0 + row, (c + i) / 4),
                                        make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]));
                         }
@@ -694,16 +710,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 group_sync<256>(1);  // (both have left the unit before, too)
                 ctl.m[w][row] = m;
                 ctl.l[w][row] = l;
-                float4 *const give = reinterpret_cast<float4 *>(smem + (w ^ 1) * C::TILE) + row;
-                const float4 *const get = reinterpret_cast<float4 *>(smem + w * C::TILE) + row;
+                float4 *const give = reinterpret_cast<float4 *>(smem + (w ^ 1) * C::QTILE) + row;
+                const float4 *const get = reinterpret_cast<float4 *>(smem + w * C::QTILE) + row;
                 if (busy && n > 0) {
 #pragma unroll 1
-                    for (int c = 0; c < HC; c += 32) {
-                        float y[32];
-                        tm_ld(tO + (w ^ 1) * HC + c, y);
-                        tm_wait_ld(y);
+                    for (int c = 0; c < HC; c += 16) {
+                        float y[16];
+                        tm_ld16(tO + (w ^ 1) * HC + c, y);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
+                        for (int i = 0; i < 16; i += 4)
                             give[(c + i) / 4 * RM] = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
                     }
                 }
@@ -717,14 +732,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     m = M;
                     const float f = l == 0.f ? 0.f : __frcp_rn(l);
 #pragma unroll 1
-                    for (int c = 0; c < HC; c += 32) {
-                        float y[32];
-                        if (n > 0) {
-                            tm_ld(tO + w * HC + c, y);
-                            tm_wait_ld(y);
-                        }
+                    for (int c = 0; c < HC; c += 16) {
+                        float y[16];
+                        if (n > 0)
+                            tm_ld16(tO + w * HC + c, y);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
+                        for (int i = 0; i < 16; i += 4) {
                             float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
                             if (other)
                                 g = get[(c + i) / 4 * RM];
@@ -736,11 +749,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         if (on) {
                             if (whole) {
 #pragma unroll
-                                for (int i = 0; i < 32; i += 8)
+                                for (int i = 0; i < 16; i += 8)
                                     st8h(w * HC + c + i, y + i, f);
                             } else {
 #pragma unroll
-                                for (int i = 0; i < 32; i += 4)
+                                for (int i = 0; i < 16; i += 4)
                                     __stcg(rec_at(rec, row, (w * HC + c + i) / 4),
                                            make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]));
                             }
@@ -858,7 +871,7 @@ cudaError_t launch_tc(SeqAttnArgs a, int nsm, cudaStream_t st)
 {
     auto kern = k_seq_tc<C>;
     constexpr size_t smem = C::OFF_CTL + sizeof(SeqCtl);
-    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+    static_assert(smem <= 227 * 1024 && C::NST <= 8, "shared memory of a CTA; see SeqCtl");
     static DeviceOnce once;
     cudaError_t e = once.run([&] {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -882,7 +895,8 @@ cudaError_t launch_tc(SeqAttnArgs a, int nsm, cudaStream_t st)
         const SeqRowsArgs &r = i ? a.v : a.k;
         if (a.pk)  // (dimension, row of a page, page and head)
             e = enc(m, i ? a.pv : a.pk, {D, (unsigned)a.page, (unsigned)(a.n_pages * a.Hkv)},
-                    {D, (long long)D * a.page}, {64, (unsigned)a.page, 1});
+                    {D, (long long)D * a.page},
+                    {64, (unsigned)(a.page < C::TP ? a.page : C::TP), 1});
         else  // (dimension, token, head)
             e = enc(m, r.p, {D, (unsigned)a.T, (unsigned)a.Hkv},
                     {a.T > 1 ? r.st : D, a.Hkv > 1 ? r.sh : D}, {64, C::TP, 1});
