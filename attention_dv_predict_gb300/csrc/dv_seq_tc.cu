@@ -190,11 +190,22 @@ DV_DEV void group_sync(int bar)
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(N) : "memory");
 }
 
+DV_DEV bool seq_try(unsigned bar, unsigned parity)
+{
+    unsigned ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity & 1)
+        : "memory");
+    return ok;
+}
 // True once the phase with this parity is complete; false after 2^21 polls of
 // at most a microsecond each.
-DV_DEV bool seq_wait(uint64_t *bar, unsigned parity)
+__device__ __noinline__ bool seq_wait_on(unsigned bar, unsigned parity)
 {
-    const unsigned b = smem_addr(bar);
 #pragma unroll 1
     for (int it = 0; it < kKvSpin; ++it) {
         unsigned ok;
@@ -203,22 +214,27 @@ DV_DEV bool seq_wait(uint64_t *bar, unsigned parity)
             "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
-            : "r"(b), "r"(parity & 1), "r"(1000)
+            : "r"(bar), "r"(parity & 1), "r"(1000)
             : "memory");
         if (ok)
             return true;
     }
     return false;
 }
+DV_DEV bool seq_wait(uint64_t *bar, unsigned parity)
+{
+    return seq_try(smem_addr(bar), parity) || seq_wait_on(smem_addr(bar), parity);
+}
 
 // A role's waits: after one has run out the others no longer wait (the
-// results are lost, the status says so, every loop still ends).
+// results are lost, the status says so, every loop still ends).  What is over
+// already costs a poll and a branch.
 struct SeqWaiter {
     int *status;
     bool dead = false;
     DV_DEV void operator()(uint64_t *bar, unsigned parity)
     {
-        if (!dead && !seq_wait(bar, parity)) {
+        if (!seq_try(smem_addr(bar), parity) && !dead && !seq_wait_on(smem_addr(bar), parity)) {
             dead = true;
             set_status(status, DV_ERR_TIMEOUT);
         }
@@ -477,15 +493,61 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     for (int i = 0; i < 2; ++i)
                         bar_arrive(smem_addr(&ctl.q_free[i]));
             }
-#pragma unroll 1
-            for (int e = 0; e < n + 2; ++e) {
-                const int t = e - 2;
+            auto entry = [&]() {  // the next ring entry is there
+                wait(&ctl.full[rs], rp);
                 const unsigned st = rs;
-                wait(&ctl.full[st], rp);
                 if (++rs == NST) {
                     rs = 0;
                     rp ^= 1;
                 }
+                return st;
+            };
+            auto value_product = [&](unsigned st, bool acc) {
+                const unsigned b = nv & 1;
+                wait(&ctl.p_full[w][b], nv++ >> 1);
+                tc_fence_after();
+                const uint64_t v = dv + st * STAGE;
+                if (one) {
+#pragma unroll
+                    for (int kk = 0; kk < TP / 16; ++kk)
+                        tc_mma_ts(tO, tS + b * 64 + kk * 8, v + kk * (16 * 128 >> 4), ID_O, acc || kk > 0);
+                    tc_commit(&ctl.o_full[w][b]);
+                }
+            };
+            // (the buffer's weights have been read by then: the value product with
+            // them was issued before)
+            auto score_product = [&](unsigned st) {
+                const unsigned b = ns++ & 1;
+                const uint64_t k = dk + st * STAGE;
+                if (one) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        tc_mma_ss(tS + b * 64, dq + (kk / 4) * (C::QHALF >> 4) + (kk % 4) * 2,
+                                  k + (kk / 4) * (C::HALF >> 4) + (kk % 4) * 2, ID_S, kk > 0);
+                    tc_commit(&ctl.s_full[w][b]);
+                }
+                --left;
+            };
+            // Most entries of a pair have both products and no edge: nothing else is
+            // done there, as every instruction keeps the tensor cores waiting.
+            const int plain = pair ? min(mine - 1, edge) : 0;
+            int e = 0;
+#pragma unroll 1
+            while (e < n + 2) {
+                if (e == 3) {
+#pragma unroll 1
+                    for (; e < plain; ++e) {
+                        const unsigned st = entry();
+                        value_product(st, true);
+                        score_product(st);
+                        if (one)
+                            tc_commit(&ctl.empty[st]);
+                        __syncwarp();
+                    }
+                }
+                const int t = e - 2;
+                const unsigned st = entry();
+                tc_fence_after();
                 const bool scores = e < n && uses(e), values = t >= 0 && uses(t);
                 if (one && e < n && e >= edge && (pair ? w == 1 : scores))
                     bar_arrive(smem_addr(&ctl.v_req[(edges + e - edge) & 7]));
@@ -494,47 +556,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         const unsigned k = edges + t - edge;
                         wait(&ctl.v_ok[k & 7], k >> 3);
                     }
-                    const unsigned b = nv & 1;
-                    wait(&ctl.p_full[w][b], nv++ >> 1);
-                    tc_fence_after();
-                    const uint64_t v = dv + st * STAGE;
-                    if (one) {
-#pragma unroll
-                        for (int kk = 0; kk < TP / 16; ++kk)
-                            tc_mma_ts(tO, tS + b * 64 + kk * 8, v + kk * (16 * 128 >> 4), ID_O,
-                                      t > (pair ? 0 : 1) || kk > 0);
-                        tc_commit(&ctl.o_full[w][b]);
-                    }
-                    __syncwarp();
+                    value_product(st, t > (pair ? 0 : 1));
                 }
-                if (scores) {
-                    // (the buffer's weights have been read by then: the value product
-                    // with them was issued before)
-                    const unsigned b = ns++ & 1;
-                    const uint64_t k = dk + st * STAGE;
-                    --left;
-                    tc_fence_after();
-                    if (one) {
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            tc_mma_ss(tS + b * 64, dq + (kk / 4) * (C::QHALF >> 4) + (kk % 4) * 2,
-                                      k + (kk / 4) * (C::HALF >> 4) + (kk % 4) * 2, ID_S, kk > 0);
-                        tc_commit(&ctl.s_full[w][b]);
-                        if (left == 0) {
-                            tc_commit(&ctl.q_free[w]);
-                            if (!pair)
-                                tc_commit(&ctl.q_free[w ^ 1]);
-                        }
-                    }
-                    __syncwarp();
-                }
+                if (scores)
+                    score_product(st);
                 if (one) {
+                    if (scores && left == 0) {
+                        tc_commit(&ctl.q_free[w]);
+                        if (!pair)
+                            tc_commit(&ctl.q_free[w ^ 1]);
+                    }
                     if (scores || values)
                         tc_commit(&ctl.empty[st]);
                     else
                         bar_arrive(smem_addr(&ctl.empty[st]));
                 }
                 __syncwarp();
+                ++e;
             }
             edges += n - edge;
             ++units;
