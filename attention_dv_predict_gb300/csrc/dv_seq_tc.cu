@@ -169,6 +169,15 @@ DV_DEV void tm_st16(unsigned addr, const unsigned *r)
                  "r"(r[13]), "r"(r[14]), "r"(r[15])
                  : "memory");
 }
+// 8 columns.
+DV_DEV void tm_st8(unsigned addr, const unsigned *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                     addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7])
+                 : "memory");
+}
 DV_DEV void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 DV_DEV bool elect_one()
@@ -190,6 +199,20 @@ DV_DEV void group_sync(int bar)
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(N) : "memory");
 }
 
+// Whether the phase with this parity is complete, without waiting.
+DV_DEV bool seq_test(uint64_t *bar, unsigned parity)
+{
+    unsigned ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity & 1)
+        : "memory");
+    return ok;
+}
+// The same; may wait a little.
 DV_DEV bool seq_try(unsigned bar, unsigned parity)
 {
     unsigned ok;
@@ -602,54 +625,67 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const bool busy = __any_sync(0xffffffffu, on);  // the warp has a row
             const int lim = x.pos + tok0 + rtok;
             float m = -INFINITY, l = 0.f;
-#pragma unroll 1
-            for (int j = 0; j < n; ++j, ++tiles) {
-                const int t = pl.pair ? j : 2 * j + w;
+            bool ready = false;  // the next scores are there already
+            // One tile: `edged` if some row does not see all of it, or another stream's
+            // row does not.
+            auto tile = [&](int j, auto edged) {
+                constexpr bool EDGE = decltype(edged)::value;
                 const unsigned buf = tiles & 1, tP = tS + buf * 64;
-                wait(&ctl.s_full[w][buf], tiles >> 1);
+                if (!ready)
+                    wait(&ctl.s_full[w][buf], tiles >> 1);
+                __syncwarp();
                 if (busy) {
                     tc_fence_after();
-                    const bool edge = t >= pl.edge;
-                    const int d = lim - (x.k0 + t) * TP;  // the last seen column
-                    float sum[4];
-                    unsigned pr[TP / 2];
-                    // Once, or twice where the reference had to move (a row's first
-                    // tile, or rarely): the scores are read again then, as keeping them
-                    // spilled registers into the shared memory that the products
-                    // saturate.
-#pragma unroll 1
-                    for (bool again = false;; again = true) {
-                        float v[TP], tops[4];
-                        tm_ld(tP, v);
-                        tm_ld(tP + 32, v + 32);
-                        tm_wait_ld(v);
-                        tm_wait_ld(v + 32);
-                        if (x.pos + tok0 < (x.k0 + t + 1) * TP - 1) {  // some row sees not all
+                    const int t = EDGE ? (pl.pair ? j : 2 * j + w) : 0;
+                    const int d = EDGE ? lim - (x.k0 + t) * TP : 0;  // the last seen column
+                    float v[TP], sum[4], tops[4];
+                    // 32 scores as weights under ms, stored 16 at a time over scores that
+                    // are in registers by then (all of them, where that was not so before)
+                    auto weigh = [&](int c0, float ms) {
 #pragma unroll
-                            for (int i = 0; i < TP; ++i)
-                                v[i] = i <= d ? v[i] : -INFINITY;
+                        for (int c = c0; c < c0 + 32; c += 16) {
+                            unsigned pr[8];
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                float p = v[c + i], q = v[c + i + 1];
+                                tops[i / 2 % 4] = max3(tops[i / 2 % 4], p, q);
+                                fma2(p, q, scale, -ms);
+                                p = ex2(p);
+                                q = ex2(q);
+                                add2(sum[i & 2], sum[(i & 2) + 1], p, q);
+                                pr[i / 2] = h2(p, q);
+                            }
+                            tm_st8(tP + c / 2, pr);
                         }
-                        const float ms = m == -INFINITY ? 0.f : m;
+                    };
+                    auto start = [&]() {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             sum[k] = 0.f;
                             tops[k] = -INFINITY;
                         }
+                    };
+                    auto mask = [&](int c0) {
+                        if (EDGE) {
 #pragma unroll
-                        for (int i = 0; i < TP; i += 2) {
-                            float p = v[i], q = v[i + 1];
-                            tops[i / 2 % 4] = max3(tops[i / 2 % 4], p, q);
-                            fma2(p, q, scale, -ms);
-                            p = ex2(p);
-                            q = ex2(q);
-                            add2(sum[i & 2], sum[(i & 2) + 1], p, q);
-                            pr[i / 2] = h2(p, q);
+                            for (int i = c0; i < c0 + 32; ++i)
+                                v[i] = i <= d ? v[i] : -INFINITY;
                         }
-                        const float high = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
-                        const bool need =
-                            !again && (m == -INFINITY ? high > -INFINITY : high - m > kSeqLimit);
-                        if (!__any_sync(0xffffffffu, need))
-                            break;
+                    };
+                    const float ms = m == -INFINITY ? 0.f : m;
+                    start();
+                    tm_ld(tP, v);
+                    tm_wait_ld(v);
+                    tm_ld(tP + 32, v + 32);
+                    mask(0);
+                    weigh(0, ms);
+                    tm_wait_ld(v + 32);
+                    mask(32);
+                    weigh(32, ms);
+                    ready = seq_test(&ctl.s_full[w][buf ^ 1], (tiles + 1) >> 1);
+                    const float high = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
+                    const bool need = m == -INFINITY ? high > -INFINITY : high - m > kSeqLimit;
+                    if (__any_sync(0xffffffffu, need)) {  // (a row's first tile, or rarely)
                         const float mn = need ? floorf(high) - kSeqShift : m;
                         const float f = need ? pow2(m - mn) : 1.f;
                         m = mn;
@@ -670,11 +706,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 tm_st16(tO + c, z);
                             }
                         }
+                        start();
+                        weigh(0, m == -INFINITY ? 0.f : m);
+                        weigh(32, m == -INFINITY ? 0.f : m);
                     }
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tm_st16(tP, pr);
-                    tm_st16(tP + 16, pr + 16);
-                    if (edge) {  // a row that sees what was taken out is not finite
+                    if (EDGE && t >= pl.edge) {  // a row that sees what was taken out is not finite
                         const unsigned e = edges + t - pl.edge;
                         wait(&ctl.v_ok[e & 7], e >> 3);
                         const unsigned *bad = ctl.bad[e & 7];
@@ -688,11 +725,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                     tm_wait_st();
                     tc_fence_before();
+                } else {
+                    ready = false;
                 }
                 __syncwarp();
                 if (lane == 0)
                     bar_arrive(smem_addr(&ctl.p_full[w][buf]));
-            }
+                ++tiles;
+            };
+            // (the first tile with an edge, of this stream's)
+            const int plain = min(n, pl.pair ? pl.edge : (pl.edge + 1 - w) >> 1);
+            int j = 0;
+#pragma unroll 1
+            for (; j < plain; ++j)
+                tile(j, std::false_type{});
+#pragma unroll 1
+            for (; j < n; ++j)
+                tile(j, std::true_type{});
             edges += pl.n - pl.edge;
 
             // ---- the piece's end
