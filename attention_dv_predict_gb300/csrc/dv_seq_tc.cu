@@ -51,9 +51,10 @@ struct SeqTcCfg {
     static constexpr int D = D_, TP = 64, RM = 128;
     static constexpr int TILE = TP * D * 2, HALF = TP * 128;    // keys or values; 64 dimensions
     static constexpr int QTILE = RM * D * 2, QHALF = RM * 128;  // queries of 128 rows
-    static constexpr int NST = D == 128 ? 5 : 8;               // ring stages
+    static constexpr int NST = D == 128 ? 4 : 8;               // ring stages
     static constexpr int THREADS = 384;
-    static constexpr int OFF_KV = 2 * QTILE, OFF_CTL = OFF_KV + NST * 2 * TILE;
+    static constexpr int OFF_KV = 2 * QTILE, OFF_OUT = OFF_KV + NST * 2 * TILE,
+                         OFF_CTL = OFF_OUT + 8 * 4096;  // (results: 64 dimensions of a warp's 32 rows)
     static constexpr int T_S = 0, T_O = 256, T_COLS = 512;  // tensor-memory columns
     static constexpr int REC = 2 * RM * D + 4 * RM;      // floats of a piece's record
     using Sched = TcSched;
@@ -491,8 +492,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         unsigned rs = 0, rp = 0;  // the ring's next stage and its phase
         typename Sched::Walk walk;
         walk.start(a, run);
+        // (the next piece is found while the last weights of one are waited for)
+        typename Sched::Piece next = {};
+        bool more = walk.next(a, run, x);
 #pragma unroll 1
-        while (walk.next(a, run, x)) {
+        for (; more; x = next) {
             const Plan<C> pl(a, x);
             // (the same in every lane, and known to be)
             const int n = __shfl_sync(0xffffffffu, wait.dead ? 0 : pl.n, 0),
@@ -568,6 +572,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         __syncwarp();
                     }
                 }
+                if (e == n)
+                    more = walk.next(a, run, next);
                 const int t = e - 2;
                 const unsigned st = entry();
                 tc_fence_after();
@@ -615,8 +621,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         unsigned tiles = 0, edges = 0;
         typename Sched::Walk walk;
         walk.start(a, run);
+        typename Sched::Piece next = {};
+        bool more = walk.next(a, run, x);
 #pragma unroll 1
-        while (walk.next(a, run, x)) {
+        for (; more; x = next) {
             const Plan<C> pl(a, x);
             const int n = pl.of_stream(w);
             const int tok0 = pl.pair && w ? 1 << a.tlog : 0;  // this stream's first token
@@ -744,23 +752,41 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 tile(j, std::true_type{});
             edges += pl.n - pl.edge;
 
-            // ---- the piece's end
+            // ---- the piece's end; the next one is found while its last product runs
+            more = walk.next(a, run, next);
             const bool whole = x.c0 == x.c1;
-            __half *const out = static_cast<__half *>(a.out) +
-                                ((long long)(x.tok + tok0 + rtok) * a.H + x.h0 + rhead) * D;
+            const long long off = ((long long)(x.tok + tok0 + rtok) * a.H + x.h0 + rhead) * D;
             float *const rec = a.rec + (size_t)Sched::slot(run.c, x.c0) * C::REC;
             float *const rec_m = rec + 2 * RM * D + w * 2 * RM, *const rec_l = rec_m + RM;
             if (n > 0) {
                 wait(&ctl.o_full[w][(tiles - 1) & 1], (tiles - 1) >> 1);
                 tc_fence_after();
             }
-            auto st8h = [&](int c, const float *y, float f) {  // 8 values of the result
-                uint4 u;
-                u.x = h2(y[0] * f, y[1] * f);
-                u.y = h2(y[2] * f, y[3] * f);
-                u.z = h2(y[4] * f, y[5] * f);
-                u.w = h2(y[6] * f, y[7] * f);
-                *reinterpret_cast<uint4 *>(out + c) = u;
+            // Results go to shared memory, 16 columns of a thread's row at a time, and from
+            // there to the output's rows in whole lines: a thread writing its own row
+            // took 7000 cycles a pair.
+            const unsigned mine = sbase + C::OFF_OUT + warp * 4096;
+            auto put = [&](int c, const float *y, float f) {  // columns c .. c + 15 of 64
+#pragma unroll
+                for (int i = 0; i < 16; i += 8)
+                    sts16(mine + lane * 128 + ((((c + i) >> 3) ^ (lane & 7)) << 4),
+                          h2(y[i] * f, y[i + 1] * f), h2(y[i + 2] * f, y[i + 3] * f),
+                          h2(y[i + 4] * f, y[i + 5] * f), h2(y[i + 6] * f, y[i + 7] * f));
+            };
+            const unsigned rows_on = __ballot_sync(0xffffffffu, on);
+            auto flush = [&](int c0, auto cols) {  // columns c0 .. of the warp's rows
+                constexpr int LPR = decltype(cols)::value / 8, RPI = 32 / LPR;
+                const int ch = lane % LPR;
+                __syncwarp();
+#pragma unroll
+                for (int r0 = 0; r0 < 32; r0 += RPI) {
+                    const int r = r0 + lane / LPR;
+                    const long long to = __shfl_sync(0xffffffffu, off, r);
+                    const uint4 u = lds16(mine + r * 128 + ((ch ^ (r & 7)) << 4));
+                    if ((rows_on >> r) & 1)
+                        *reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + to + c0 + 8 * ch) = u;
+                }
+                __syncwarp();
             };
             // four values of row r's piece, columns 4 c ..
             auto rec_at = [&](float *base, int r, int c) {
@@ -776,10 +802,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         if (n > 0)
                             tm_ld16(tO + c, y);
                         if (whole) {
-                            if (on)
-#pragma unroll
-                                for (int i = 0; i < 16; i += 8)
-                                    st8h(c + i, y + i, f);
+                            put(c & 63, y, f);
+                            if ((c & 63) == 48)
+                                flush(c - 48, std::integral_constant<int, 64>{});
                         } else if (on && n > 0) {
 #pragma unroll
                             for (int i = 0; i < 16; i += 4)
@@ -833,19 +858,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             y[i + 2] = n > 0 ? fmaf(y[i + 2], fw, g.z * fo) : g.z * fo;
                             y[i + 3] = n > 0 ? fmaf(y[i + 3], fw, g.w * fo) : g.w * fo;
                         }
-                        if (on) {
-                            if (whole) {
+                        if (whole) {
+                            put(c, y, f);
+                        } else if (on) {
 #pragma unroll
-                                for (int i = 0; i < 16; i += 8)
-                                    st8h(w * HC + c + i, y + i, f);
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 16; i += 4)
-                                    __stcg(rec_at(rec, row, (w * HC + c + i) / 4),
-                                           make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]));
-                            }
+                            for (int i = 0; i < 16; i += 4)
+                                __stcg(rec_at(rec, row, (w * HC + c + i) / 4),
+                                       make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]));
                         }
                     }
+                    if (whole)
+                        flush(w * HC, std::integral_constant<int, HC>{});
                     tc_fence_before();
                 }
                 fence_async_smem();
