@@ -646,51 +646,22 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     tc_fence_after();
                     const int t = EDGE ? (pl.pair ? j : 2 * j + w) : 0;
                     const int d = EDGE ? lim - (x.k0 + t) * TP : 0;  // the last seen column
-                    float v[TP], sum[4], tops[4];
-                    // 32 scores as weights under ms, stored 16 at a time over scores that
-                    // are in registers by then (all of them, where that was not so before)
-                    auto weigh = [&](int c0, float ms) {
-#pragma unroll
-                        for (int c = c0; c < c0 + 32; c += 16) {
-                            unsigned pr[8];
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                float p = v[c + i], q = v[c + i + 1];
-                                tops[i / 2 % 4] = max3(tops[i / 2 % 4], p, q);
-                                fma2(p, q, scale, -ms);
-                                p = ex2(p);
-                                q = ex2(q);
-                                add2(sum[i & 2], sum[(i & 2) + 1], p, q);
-                                pr[i / 2] = h2(p, q);
-                            }
-                            tm_st8(tP + c / 2, pr);
-                        }
-                    };
-                    auto start = [&]() {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            sum[k] = 0.f;
-                            tops[k] = -INFINITY;
-                        }
-                    };
-                    auto mask = [&](int c0) {
-                        if (EDGE) {
-#pragma unroll
-                            for (int i = c0; i < c0 + 32; ++i)
-                                v[i] = i <= d ? v[i] : -INFINITY;
-                        }
-                    };
-                    const float ms = m == -INFINITY ? 0.f : m;
-                    start();
+                    float v[TP], tops[4];
                     tm_ld(tP, v);
-                    tm_wait_ld(v);
                     tm_ld(tP + 32, v + 32);
-                    mask(0);
-                    weigh(0, ms);
+                    tm_wait_ld(v);
                     tm_wait_ld(v + 32);
-                    mask(32);
-                    weigh(32, ms);
-                    ready = seq_test(&ctl.s_full[w][buf ^ 1], (tiles + 1) >> 1);
+                    if (EDGE) {
+#pragma unroll
+                        for (int i = 0; i < TP; ++i)
+                            v[i] = i <= d ? v[i] : -INFINITY;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tops[k] = fmaxf(v[2 * k], v[2 * k + 1]);
+#pragma unroll
+                    for (int i = 8; i < TP; i += 2)
+                        tops[i / 2 % 4] = max3(tops[i / 2 % 4], v[i], v[i + 1]);
                     const float high = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
                     const bool need = m == -INFINITY ? high > -INFINITY : high - m > kSeqLimit;
                     if (__any_sync(0xffffffffu, need)) {  // (a row's first tile, or rarely)
@@ -714,10 +685,24 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 tm_st16(tO + c, z);
                             }
                         }
-                        start();
-                        weigh(0, m == -INFINITY ? 0.f : m);
-                        weigh(32, m == -INFINITY ? 0.f : m);
                     }
+                    const float ms = m == -INFINITY ? 0.f : m;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < TP; c += 16) {
+                        unsigned pr[8];
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            float p = v[c + i], q = v[c + i + 1];
+                            fma2(p, q, scale, -ms);
+                            p = ex2(p);
+                            q = ex2(q);
+                            add2(sum[i & 2], sum[(i & 2) + 1], p, q);
+                            pr[i / 2] = h2(p, q);
+                        }
+                        tm_st8(tP + c / 2, pr);
+                    }
+                    ready = seq_test(&ctl.s_full[w][buf ^ 1], (tiles + 1) >> 1);
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     if (EDGE && t >= pl.edge) {  // a row that sees what was taken out is not finite
                         const unsigned e = edges + t - pl.edge;
@@ -778,7 +763,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 constexpr int LPR = decltype(cols)::value / 8, RPI = 32 / LPR;
                 const int ch = lane % LPR;
                 __syncwarp();
-#pragma unroll
+#pragma unroll 2
                 for (int r0 = 0; r0 < 32; r0 += RPI) {
                     const int r = r0 + lane / LPR;
                     const long long to = __shfl_sync(0xffffffffu, off, r);
