@@ -62,6 +62,7 @@ struct SeqAttnArgs {
     // query heads of a KV head fill a unit's rows in groups of `group` (which
     // divides their number), `tq` tokens (a power of two) to 2^tlog x group rows
     int group, tlog;
+    int sub;                 // groups of a KV head's query heads
     float scale;             // softmax scale x log2(e)
     void *out;               // [T][H][D]
     float *rec;

@@ -171,6 +171,7 @@ void seq_group(SeqAttnArgs &a, int rows)
         }
     }
     a.tlog = log_tokens(a.group);
+    a.sub = G / a.group;
 }
 
 }  // namespace dv

@@ -210,12 +210,22 @@ struct SeqSched {
                 p.pair = PAIR && p.ntok > 1 << a.tlog;
                 p.b = b;
                 p.h0 = hs * a.group;
-                p.hkv = p.h0 / (a.H / a.Hkv);
+                p.hkv = a.sub == 1 ? hs : hs / a.sub;
                 const int wt = p.pair;  // (log2 of a tile's places)
-                const long long t0 = u0 + COST;
-                p.k0 = (int)max(0ll, (r.lo - t0 + wt) >> wt);
-                p.k1 = (int)max(0ll, min((long long)p.nt, (r.hi - t0 + wt) >> wt));
-                u0 = t0 + ((long long)p.nt << wt);
+                const long long t0 = u0 + COST, end = t0 + ((long long)p.nt << wt);
+                const bool head = t0 >= r.lo, tail = end <= r.hi;  // its first, last tile is here
+                p.k0 = 0;
+                p.k1 = p.nt;
+                p.c0 = p.c1 = r.c;
+                if (!head || !tail) {
+                    p.k0 = (int)max(0ll, (r.lo - t0 + wt) >> wt);
+                    p.k1 = (int)max(0ll, min((long long)p.nt, (r.hi - t0 + wt) >> wt));
+                    if (p.k0 > 0)
+                        p.c0 = run_of(r, t0);
+                    if (p.k1 < p.nt)
+                        p.c1 = run_of(r, t0 + ((long long)(p.nt - 1) << wt));
+                }
+                u0 = end;
                 if (++i >= units(a)) {
                     i = 0;
                     if (++hs == a.H / a.group) {
@@ -229,14 +239,8 @@ struct SeqSched {
                             u0 = max(u0, r.hi);
                     }
                 }
-                if (p.k0 >= p.k1)
-                    continue;
-                p.c0 = p.c1 = r.c;
-                if (p.k0 > 0)
-                    p.c0 = run_of(r, t0);
-                if (p.k1 < p.nt)
-                    p.c1 = run_of(r, t0 + ((long long)(p.nt - 1) << wt));
-                return true;
+                if (p.k0 < p.k1)
+                    return true;
             }
             return false;
         }

@@ -41,7 +41,7 @@ namespace dv {
 namespace {
 
 struct SeqMaps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, out;
 };
 
 using TcSched = SeqSched<64, true, 6, 16>;
@@ -51,10 +51,10 @@ struct SeqTcCfg {
     static constexpr int D = D_, TP = 64, RM = 128;
     static constexpr int TILE = TP * D * 2, HALF = TP * 128;    // keys or values; 64 dimensions
     static constexpr int QTILE = RM * D * 2, QHALF = RM * 128;  // queries of 128 rows
-    static constexpr int NST = D == 128 ? 4 : 8;               // ring stages
+    static constexpr int NST = D == 128 ? 3 : 8;               // ring stages
     static constexpr int THREADS = 384;
     static constexpr int OFF_KV = 2 * QTILE, OFF_OUT = OFF_KV + NST * 2 * TILE,
-                         OFF_CTL = OFF_OUT + 8 * 4096;  // (results: 64 dimensions of a warp's 32 rows)
+                         OFF_CTL = OFF_OUT + 2 * QTILE;  // (results of both streams)
     static constexpr int T_S = 0, T_O = 256, T_COLS = 512;  // tensor-memory columns
     static constexpr int REC = 2 * RM * D + 4 * RM;      // floats of a piece's record
     using Sched = TcSched;
@@ -66,8 +66,8 @@ struct SeqCtl {
     uint64_t full[8], empty[8], q_full[2];
     uint64_t s_full[2][2], p_full[2][2];  // scores and weights of a stream's buffers
     uint64_t o_full[2][2];                // the value product with a buffer's weights is done
-    uint64_t q_free[2];          // a unit's score products are done
-    uint64_t x_free[2];          // a unit of one tile no longer uses the queries' place
+    // A unit's score products are done: of a pair's streams each; of both.
+    uint64_t q_free[2], q_both;
     // Edge tiles, by their number modulo 8.  (With no more ring stages than that a
     // slot is used again only after both streams have released its tile's values.)
     uint64_t v_req[8], v_ok[8];
@@ -77,6 +77,7 @@ struct SeqCtl {
     int last[2];
     unsigned tmem;
     SeqRun run;
+    int4 plan[2][4];             // a products' warp: pieces between their keys and values
 };
 
 DV_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -181,6 +182,15 @@ DV_DEV void tm_st8(unsigned addr, const unsigned *r)
 }
 DV_DEV void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// A box of shared memory to (dimension, head, token) of the results.
+DV_DEV void tma_store(const CUtensorMap *map, int x, int h, int tok, unsigned src)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     map),
+                 "r"(x), "r"(h), "r"(tok), "r"(src)
+                 : "memory");
+}
+
 DV_DEV bool elect_one()
 {
     unsigned p;
@@ -265,9 +275,9 @@ struct SeqWaiter {
     }
 };
 
-// A piece's tiles as both streams see them.  Entry e of its part of the ring
-// holds the keys of tile e and the values of tile e - 2, which are used together
-// (two tiles' scores are computed ahead): one wait for both.
+// A piece's tiles as both streams see them.  Entry e of the ring holds the keys
+// of the run's tile e and the values of its tile e - 2, which are used together
+// (two tiles' scores are computed ahead, of the next piece too): one wait for both.
 template <class C>
 struct Plan {
     int n, n0;       // tiles; of them, a pair's first 128 rows' own
@@ -318,9 +328,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             init(ctl.q_full[w], 1);
             init(ctl.end[w], 1);
-            init(ctl.q_free[w], 2);
-            init(ctl.x_free[w], 4);
+            init(ctl.q_free[w], 1);
         }
+        init(ctl.q_both, 2);
         for (int i = 0; i < 8; ++i) {
             init(ctl.v_req[i], 1);
             init(ctl.v_ok[i], 1);
@@ -356,47 +366,53 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             return pg * a.Hkv + x.hkv;
         };
-        auto load = [&](const CUtensorMap *map, unsigned dst, unsigned full, int t, int z) {
+        // (row, z): where the lane's copies of a tile begin
+        auto load = [&](const CUtensorMap *map, unsigned dst, unsigned full, int row, int z) {
             if (lane < np) {
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    if (a.pk)
-                        tma_load(dst + c * C::HALF + lane * rows * 128, map, 64 * c,
-                                 t * TP & (a.page - 1), z, full);
-                    else
-                        tma_load(dst + c * C::HALF, map, 64 * c, x.tok - x.pos + t * TP, x.hkv,
-                                 full);
-                }
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load(dst + c * C::HALF + lane * rows * 128, map, 64 * c, row, z, full);
             }
         };
         typename Sched::Walk walk;
         walk.start(a, run);
+        int t = 0, zn = 0, row[3] = {}, z[3] = {};  // of the run's tiles e, e - 1, e - 2
+        bool more = true;
+        int behind = 0;  // tiles whose values are still to come
 #pragma unroll 1
-        while (walk.next(a, run, x)) {
-            int z = 0, z1 = 0, z2 = 0;  // of tile t, t - 1, t - 2
-            int zn = a.pk ? page_of(x.k0) : 0;
-#pragma unroll 1
-            for (int t = x.k0; t < x.k1 + 2; ++t, ++i) {
-                const unsigned st = i % NST, full = smem_addr(&ctl.full[st]);
-                const unsigned dst = sbase + C::OFF_KV + st * 2 * C::TILE;
-                const bool k = t < x.k1, v = t - 2 >= x.k0;
-                z2 = z1;
-                z1 = z;
-                z = zn;
+        for (;; ++i) {
+            if (more && t >= x.k1) {
+                more = walk.next(a, run, x);
+                t = x.k0;
+                if (more && a.pk)
+                    zn = page_of(t);
+            }
+            const bool v = i >= 2 && behind > 0;
+            if (!more && behind == 0)
+                break;
+            row[2] = row[1], row[1] = row[0];
+            z[2] = z[1], z[1] = z[0];
+            if (more) {
+                row[0] = a.pk ? t * TP & (a.page - 1) : x.tok - x.pos + t * TP;
+                z[0] = a.pk ? zn : x.hkv;
                 if (a.pk && t + 1 < x.k1)
                     zn = page_of(t + 1);
-                if (i >= NST)
-                    wait(&ctl.empty[st], i / NST - 1);
-                if (wait.dead)
-                    continue;
-                if (lane == 0)
-                    bar_expect(full, (k + v) * C::TILE);
-                __syncwarp();
-                if (k)
-                    load(&maps.k, dst, full, t, z);
-                if (v)
-                    load(&maps.v, dst + C::TILE, full, t - 2, z2);
             }
+            const unsigned st = i % NST, full = smem_addr(&ctl.full[st]);
+            const unsigned dst = sbase + C::OFF_KV + st * 2 * C::TILE;
+            if (i >= NST)
+                wait(&ctl.empty[st], i / NST - 1);
+            if (!wait.dead) {
+                if (lane == 0)
+                    bar_expect(full, ((int)more + v) * C::TILE);
+                __syncwarp();
+                if (more)
+                    load(&maps.k, dst, full, row[0], z[0]);
+                if (v)
+                    load(&maps.v, dst + C::TILE, full, row[2], z[2]);
+            }
+            behind += (int)more - v;
+            t += more;
         }
         // no copy may outlive the CTA
         for (unsigned k = i < NST ? 0 : i - NST; k < i && !wait.dead; ++k)
@@ -410,33 +426,53 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // ---- queries, and value rows that some row does not see
         unsigned u = 0, pairs = 0, singles = 0, base = 0, edges = 0;
         const unsigned bytes = (unsigned)(a.group * q_tokens) * 128 * (D / 64);
+        auto queries = [&](const typename Sched::Piece &q, int w) {
+            if (lane == 0 && !wait.dead && (w == 0 || q.pair)) {
+                const unsigned full = smem_addr(&ctl.q_full[w]);
+                bar_expect(full, bytes);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load(sbase + w * C::QTILE + c * C::QHALF, &maps.q, 64 * c, q.h0,
+                             q.tok + (w << a.tlog), full);
+            }
+            __syncwarp();
+        };
         typename Sched::Walk walk;
         walk.start(a, run);
+        typename Sched::Piece next = {};
+        bool more = walk.next(a, run, x);
+        if (more) {
+            queries(x, 0);
+            queries(x, 1);
+        }
 #pragma unroll 1
-        while (walk.next(a, run, x)) {
-#pragma unroll 1
-            for (int w = 0; w < 2; ++w) {
-                if (u > 0)
-                    wait(&ctl.q_free[w], u - 1);
-                if (singles > 0)
-                    wait(&ctl.x_free[w], singles - 1);
-                if (lane == 0 && !wait.dead && (w == 0 || x.pair)) {
-                    const unsigned full = smem_addr(&ctl.q_full[w]);
-                    bar_expect(full, bytes);
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                        tma_load(sbase + w * C::QTILE + c * C::QHALF, &maps.q, 64 * c, x.h0,
-                                 x.tok + (w << a.tlog), full);
-                }
-                __syncwarp();
-            }
+        for (; more; x = next) {
             const Plan<C> pl(a, x);
+            more = walk.next(a, run, next);
+            int loaded = 0;  // queries of the next piece on their way
+            // (sent for as soon as the products with this piece's are done, between its
+            // edge tiles too)
+            auto ahead = [&](bool must) {
+#pragma unroll 1
+                while (loaded < 2) {
+                    uint64_t *const bar = x.pair ? &ctl.q_free[loaded] : &ctl.q_both;
+                    const unsigned phase = x.pair ? pairs : singles;
+                    if (must)
+                        wait(bar, phase);
+                    else if (!__all_sync(0xffffffffu, seq_test(bar, phase)))
+                        return;
+                    if (more)
+                        queries(next, loaded);
+                    ++loaded;
+                }
+            };
 #pragma unroll 1
             for (int t = pl.edge; t < pl.n; ++t, ++edges) {
                 // (asked for when the tile's keys are there: what the ring's stage held
                 // before its values has been waited for by then, so a parity tells the
                 // phases apart)
                 wait(&ctl.v_req[edges & 7], edges >> 3);
+                ahead(false);
                 const unsigned i = base + t + 2, st = i % NST;
                 wait(&ctl.full[st], i / NST);
                 unsigned *const bad = ctl.bad[edges & 7];
@@ -467,7 +503,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (lane == 0)
                     bar_arrive(smem_addr(&ctl.v_ok[edges & 7]));
             }
-            base += pl.n + 2;
+            ahead(true);
+            base += pl.n;
             ++u;
             pairs += x.pair;
             singles += !x.pair;
@@ -492,120 +529,129 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         unsigned rs = 0, rp = 0;  // the ring's next stage and its phase
         typename Sched::Walk walk;
         walk.start(a, run);
-        // (the next piece is found while the last weights of one are waited for)
-        typename Sched::Piece next = {};
-        bool more = walk.next(a, run, x);
-#pragma unroll 1
-        for (; more; x = next) {
-            const Plan<C> pl(a, x);
-            // (the same in every lane, and known to be)
-            const int n = __shfl_sync(0xffffffffu, wait.dead ? 0 : pl.n, 0),
-                      n0 = __shfl_sync(0xffffffffu, pl.n0, 0),
-                      edge = __shfl_sync(0xffffffffu, pl.edge, 0),
-                      pair = __shfl_sync(0xffffffffu, (int)pl.pair, 0);
-            const int mine = pair ? (w ? n : n0) : (n + 1 - w) >> 1;
-            int left = mine;  // score products to come
-            auto uses = [&](int t) { return pair ? w || t < n0 : (t & 1) == w; };
-            const uint64_t dq = tc_desc(sbase + (pair ? w * C::QTILE : 0), 16);
-            wait(&ctl.q_full[0], units);
-            if (pair && w)
-                wait(&ctl.q_full[1], pairs);
-            // the other stream's queries of a pair; one's own if they have no tile
-            if (one && pair)
-                bar_arrive(smem_addr(&ctl.q_free[w ^ 1]));
-            if (one && !mine) {
-                if (pair)
-                    bar_arrive(smem_addr(&ctl.q_free[w]));
-                else
-                    for (int i = 0; i < 2; ++i)
-                        bar_arrive(smem_addr(&ctl.q_free[i]));
+        auto entry = [&]() {  // the next ring entry is there
+            wait(&ctl.full[rs], rp);
+            const unsigned st = rs;
+            if (++rs == NST) {
+                rs = 0;
+                rp ^= 1;
             }
-            auto entry = [&]() {  // the next ring entry is there
-                wait(&ctl.full[rs], rp);
-                const unsigned st = rs;
-                if (++rs == NST) {
-                    rs = 0;
-                    rp ^= 1;
-                }
-                return st;
-            };
-            auto value_product = [&](unsigned st, bool acc) {
-                const unsigned b = nv & 1;
-                wait(&ctl.p_full[w][b], nv++ >> 1);
-                tc_fence_after();
-                const uint64_t v = dv + st * STAGE;
-                if (one) {
+            return st;
+        };
+        auto value_product = [&](unsigned st, bool acc) {
+            const unsigned b = nv & 1;
+            wait(&ctl.p_full[w][b], nv++ >> 1);
+            tc_fence_after();
+            const uint64_t v = dv + st * STAGE;
+            if (one) {
 #pragma unroll
-                    for (int kk = 0; kk < TP / 16; ++kk)
-                        tc_mma_ts(tO, tS + b * 64 + kk * 8, v + kk * (16 * 128 >> 4), ID_O, acc || kk > 0);
-                    tc_commit(&ctl.o_full[w][b]);
-                }
-            };
-            // (the buffer's weights have been read by then: the value product with
-            // them was issued before)
-            auto score_product = [&](unsigned st) {
-                const unsigned b = ns++ & 1;
-                const uint64_t k = dk + st * STAGE;
-                if (one) {
+                for (int kk = 0; kk < TP / 16; ++kk)
+                    tc_mma_ts(tO, tS + b * 64 + kk * 8, v + kk * (16 * 128 >> 4), ID_O, acc || kk > 0);
+                tc_commit(&ctl.o_full[w][b]);
+            }
+        };
+        uint64_t dq = 0;
+        // (the buffer's weights have been read by then: the value product with them
+        // was issued before)
+        auto score_product = [&](unsigned st) {
+            const unsigned b = ns++ & 1;
+            const uint64_t k = dk + st * STAGE;
+            if (one) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        tc_mma_ss(tS + b * 64, dq + (kk / 4) * (C::QHALF >> 4) + (kk % 4) * 2,
-                                  k + (kk / 4) * (C::HALF >> 4) + (kk % 4) * 2, ID_S, kk > 0);
-                    tc_commit(&ctl.s_full[w][b]);
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc_mma_ss(tS + b * 64, dq + (kk / 4) * (C::QHALF >> 4) + (kk % 4) * 2,
+                              k + (kk / 4) * (C::HALF >> 4) + (kk % 4) * 2, ID_S, kk > 0);
+                tc_commit(&ctl.s_full[w][b]);
+            }
+        };
+        // The piece whose keys come and the one whose values come, two tiles behind:
+        // its tiles, those of them that are this stream's, the first with an edge and
+        // whether it is a pair.  (Shuffled, so that they are known to be the same in
+        // every lane: descriptors are then formed in uniform registers.)
+        int4 kp = make_int4(0, 0, 0, 0), vp = kp;
+        int tk = 0, tv = 0, behind = 0;
+        unsigned vpieces = 0, vedges = 0;  // pieces and edges that the values have come to
+        bool more = true;
+        // whether a tile is this stream's
+        auto uses = [&](const int4 &p, int t) { return p.w ? t < p.y : (t & 1) == w; };
+#pragma unroll 1
+        for (unsigned e = 0;; ++e) {
+            if (more && tk == kp.x) {
+                edges += kp.x - kp.z;
+                more = walk.next(a, run, x);
+                if (more) {
+                    const Plan<C> pl(a, x);
+                    kp = make_int4(__shfl_sync(0xffffffffu, pl.n, 0),
+                                   __shfl_sync(0xffffffffu, pl.of_stream(w), 0),
+                                   __shfl_sync(0xffffffffu, pl.edge, 0),
+                                   __shfl_sync(0xffffffffu, (int)pl.pair, 0));
+                    if (lane == 0)
+                        ctl.plan[w][units & 3] = kp;
+                    __syncwarp();
+                    tk = 0;
+                    dq = tc_desc(sbase + (kp.w ? w * C::QTILE : 0), 16);
                 }
-                --left;
-            };
+            }
+            const bool k_on = more, v_on = e >= 2 && behind > 0;
+            if (!k_on && behind == 0)
+                break;
+            if (v_on && tv == vp.x) {  // (its place is written again four pieces on)
+                vedges += vp.x - vp.z;
+                const int4 p = ctl.plan[w][vpieces++ & 3];
+                vp = make_int4(__shfl_sync(0xffffffffu, p.x, 0), __shfl_sync(0xffffffffu, p.y, 0),
+                               __shfl_sync(0xffffffffu, p.z, 0), __shfl_sync(0xffffffffu, p.w, 0));
+                tv = 0;
+            }
             // Most entries of a pair have both products and no edge: nothing else is
             // done there, as every instruction keeps the tensor cores waiting.
-            const int plain = pair ? min(mine - 1, edge) : 0;
-            int e = 0;
+            if (k_on && vpieces == units && tk == tv + 2 && tv >= 1 && kp.w) {
+                const int plain = min(kp.y - 1, kp.z), from = tk;
 #pragma unroll 1
-            while (e < n + 2) {
-                if (e == 3) {
-#pragma unroll 1
-                    for (; e < plain; ++e) {
-                        const unsigned st = entry();
-                        value_product(st, true);
-                        score_product(st);
-                        if (one)
-                            tc_commit(&ctl.empty[st]);
-                        __syncwarp();
-                    }
-                }
-                if (e == n)
-                    more = walk.next(a, run, next);
-                const int t = e - 2;
-                const unsigned st = entry();
-                tc_fence_after();
-                const bool scores = e < n && uses(e), values = t >= 0 && uses(t);
-                if (one && e < n && e >= edge && (pair ? w == 1 : scores))
-                    bar_arrive(smem_addr(&ctl.v_req[(edges + e - edge) & 7]));
-                if (values) {
-                    if (t >= edge) {
-                        const unsigned k = edges + t - edge;
-                        wait(&ctl.v_ok[k & 7], k >> 3);
-                    }
-                    value_product(st, t > (pair ? 0 : 1));
-                }
-                if (scores)
+                for (; tk < plain; ++tk) {
+                    const unsigned st = entry();
+                    value_product(st, true);
                     score_product(st);
-                if (one) {
-                    if (scores && left == 0) {
-                        tc_commit(&ctl.q_free[w]);
-                        if (!pair)
-                            tc_commit(&ctl.q_free[w ^ 1]);
-                    }
-                    if (scores || values)
+                    if (one)
                         tc_commit(&ctl.empty[st]);
-                    else
-                        bar_arrive(smem_addr(&ctl.empty[st]));
+                    __syncwarp();
                 }
-                __syncwarp();
-                ++e;
+                tv += tk - from;
             }
-            edges += n - edge;
-            ++units;
-            pairs += pair;
+            const unsigned st = entry();
+            tc_fence_after();
+            const bool values = v_on && uses(vp, tv), scores = k_on && uses(kp, tk);
+            if (one && k_on && tk >= kp.z && (kp.w ? w == 1 : scores))
+                bar_arrive(smem_addr(&ctl.v_req[(edges + tk - kp.z) & 7]));
+            if (values) {
+                if (tv >= vp.z) {
+                    const unsigned k = vedges + tv - vp.z;
+                    wait(&ctl.v_ok[k & 7], k >> 3);
+                }
+                value_product(st, tv > (vp.w ? 0 : 1));
+            }
+            if (k_on && tk == 0) {  // the piece's queries
+                wait(&ctl.q_full[0], units++);
+                if (kp.w && w)
+                    wait(&ctl.q_full[1], pairs);
+                pairs += kp.w;
+                tc_fence_after();
+                if (one && kp.y == 0)  // (no tile of them is this stream's)
+                    bar_arrive(smem_addr(kp.w ? &ctl.q_free[w] : &ctl.q_both));
+            }
+            if (scores)
+                score_product(st);
+            if (one) {
+                if (scores && (kp.w ? tk == kp.y - 1 : tk + 2 >= kp.x))  // its last
+                    tc_commit(kp.w ? &ctl.q_free[w] : &ctl.q_both);
+                if (scores || values)
+                    tc_commit(&ctl.empty[st]);
+                else
+                    bar_arrive(smem_addr(&ctl.empty[st]));
+            }
+            __syncwarp();
+            behind += (int)k_on - v_on;
+            tk += k_on;
+            tv += v_on;
         }
         // every product is done before tensor memory goes
         if (one)
@@ -747,68 +793,86 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 wait(&ctl.o_full[w][(tiles - 1) & 1], (tiles - 1) >> 1);
                 tc_fence_after();
             }
-            // Results go to shared memory, 16 columns of a thread's row at a time, and from
-            // there to the output's rows in whole lines: a thread writing its own row
-            // took 7000 cycles a pair.
-            const unsigned mine = sbase + C::OFF_OUT + warp * 4096;
-            auto put = [&](int c, const float *y, float f) {  // columns c .. c + 15 of 64
-#pragma unroll
-                for (int i = 0; i < 16; i += 8)
-                    sts16(mine + lane * 128 + ((((c + i) >> 3) ^ (lane & 7)) << 4),
-                          h2(y[i] * f, y[i + 1] * f), h2(y[i + 2] * f, y[i + 3] * f),
-                          h2(y[i + 4] * f, y[i + 5] * f), h2(y[i + 6] * f, y[i + 7] * f));
-            };
-            const unsigned rows_on = __ballot_sync(0xffffffffu, on);
-            auto flush = [&](int c0, auto cols) {  // columns c0 .. of the warp's rows
-                constexpr int LPR = decltype(cols)::value / 8, RPI = 32 / LPR;
-                const int ch = lane % LPR;
-                __syncwarp();
-#pragma unroll 2
-                for (int r0 = 0; r0 < 32; r0 += RPI) {
-                    const int r = r0 + lane / LPR;
-                    const long long to = __shfl_sync(0xffffffffu, off, r);
-                    const uint4 u = lds16(mine + r * 128 + ((ch ^ (r & 7)) << 4));
-                    if ((rows_on >> r) & 1)
-                        *reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + to + c0 + 8 * ch) = u;
-                }
-                __syncwarp();
-            };
+            // Results go to shared memory, laid out as a copy to the output takes them: a
+            // thread writing its own row took 7000 cycles a pair.
+            const unsigned mine = sbase + C::OFF_OUT + w * C::QTILE;
+            if (row == 0)  // the copy before has read it
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             // four values of row r's piece, columns 4 c ..
             auto rec_at = [&](float *base, int r, int c) {
                 return reinterpret_cast<float4 *>(base) + c * (2 * RM) + r;
             };
             const int r0 = pl.pair ? w * RM : 0;  // the record's rows of this stream
-            if (pl.pair) {
+            if (pl.pair && whole) {
+                group_sync<128>(2 + w);
+                const float f = l == 0.f ? 0.f : __frcp_rn(l);
                 if (busy) {
-                    const float f = l == 0.f ? 0.f : __frcp_rn(l);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 64) {
+                        float y[64];
+                        tm_ld(tO + c, y);
+                        tm_ld(tO + c + 32, y + 32);
+                        tm_wait_ld(y);
+                        tm_wait_ld(y + 32);
+#pragma unroll
+                        for (int i = 0; i < 64; i += 8) {
+#pragma unroll
+                            for (int k = 0; k < 8; k += 2)
+                                mul2(y[i + k], y[i + k + 1], f, f);
+                            sts16(mine + (c >> 6) * C::QHALF + row * 128 + (((i >> 3) ^ (row & 7)) << 4),
+                                  h2(y[i], y[i + 1]), h2(y[i + 2], y[i + 3]), h2(y[i + 4], y[i + 5]),
+                                  h2(y[i + 6], y[i + 7]));
+                        }
+                    }
+                    tc_fence_before();
+                }
+                if (ntok == 1 << a.tlog) {  // all of the tile's tokens: by a copy
+                    fence_async_smem();
+                    group_sync<128>(2 + w);
+                    if (row == 0) {
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_store(&maps.out, 64 * c, x.h0, x.tok + tok0, mine + c * C::QHALF);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                } else {  // a warp its rows, in whole lines
+                    __syncwarp();
+                    const unsigned rows_on = __ballot_sync(0xffffffffu, on);
+#pragma unroll 1
+                    for (int i = lane; i < 32 * (D / 8); i += 32) {
+                        const int r = i / (D / 8), ch = i % (D / 8), at = row - lane + r;
+                        const long long to = __shfl_sync(0xffffffffu, off, r);
+                        const uint4 u = lds16(mine + (ch >> 3) * C::QHALF + at * 128 +
+                                              (((ch ^ at) & 7) << 4));
+                        if ((rows_on >> r) & 1)
+                            *reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + to + 8 * ch) = u;
+                    }
+                }
+            } else if (pl.pair) {
+                if (busy && n > 0) {
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
                         float y[16];
-                        if (n > 0)
-                            tm_ld16(tO + c, y);
-                        if (whole) {
-                            put(c & 63, y, f);
-                            if ((c & 63) == 48)
-                                flush(c - 48, std::integral_constant<int, 64>{});
-                        } else if (on && n > 0) {
+                        tm_ld16(tO + c, y);
+                        if (on) {
 #pragma unroll
                             for (int i = 0; i < 16; i += 4)
                                 __stcg(rec_at(rec, r0 + row, (c + i) / 4),
                                        make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]));
                         }
+                        __syncwarp();
                     }
-                    tc_fence_before();
                 }
+                tc_fence_before();
             } else {
                 // Stream w finishes columns w D / 2 .. of all rows; the other
-                // stream's share of them comes through the queries' place, whose
-                // products are done when both streams' are.
+                // stream's share of them comes through the results' place.
                 constexpr int HC = D / 2;
                 group_sync<256>(1);  // (both have left the unit before, too)
                 ctl.m[w][row] = m;
                 ctl.l[w][row] = l;
-                float4 *const give = reinterpret_cast<float4 *>(smem + (w ^ 1) * C::QTILE) + row;
-                const float4 *const get = reinterpret_cast<float4 *>(smem + w * C::QTILE) + row;
+                float4 *const give = reinterpret_cast<float4 *>(smem + C::OFF_OUT + (w ^ 1) * C::QTILE) + row;
+                const float4 *const get = reinterpret_cast<float4 *>(smem + C::OFF_OUT + w * C::QTILE) + row;
                 if (busy && n > 0) {
 #pragma unroll 1
                     for (int c = 0; c < HC; c += 16) {
@@ -843,23 +907,25 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             y[i + 2] = n > 0 ? fmaf(y[i + 2], fw, g.z * fo) : g.z * fo;
                             y[i + 3] = n > 0 ? fmaf(y[i + 3], fw, g.w * fo) : g.w * fo;
                         }
-                        if (whole) {
-                            put(c, y, f);
+                        if (on && whole) {
+#pragma unroll
+                            for (int i = 0; i < 16; i += 8)
+                                *reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + off + w * HC +
+                                                           c + i) =
+                                    make_uint4(h2(y[i] * f, y[i + 1] * f),
+                                               h2(y[i + 2] * f, y[i + 3] * f),
+                                               h2(y[i + 4] * f, y[i + 5] * f),
+                                               h2(y[i + 6] * f, y[i + 7] * f));
                         } else if (on) {
 #pragma unroll
                             for (int i = 0; i < 16; i += 4)
                                 __stcg(rec_at(rec, row, (w * HC + c + i) / 4),
                                        make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]));
                         }
+                        __syncwarp();
                     }
-                    if (whole)
-                        flush(w * HC, std::integral_constant<int, HC>{});
                     tc_fence_before();
                 }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    bar_arrive(smem_addr(&ctl.x_free[w]));
             }
             if (whole)
                 continue;
@@ -915,6 +981,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 *reinterpret_cast<uint2 *>(to) = make_uint2(h2(o.x * f, o.y * f), h2(o.z * f, o.w * f));
             }
         }
+        if (row == 0)
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
@@ -984,6 +1052,10 @@ cudaError_t launch_tc(SeqAttnArgs a, int nsm, cudaStream_t st)
     if ((e = enc(&maps.q, a.q.p, {D, (unsigned)a.H, (unsigned)a.T},
                  {a.H > 1 ? a.q.sh : D, a.T > 1 ? a.q.st : D},
                  {64, (unsigned)a.group, (unsigned)q_tokens})))
+        return e;
+    // results, a unit's 128 rows
+    if ((e = enc(&maps.out, a.out, {D, (unsigned)a.H, (unsigned)a.T}, {D, (long long)D * a.H},
+                 {64, (unsigned)a.group, 1u << a.tlog})))
         return e;
     for (int i = 0; i < 2; ++i) {
         CUtensorMap *m = i ? &maps.v : &maps.k;
