@@ -947,38 +947,53 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             group_sync<128>(2 + w);
             if (!ctl.last[w])
                 continue;
-            // ---- merge: rows x groups of four columns over the stream's threads
-            const int rows = min(ntok * a.group, RM);
-            const int cg = pl.pair ? D / 4 : D / 8, cg0 = pl.pair ? 0 : w * (D / 8);
-#pragma unroll 1
-            for (int k = row; k < rows * cg; k += 128) {
-                const int r = k % rows, c = cg0 + k / rows;
+            // ---- merge: the rows (a power of two of them) x groups of columns over the
+            // stream's threads, eight float4 of every piece on their way at once
+            const int rows = min(ntok * a.group, RM), rlog = rows > 1 ? 32 - __clz(rows - 1) : 0;
+            const int r = row & ((1 << rlog) - 1), cg = pl.pair ? D / 4 : D / 8;
+            const int per = max(1, cg >> (7 - rlog)), c0 = (row >> rlog) * per;
+            if (r < rows && c0 < cg) {
+                auto rec_of = [&](int p) { return a.rec + (size_t)Sched::slot(p, x.c0) * C::REC; };
+                const int at_m = 2 * RM * D + w * 2 * RM + r;
                 float M = -INFINITY, L = 0.f;
-                for (int p = x.c0; p <= x.c1; ++p)
-                    M = fmaxf(M, ld_cg(a.rec + (size_t)Sched::slot(p, x.c0) * C::REC + 2 * RM * D +
-                                       w * 2 * RM + r));
-                const float ms = M == -INFINITY ? 0.f : M;
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-                for (int p = x.c0; p <= x.c1; ++p) {
-                    float *q = a.rec + (size_t)Sched::slot(p, x.c0) * C::REC;
-                    const float mp = ld_cg(q + 2 * RM * D + w * 2 * RM + r);
-                    const float lp = ld_cg(q + 2 * RM * D + w * 2 * RM + RM + r);
-                    const float4 y = __ldcg(rec_at(q, r0 + r, c));
-                    if (mp == -INFINITY && lp == 0.f)
-                        continue;
-                    const float f = pow2(mp - ms);
-                    L = fmaf(lp, f, L);
-                    o.x = fmaf(y.x, f, o.x);
-                    o.y = fmaf(y.y, f, o.y);
-                    o.z = fmaf(y.z, f, o.z);
-                    o.w = fmaf(y.w, f, o.w);
-                }
+                for (int p = x.c0; p <= x.c1; ++p)
+                    M = fmaxf(M, ld_cg(rec_of(p) + at_m));
+                const float ms = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
+                for (int p = x.c0; p <= x.c1; ++p)
+                    L = fmaf(ld_cg(rec_of(p) + at_m + RM), pow2(ld_cg(rec_of(p) + at_m) - ms), L);
                 const float f = L == 0.f ? 0.f : __frcp_rn(L);
-                __half *to = static_cast<__half *>(a.out) +
-                             ((long long)(x.tok + tok0 + r / a.group) * a.H + x.h0 + r % a.group) * D +
-                             4 * c;
-                *reinterpret_cast<uint2 *>(to) = make_uint2(h2(o.x * f, o.y * f), h2(o.z * f, o.w * f));
+                __half *const to = static_cast<__half *>(a.out) +
+                                   ((long long)(x.tok + tok0 + r / a.group) * a.H + x.h0 + r % a.group) * D;
+                const int first = (pl.pair ? 0 : w * (D / 8)) + c0;
+#pragma unroll 1
+                for (int i0 = 0; i0 < per; i0 += 8) {
+                    float4 o[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                    for (int p = x.c0; p <= x.c1; ++p) {
+                        const float mp = ld_cg(rec_of(p) + at_m), g = pow2(mp - ms);
+                        if (mp == -INFINITY)  // (a stream without a tile of the piece left none)
+                            continue;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (i < per) {
+                                const float4 y = __ldcg(rec_at(rec_of(p), r0 + r, first + i0 + i));
+                                o[i].x = fmaf(y.x, g, o[i].x);
+                                o[i].y = fmaf(y.y, g, o[i].y);
+                                o[i].z = fmaf(y.z, g, o[i].z);
+                                o[i].w = fmaf(y.w, g, o[i].w);
+                            }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < per)
+                            *reinterpret_cast<uint2 *>(to + 4 * (first + i0 + i)) =
+                                make_uint2(h2(o[i].x * f, o[i].y * f), h2(o[i].z * f, o[i].w * f));
+                }
             }
         }
         if (row == 0)
