@@ -3,7 +3,7 @@
 //
 // A warp takes one token and a run of its rows (queries, keys, values): it forms
 // the token's sines and cosines from 64-bit fixed-point angles, and then a lane
-// holds the same 8 dimensions of every row that it meets, with their angles in
+// holds the same four pairs of every row that it meets, with their angles in
 // registers.  A row is read once and written once, so bytes bound it; several
 // rows a lane are on their way at once, and no warp waits for another (a CTA a
 // token, with its barrier, took 411 us for 16384 tokens of 64 + 8 + 8 binary32
@@ -18,30 +18,38 @@ namespace {
 
 constexpr int kRopeThreads = 128;
 
+// Four values, as they lie.
 template <bool F16>
-DV_DEV void ld8(const char *p, float (&x)[8])
-{
-    if constexpr (F16) {
-        Elem<__half>::unpack(__ldcs(reinterpret_cast<const uint4 *>(p)), x);
-    } else {
-        const float4 *q = reinterpret_cast<const float4 *>(p);
-        const float4 a = __ldcs(q), b = __ldcs(q + 1);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+struct Raw4 {
+    DV_DEV static void load(const char *p, uint4 &u)
+    {
+        if constexpr (F16) {
+            const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+            u.x = v.x, u.y = v.y;
+        } else {
+            u = __ldcs(reinterpret_cast<const uint4 *>(p));
+        }
     }
-}
-DV_DEV void st8(char *p, bool f16, const float (&x)[8])
+    DV_DEV static void get(const uint4 &u, float *x)
+    {
+        if constexpr (F16) {
+            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
+            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
+            x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+        } else {
+            x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y);
+            x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
+        }
+    }
+};
+DV_DEV void st4(char *p, bool f16, const float *x)
 {
     if (f16) {
-        __half2 h[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            h[e] = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
-        *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<uint4 *>(h);
+        const __half2 a = __floats2half2_rn(x[0], x[1]), b = __floats2half2_rn(x[2], x[3]);
+        *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const unsigned *>(&a),
+                                                   *reinterpret_cast<const unsigned *>(&b));
     } else {
-        float4 *q = reinterpret_cast<float4 *>(p);
-        q[0] = make_float4(x[0], x[1], x[2], x[3]);
-        q[1] = make_float4(x[4], x[5], x[6], x[7]);
+        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
     }
 }
 
@@ -64,10 +72,10 @@ DV_DEV void sincos_turns(unsigned long long turns, float *s, float *c)
 // work is cut into runs of `per` rows: query heads (the first q_runs), then KV
 // heads (their keys, then their values).
 template <bool SRC16, int D>
-__global__ void __launch_bounds__(kRopeThreads, 6)
+__global__ void __launch_bounds__(kRopeThreads, 5)
     k_qk_rope(const SeqRopeArgs a, int runs, int q_runs, int per)
 {
-    constexpr int LPR = D / 8, RPW = 32 / LPR, ROWS = SRC16 ? 6 : 4, NW = kRopeThreads / 32;
+    constexpr int LPR = D / 8, RPW = 32 / LPR, ROWS = 4, NW = kRopeThreads / 32;
     constexpr int ES = SRC16 ? 2 : 4;
     __shared__ float s_cos[NW][D / 2], s_sin[NW][D / 2];
     __shared__ float s_row[NW][256];
@@ -81,11 +89,19 @@ __global__ void __launch_bounds__(kRopeThreads, 6)
         return;
     const bool is_q = run < q_runs;
     const int h0 = (is_q ? run : run - q_runs) * per, h1 = min(is_q ? a.H : a.Hkv, h0 + per);
-    const int part = lane % LPR, c0 = part * 8, mine = lane / LPR, half = a.rot / 2;
+    const int part = lane % LPR, mine = lane / LPR, half = a.rot / 2;
+    // A lane's dimensions, four from ca and four from cb: both members of its pairs
+    // (as halves: ca and the same place of the second half), so that none comes from
+    // another lane, unless halves end inside four.
+    const bool odd = !a.interleaved && half % 4 != 0, split = !a.interleaved && !odd;
+    int ca = 8 * part, cb = ca + 4;
+    if (split && ca < a.rot) {
+        ca = 4 * part;
+        cb = half + ca;
+    }
 
-    // sines and cosines, by the lanes; then this lane's: element e turns with sine
-    // sn[e] (its sign for the pair's first or second), cosine cs[e]
-    float sn[8], cs[8];
+    // sines and cosines, by the lanes; then this lane's four pairs'
+    float sn[4], cs[4];
     if (a.rot) {
         for (int i = lane; i < half; i += 32) {
             float s, c;
@@ -95,20 +111,13 @@ __global__ void __launch_bounds__(kRopeThreads, 6)
         }
         __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int c = c0 + e;
-            const bool turns = c < a.rot;
-            const int i = !turns ? 0 : a.interleaved ? c >> 1 : c < half ? c : c - half;
-            const bool first = a.interleaved ? !(c & 1) : c < half;
-            sn[e] = turns ? (first ? -s_sin[warp][i] : s_sin[warp][i]) : 0.f;
+        for (int e = 0; e < 4; ++e) {
+            const int i = split ? ca + e : 4 * part + e;  // the pair, if there is one
+            const bool turns = split ? ca < half : i < half;
+            sn[e] = turns ? s_sin[warp][i] : 0.f;
             cs[e] = turns ? s_cos[warp][i] : 1.f;
         }
     }
-    // where the other of a pair lies: the same element of another lane, or, for
-    // halves that end inside a lane's elements, through shared memory
-    const bool by_lane = half % 8 == 0;
-    const int other = a.interleaved || c0 >= a.rot ? lane
-                      : c0 < half ? lane + half / 8 : lane - half / 8;
     float *const row = s_row[warp] + mine * D;
 
     // Rows h0 .. h1 - 1 of src, to dst (type f16) and, where pool is set, a token's
@@ -117,35 +126,36 @@ __global__ void __launch_bounds__(kRopeThreads, 6)
                     bool turn) {
         const long long sstep = src.sh * RPW * ES;
         const char *from = static_cast<const char *>(src.p) +
-                           (t * src.st + (h0 + mine) * src.sh + c0) * ES;
+                           (t * src.st + (h0 + mine) * src.sh + ca) * ES;
         const int de = dst.f16 ? 2 : 4, pe = a.f16 ? 2 : 4;
         const long long dstep = dst.sh * RPW * de, pstep = (long long)a.page * D * RPW * pe;
-        char *to = static_cast<char *>(dst.p) + (t * dst.st + (h0 + mine) * dst.sh + c0) * de;
+        char *to = static_cast<char *>(dst.p) + (t * dst.st + (h0 + mine) * dst.sh + ca) * de;
+        const int fb = (cb - ca) * ES, db = (cb - ca) * de, pb = (cb - ca) * pe;
         const bool put = dst.p != nullptr, store = pool != nullptr;
-        char *in = pool + (store ? ((long long)(h0 + mine) * a.page * D + c0) * pe : 0);
+        char *in = pool + (store ? ((long long)(h0 + mine) * a.page * D + ca) * pe : 0);
         float g[8];
         if (gain) {
-            const float4 g0 = __ldg(reinterpret_cast<const float4 *>(gain + c0));
-            const float4 g1 = __ldg(reinterpret_cast<const float4 *>(gain + c0) + 1);
+            const float4 g0 = __ldg(reinterpret_cast<const float4 *>(gain + ca));
+            const float4 g1 = __ldg(reinterpret_cast<const float4 *>(gain + cb));
             g[0] = g0.x, g[1] = g0.y, g[2] = g0.z, g[3] = g0.w;
             g[4] = g1.x, g[5] = g1.y, g[6] = g1.z, g[7] = g1.w;
         }
 #pragma unroll 1
         for (int h = h0 + mine; h - mine < h1; h += ROWS * RPW) {
-            float x[ROWS][8];
+            uint4 x[ROWS][2];
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
-                if (h + i * RPW < h1)
-                    ld8<SRC16>(from, x[i]);
-                else
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        x[i][e] = 0.f;
+                if (h + i * RPW < h1) {
+                    Raw4<SRC16>::load(from, x[i][0]);
+                    Raw4<SRC16>::load(from + fb, x[i][1]);
+                }
                 from += sstep;
             }
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
-                float(&y)[8] = x[i];
+                float y[8];  // (rows behind the last: whatever is there, stored nowhere)
+                Raw4<SRC16>::get(x[i][0], y);
+                Raw4<SRC16>::get(x[i][1], y + 4);
                 if (gain) {
                     float mean = 0.f;
                     if (a.layer) {
@@ -171,40 +181,45 @@ __global__ void __launch_bounds__(kRopeThreads, 6)
                     for (int e = 0; e < 8; ++e)
                         y[e] *= f * g[e];
                 }
-                if (turn) {
-                    float z[8];
+                if (turn && !odd) {
+                    auto rotate = [&](float &p, float &q, int e) {
+                        const float r = fmaf(p, cs[e], -q * sn[e]);
+                        q = fmaf(q, cs[e], p * sn[e]);
+                        p = r;
+                    };
                     if (a.interleaved) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            z[e] = y[e ^ 1];
-                    } else if (by_lane) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            z[e] = __shfl_sync(0xffffffffu, y[e], other);
+                        for (int e = 0; e < 4; ++e)
+                            rotate(y[2 * e], y[2 * e + 1], e);
                     } else {
-                        __syncwarp();
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            row[c0 + e] = y[e];
-                        __syncwarp();
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int c = c0 + e;
-                            z[e] = c >= a.rot ? 0.f : row[c < half ? c + half : c - half];
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            rotate(y[e], y[4 + e], e);
                     }
-                    if (c0 < a.rot) {  // (others keep what they have, whatever z is)
+                } else if (turn) {
+                    __syncwarp();
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (c0 + e < a.rot)
-                                y[e] = fmaf(y[e], cs[e], z[e] * sn[e]);
+                    for (int e = 0; e < 8; ++e)
+                        row[ca + e] = y[e];
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int c = ca + e, k = c < half ? c : c - half;
+                        if (c < a.rot)
+                            y[e] = fmaf(y[e], s_cos[warp][k],
+                                        c < half ? -row[c + half] * s_sin[warp][k]
+                                                 : row[k] * s_sin[warp][k]);
                     }
                 }
                 if (h + i * RPW < h1) {
-                    if (put)
-                        st8(to, dst.f16, y);
-                    if (store)
-                        st8(in, a.f16, y);
+                    if (put) {
+                        st4(to, dst.f16, y);
+                        st4(to + db, dst.f16, y + 4);
+                    }
+                    if (store) {
+                        st4(in, a.f16, y);
+                        st4(in + pb, a.f16, y + 4);
+                    }
                 }
                 to += dstep;
                 in += pstep;
