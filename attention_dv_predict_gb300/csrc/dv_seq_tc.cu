@@ -46,15 +46,21 @@ struct SeqMaps {
 
 using TcSched = SeqSched<64, true, 6, 16>;
 
-template <int D_>
+// FEW: no unit has more than 32 rows (decode): none is a pair, and the room that
+// queries and results do not need is two more stages of the ring (64 rows of 8 x 8
+// heads over 4096 positions in pages of 16: 250 us with three, @FEW@ with five).
+template <int D_, bool FEW_>
 struct SeqTcCfg {
+    static constexpr bool FEW = FEW_;
     static constexpr int D = D_, TP = 64, RM = 128;
     static constexpr int TILE = TP * D * 2, HALF = TP * 128;    // keys or values; 64 dimensions
     static constexpr int QTILE = RM * D * 2, QHALF = RM * 128;  // queries of 128 rows
-    static constexpr int NST = D == 128 ? 3 : 8;               // ring stages
+    static constexpr int NST = D == 128 ? (FEW ? 5 : 3) : 8;    // ring stages
     static constexpr int THREADS = 384;
-    static constexpr int OFF_KV = 2 * QTILE, OFF_OUT = OFF_KV + NST * 2 * TILE,
-                         OFF_CTL = OFF_OUT + 2 * QTILE;  // (results of both streams)
+    static constexpr int XROWS = FEW ? 32 : RM;                 // rows that streams exchange
+    static constexpr int OUT = XROWS * D * 2;                   // a stream's results
+    static constexpr int OFF_KV = (FEW ? 1 : 2) * QTILE, OFF_OUT = OFF_KV + NST * 2 * TILE,
+                         OFF_CTL = OFF_OUT + 2 * OUT;
     static constexpr int T_S = 0, T_O = 256, T_COLS = 512;  // tensor-memory columns
     static constexpr int REC = 2 * RM * D + 4 * RM;      // floats of a piece's record
     using Sched = TcSched;
@@ -285,7 +291,7 @@ struct Plan {
     bool pair;
     DV_DEV Plan(const SeqAttnArgs &a, const typename C::Sched::Piece &x)
     {
-        pair = x.pair;
+        pair = !C::FEW && x.pair;
         n = x.k1 - x.k0;
         n0 = pair ? min(max((x.pos + (1 << a.tlog) + C::TP - 1) / C::TP - x.k0, 0), n) : n;
         edge = min(max((x.pos + 1) / C::TP - x.k0, 0), n);
@@ -351,13 +357,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (warp == 8) {
         // ---- keys and values
         unsigned i = 0;  // ring entries so far
-        const int rows = a.pk ? min(a.page, TP) : TP, np = TP / rows;  // of a copy; copies of a tile
+        // A lane a copy: `rows` rows of 64 dimensions (c) of the keys or the values.
+        const int rows = a.pk ? min(a.page, TP) : TP, np = TP / rows, piece = lane % np;
+        const int c = lane / np % (D / 64), kv = lane / np / (D / 64);
+        const CUtensorMap *const map = kv ? &maps.v : &maps.k;
+        const unsigned lane_dst = kv * C::TILE + c * C::HALF + piece * rows * 128;
         const int none = a.pk ? a.n_pages * a.Hkv : 0;
         // where this lane's page of tile t lies: the page and head in the pool, or
         // one behind the pool, which reads as zeros
         auto page_of = [&](int t) {
-            const int p = t * TP + lane * rows;
-            if (lane >= np || p >= x.pos + x.ntok)
+            const int p = t * TP + piece * rows;
+            if (p >= x.pos + x.ntok)
                 return none;
             const int pg = __ldg(a.tables + (long long)x.b * a.width + p / a.page);
             if ((unsigned)pg >= (unsigned)a.n_pages) {
@@ -365,14 +375,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 return none;
             }
             return pg * a.Hkv + x.hkv;
-        };
-        // (row, z): where the lane's copies of a tile begin
-        auto load = [&](const CUtensorMap *map, unsigned dst, unsigned full, int row, int z) {
-            if (lane < np) {
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load(dst + c * C::HALF + lane * rows * 128, map, 64 * c, row, z, full);
-            }
         };
         typename Sched::Walk walk;
         walk.start(a, run);
@@ -399,17 +401,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     zn = page_of(t + 1);
             }
             const unsigned st = i % NST, full = smem_addr(&ctl.full[st]);
-            const unsigned dst = sbase + C::OFF_KV + st * 2 * C::TILE;
             if (i >= NST)
                 wait(&ctl.empty[st], i / NST - 1);
             if (!wait.dead) {
                 if (lane == 0)
                     bar_expect(full, ((int)more + v) * C::TILE);
                 __syncwarp();
-                if (more)
-                    load(&maps.k, dst, full, row[0], z[0]);
-                if (v)
-                    load(&maps.v, dst + C::TILE, full, row[2], z[2]);
+                if (kv == 0 ? more : kv == 1 && v)
+                    tma_load(sbase + C::OFF_KV + st * 2 * C::TILE + lane_dst, map, 64 * c,
+                             kv ? row[2] : row[0], kv ? z[2] : z[0], full);
             }
             behind += (int)more - v;
             t += more;
@@ -795,7 +795,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             // Results go to shared memory, laid out as a copy to the output takes them: a
             // thread writing its own row took 7000 cycles a pair.
-            const unsigned mine = sbase + C::OFF_OUT + w * C::QTILE;
+            const unsigned mine = sbase + C::OFF_OUT + w * C::OUT;
             if (row == 0)  // the copy before has read it
                 asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             // four values of row r's piece, columns 4 c ..
@@ -871,8 +871,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 group_sync<256>(1);  // (both have left the unit before, too)
                 ctl.m[w][row] = m;
                 ctl.l[w][row] = l;
-                float4 *const give = reinterpret_cast<float4 *>(smem + C::OFF_OUT + (w ^ 1) * C::QTILE) + row;
-                const float4 *const get = reinterpret_cast<float4 *>(smem + C::OFF_OUT + w * C::QTILE) + row;
+                float4 *const give = reinterpret_cast<float4 *>(smem + C::OFF_OUT + (w ^ 1) * C::OUT) + row;
+                const float4 *const get = reinterpret_cast<float4 *>(smem + C::OFF_OUT + w * C::OUT) + row;
                 if (busy && n > 0) {
 #pragma unroll 1
                     for (int c = 0; c < HC; c += 16) {
@@ -880,7 +880,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         tm_ld16(tO + (w ^ 1) * HC + c, y);
 #pragma unroll
                         for (int i = 0; i < 16; i += 4)
-                            give[(c + i) / 4 * RM] = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+                            give[(c + i) / 4 * C::XROWS] = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
                     }
                 }
                 group_sync<256>(1);
@@ -901,7 +901,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         for (int i = 0; i < 16; i += 4) {
                             float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
                             if (other)
-                                g = get[(c + i) / 4 * RM];
+                                g = get[(c + i) / 4 * C::XROWS];
                             y[i] = n > 0 ? fmaf(y[i], fw, g.x * fo) : g.x * fo;
                             y[i + 1] = n > 0 ? fmaf(y[i + 1], fw, g.y * fo) : g.y * fo;
                             y[i + 2] = n > 0 ? fmaf(y[i + 2], fw, g.z * fo) : g.z * fo;
@@ -1045,7 +1045,7 @@ struct SeqMapEncoder {
 };
 
 template <class C>
-cudaError_t launch_tc(SeqAttnArgs a, int nsm, cudaStream_t st)
+cudaError_t launch_tc(const SeqAttnArgs &a, int nsm, cudaStream_t st)
 {
     auto kern = k_seq_tc<C>;
     constexpr size_t smem = C::OFF_CTL + sizeof(SeqCtl);
@@ -1056,7 +1056,6 @@ cudaError_t launch_tc(SeqAttnArgs a, int nsm, cudaStream_t st)
     });
     if (e != cudaSuccess)
         return e;
-    seq_group(a, C::RM);
     int q_tokens = 1;  // of a copy: no more than a request can have
     while (q_tokens < a.max_tok && q_tokens < 1 << a.tlog)
         q_tokens *= 2;
@@ -1097,12 +1096,17 @@ cudaError_t launch_tc(SeqAttnArgs a, int nsm, cudaStream_t st)
 
 cudaError_t launch_seq_tc(const SeqAttnArgs &a, int nsm, cudaStream_t st)
 {
-    return a.D == 128 ? launch_tc<SeqTcCfg<128>>(a, nsm, st) : launch_tc<SeqTcCfg<64>>(a, nsm, st);
+    SeqAttnArgs b = a;
+    seq_group(b, 128);
+    const bool few = b.max_tok <= 1 << b.tlog && (long long)b.max_tok * b.group <= 32;
+    if (a.D == 128)
+        return few ? launch_tc<SeqTcCfg<128, true>>(b, nsm, st) : launch_tc<SeqTcCfg<128, false>>(b, nsm, st);
+    return few ? launch_tc<SeqTcCfg<64, true>>(b, nsm, st) : launch_tc<SeqTcCfg<64, false>>(b, nsm, st);
 }
 
 size_t seq_tc_record_bytes(int D)
 {
-    return 2 * (size_t)kSeqTcCtas * (D == 128 ? SeqTcCfg<128>::REC : SeqTcCfg<64>::REC) * 4;
+    return 2 * (size_t)kSeqTcCtas * (D == 128 ? SeqTcCfg<128, false>::REC : SeqTcCfg<64, false>::REC) * 4;
 }
 
 }  // namespace dv
