@@ -46,14 +46,20 @@ struct SeqMaps {
 
 using TcSched = SeqSched<64, true, 6, 16>;
 
+// PAGED: keys and values of a pool.  Their tiles are laid out by groups of 8 rows,
+// a group's 64-dimension halves side by side, so that one copy brings a whole page
+// (as two halves of 64 rows each, like packed rows', 64 rows of 8 x 8 heads over
+// 4096 positions took 248 us in pages of 16, and 198 so).
 // FEW: no unit has more than 32 rows (decode): none is a pair, and the room that
-// queries and results do not need is two more stages of the ring (64 rows of 8 x 8
-// heads over 4096 positions in pages of 16: 250 us with three, @FEW@ with five).
-template <int D_, bool FEW_>
+// queries and results do not need is two more stages of the ring (pages of 64: 182
+// us with three, 172 with five).
+template <int D_, bool PAGED_, bool FEW_>
 struct SeqTcCfg {
-    static constexpr bool FEW = FEW_;
+    static constexpr bool PAGED = PAGED_, FEW = FEW_;
     static constexpr int D = D_, TP = 64, RM = 128;
     static constexpr int TILE = TP * D * 2, HALF = TP * 128;    // keys or values; 64 dimensions
+    static constexpr int GROUP = PAGED ? D * 16 : 1024;         // bytes from 8 rows to the next 8
+    static constexpr int KHALF = PAGED ? 1024 : HALF;           // and to their other half
     static constexpr int QTILE = RM * D * 2, QHALF = RM * 128;  // queries of 128 rows
     static constexpr int NST = D == 128 ? (FEW ? 5 : 3) : 8;    // ring stages
     static constexpr int THREADS = 384;
@@ -90,12 +96,12 @@ DV_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;
 DV_DEV void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 DV_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Shared-memory matrix descriptor, 128-byte swizzle: 8-row groups 1024 bytes
+// Shared-memory matrix descriptor, 128-byte swizzle: 8-row groups sbo bytes
 // apart; lbo: bytes between 64-element blocks of an MN-major operand.
-DV_DEV uint64_t tc_desc(unsigned saddr, unsigned lbo)
+DV_DEV uint64_t tc_desc(unsigned saddr, unsigned lbo, unsigned sbo)
 {
     return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+           ((uint64_t)(sbo >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 // kind::f16, f32 accumulate, M = 128, N columns; tb: B is MN-major.
 __host__ __device__ constexpr uint32_t tc_idesc(int N, bool tb)
@@ -188,6 +194,15 @@ DV_DEV void tm_st8(unsigned addr, const unsigned *r)
 }
 DV_DEV void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// From a page: its groups of 8 rows from `group` on, whole rows.
+DV_DEV void tma_load_page(unsigned dst, const CUtensorMap *map, int group, int z, unsigned bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %2, %2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(0), "r"(group), "r"(z), "r"(bar)
+        : "memory");
+}
 // A box of shared memory to (dimension, head, token) of the results.
 DV_DEV void tma_store(const CUtensorMap *map, int x, int h, int tok, unsigned src)
 {
@@ -357,12 +372,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (warp == 8) {
         // ---- keys and values
         unsigned i = 0;  // ring entries so far
-        // A lane a copy: `rows` rows of 64 dimensions (c) of the keys or the values.
-        const int rows = a.pk ? min(a.page, TP) : TP, np = TP / rows, piece = lane % np;
-        const int c = lane / np % (D / 64), kv = lane / np / (D / 64);
+        // A lane a copy, of the keys or the values: a page's rows of the tile, or of
+        // packed rows 64 dimensions (c).
+        constexpr int NC = C::PAGED ? 1 : D / 64;
+        const int rows = C::PAGED ? min(a.page, TP) : TP, np = TP / rows, piece = lane % np;
+        const int c = lane / np % NC, kv = lane / np / NC;
         const CUtensorMap *const map = kv ? &maps.v : &maps.k;
-        const unsigned lane_dst = kv * C::TILE + c * C::HALF + piece * rows * 128;
-        const int none = a.pk ? a.n_pages * a.Hkv : 0;
+        const unsigned lane_dst = kv * C::TILE + c * C::HALF + piece * (rows * D * 2);
+        const int none = C::PAGED ? a.n_pages * a.Hkv : 0;
         // where this lane's page of tile t lies: the page and head in the pool, or
         // one behind the pool, which reads as zeros
         auto page_of = [&](int t) {
@@ -386,7 +403,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (more && t >= x.k1) {
                 more = walk.next(a, run, x);
                 t = x.k0;
-                if (more && a.pk)
+                if (more && C::PAGED)
                     zn = page_of(t);
             }
             const bool v = i >= 2 && behind > 0;
@@ -395,9 +412,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             row[2] = row[1], row[1] = row[0];
             z[2] = z[1], z[1] = z[0];
             if (more) {
-                row[0] = a.pk ? t * TP & (a.page - 1) : x.tok - x.pos + t * TP;
-                z[0] = a.pk ? zn : x.hkv;
-                if (a.pk && t + 1 < x.k1)
+                row[0] = C::PAGED ? (t * TP & (a.page - 1)) >> 3 : x.tok - x.pos + t * TP;
+                z[0] = C::PAGED ? zn : x.hkv;
+                if (C::PAGED && t + 1 < x.k1)
                     zn = page_of(t + 1);
             }
             const unsigned st = i % NST, full = smem_addr(&ctl.full[st]);
@@ -407,9 +424,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (lane == 0)
                     bar_expect(full, ((int)more + v) * C::TILE);
                 __syncwarp();
-                if (kv == 0 ? more : kv == 1 && v)
-                    tma_load(sbase + C::OFF_KV + st * 2 * C::TILE + lane_dst, map, 64 * c,
-                             kv ? row[2] : row[0], kv ? z[2] : z[0], full);
+                if (kv == 0 ? more : kv == 1 && v) {
+                    const unsigned dst = sbase + C::OFF_KV + st * 2 * C::TILE + lane_dst;
+                    const int r = kv ? row[2] : row[0], zz = kv ? z[2] : z[0];
+                    if constexpr (C::PAGED)
+                        tma_load_page(dst, map, r, zz, full);
+                    else
+                        tma_load(dst, map, 64 * c, r, zz, full);
+                }
             }
             behind += (int)more - v;
             t += more;
@@ -486,7 +508,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 for (int c = 0; c < D / 64; ++c)
 #pragma unroll 4
                     for (int j = r0 * 8 + lane; j < TP * 8; j += 32) {
-                        const unsigned p = at + c * C::HALF + j * 16;
+                        const unsigned p = at + c * C::KHALF + (j >> 6) * C::GROUP + (j & 63) * 16;
                         const uint4 y = lds16(p);
                         // an exponent field of ones carries into its half's top bit
                         unsigned z = ((y.x & 0x7c007c00u) + 0x04000400u) |
@@ -520,8 +542,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         constexpr uint32_t ID_S = tc_idesc(TP, false), ID_O = tc_idesc(D, true);
         constexpr unsigned STAGE = 2 * C::TILE >> 4;
         const int w = warp - 9;
-        const uint64_t dk = tc_desc(sbase + C::OFF_KV, 16),
-                       dv = tc_desc(sbase + C::OFF_KV + C::TILE, C::HALF);
+        const uint64_t dk = tc_desc(sbase + C::OFF_KV, 16, C::GROUP),
+                       dv = tc_desc(sbase + C::OFF_KV + C::TILE, C::KHALF, C::GROUP);
         const unsigned tS = tmem + C::T_S + w * 128, tO = tmem + C::T_O + w * 128;
         const bool one = elect_one();
         unsigned units = 0, pairs = 0, edges = 0;
@@ -546,7 +568,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (one) {
 #pragma unroll
                 for (int kk = 0; kk < TP / 16; ++kk)
-                    tc_mma_ts(tO, tS + b * 64 + kk * 8, v + kk * (16 * 128 >> 4), ID_O, acc || kk > 0);
+                    tc_mma_ts(tO, tS + b * 64 + kk * 8, v + kk * (2 * C::GROUP >> 4), ID_O, acc || kk > 0);
                 tc_commit(&ctl.o_full[w][b]);
             }
         };
@@ -560,7 +582,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     tc_mma_ss(tS + b * 64, dq + (kk / 4) * (C::QHALF >> 4) + (kk % 4) * 2,
-                              k + (kk / 4) * (C::HALF >> 4) + (kk % 4) * 2, ID_S, kk > 0);
+                              k + (kk / 4) * (C::KHALF >> 4) + (kk % 4) * 2, ID_S, kk > 0);
                 tc_commit(&ctl.s_full[w][b]);
             }
         };
@@ -589,7 +611,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         ctl.plan[w][units & 3] = kp;
                     __syncwarp();
                     tk = 0;
-                    dq = tc_desc(sbase + (kp.w ? w * C::QTILE : 0), 16);
+                    dq = tc_desc(sbase + (kp.w ? w * C::QTILE : 0), 16, 1024);
                 }
             }
             const bool k_on = more, v_on = e >= 2 && behind > 0;
@@ -1025,17 +1047,24 @@ struct SeqMapEncoder {
         }();
         encode = fn;
     }
-    // Three dimensions, the strides of the outer two in elements; swizzled rows
-    // of 128 bytes.
-    cudaError_t operator()(CUtensorMap *m, const void *p, const unsigned (&dims)[3],
-                           const long long (&strides)[2], const unsigned (&box)[3]) const
+    // N dimensions, the strides of all but the first in elements; swizzled rows of
+    // 128 bytes.
+    template <int N>
+    cudaError_t operator()(CUtensorMap *m, const void *p, const unsigned (&dims)[N],
+                           const long long (&strides)[N - 1], const unsigned (&box)[N]) const
     {
         if (!encode)
             return cudaErrorNotSupported;
-        const cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
-        const cuuint64_t s[2] = {(cuuint64_t)strides[0] * 2, (cuuint64_t)strides[1] * 2};
-        const cuuint32_t b[3] = {box[0], box[1], box[2]}, one[3] = {1, 1, 1};
-        return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(p), d, s, b, one,
+        cuuint64_t d[N], s[N - 1];
+        cuuint32_t b[N], one[N];
+        for (int i = 0; i < N; ++i) {
+            d[i] = dims[i];
+            b[i] = box[i];
+            one[i] = 1;
+            if (i)
+                s[i - 1] = (cuuint64_t)strides[i - 1] * 2;
+        }
+        return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, N, const_cast<void *>(p), d, s, b, one,
                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
@@ -1063,24 +1092,28 @@ cudaError_t launch_tc(const SeqAttnArgs &a, int nsm, cudaStream_t st)
     SeqMaps maps;
     constexpr unsigned D = C::D;
     // queries (dimension, head, token), boxes of a unit's heads and tokens
-    if ((e = enc(&maps.q, a.q.p, {D, (unsigned)a.H, (unsigned)a.T},
+    if ((e = enc.template operator()<3>(
+             &maps.q, a.q.p, {D, (unsigned)a.H, (unsigned)a.T},
                  {a.H > 1 ? a.q.sh : D, a.T > 1 ? a.q.st : D},
                  {64, (unsigned)a.group, (unsigned)q_tokens})))
         return e;
     // results, a unit's 128 rows
-    if ((e = enc(&maps.out, a.out, {D, (unsigned)a.H, (unsigned)a.T}, {D, (long long)D * a.H},
+    if ((e = enc.template operator()<3>(
+             &maps.out, a.out, {D, (unsigned)a.H, (unsigned)a.T}, {D, (long long)D * a.H},
                  {64, (unsigned)a.group, 1u << a.tlog})))
         return e;
     for (int i = 0; i < 2; ++i) {
         CUtensorMap *m = i ? &maps.v : &maps.k;
         const SeqRowsArgs &r = i ? a.v : a.k;
-        if (a.pk)  // (dimension, row of a page, page and head)
-            e = enc(m, i ? a.pv : a.pk, {D, (unsigned)a.page, (unsigned)(a.n_pages * a.Hkv)},
-                    {D, (long long)D * a.page},
-                    {64, (unsigned)(a.page < C::TP ? a.page : C::TP), 1});
+        const unsigned groups = (unsigned)a.page / 8;
+        if (C::PAGED)  // (dimension, row of 8, half, group of 8 rows, page and head)
+            e = enc.template operator()<5>(
+                m, i ? a.pv : a.pk, {64, 8, D / 64, groups, (unsigned)(a.n_pages * a.Hkv)},
+                {D, 64, 8 * D, (long long)D * a.page}, {64, 8, D / 64, groups < 8 ? groups : 8, 1});
         else  // (dimension, token, head)
-            e = enc(m, r.p, {D, (unsigned)a.T, (unsigned)a.Hkv},
-                    {a.T > 1 ? r.st : D, a.Hkv > 1 ? r.sh : D}, {64, C::TP, 1});
+            e = enc.template operator()<3>(m, r.p, {D, (unsigned)a.T, (unsigned)a.Hkv},
+                                           {a.T > 1 ? r.st : D, a.Hkv > 1 ? r.sh : D},
+                                           {64, C::TP, 1});
         if (e)
             return e;
     }
@@ -1099,14 +1132,18 @@ cudaError_t launch_seq_tc(const SeqAttnArgs &a, int nsm, cudaStream_t st)
     SeqAttnArgs b = a;
     seq_group(b, 128);
     const bool few = b.max_tok <= 1 << b.tlog && (long long)b.max_tok * b.group <= 32;
-    if (a.D == 128)
-        return few ? launch_tc<SeqTcCfg<128, true>>(b, nsm, st) : launch_tc<SeqTcCfg<128, false>>(b, nsm, st);
-    return few ? launch_tc<SeqTcCfg<64, true>>(b, nsm, st) : launch_tc<SeqTcCfg<64, false>>(b, nsm, st);
+    const auto go = [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        return !a.pk ? launch_tc<SeqTcCfg<D, false, false>>(b, nsm, st)
+               : few ? launch_tc<SeqTcCfg<D, true, true>>(b, nsm, st)
+                     : launch_tc<SeqTcCfg<D, true, false>>(b, nsm, st);
+    };
+    return a.D == 128 ? go(std::integral_constant<int, 128>{}) : go(std::integral_constant<int, 64>{});
 }
 
 size_t seq_tc_record_bytes(int D)
 {
-    return 2 * (size_t)kSeqTcCtas * (D == 128 ? SeqTcCfg<128, false>::REC : SeqTcCfg<64, false>::REC) * 4;
+    return 2 * (size_t)kSeqTcCtas * (2 * 128 * D + 4 * 128) * 4;
 }
 
 }  // namespace dv
