@@ -60,6 +60,13 @@ DV_DEV SeqRow seq_row(const SeqAttnArgs &a, int b, bool report)
     return r;
 }
 
+// a / b for 0 <= a, 0 < b: in 32 bits where that does (a 64-bit division is a
+// subroutine of some 100 instructions, and a CTA starts with several).
+DV_DEV long long seq_quot(long long a, long long b)
+{
+    return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
 template <int TP_, bool PAIR_, int COST_, int MIN_RUN_>
 struct SeqSched {
     static constexpr int TP = TP_, COST = COST_, MIN_RUN = MIN_RUN_;
@@ -97,7 +104,7 @@ struct SeqSched {
         return w;
     }
 
-    // Every thread of the CTA calls it.  (At most 1024 threads.)
+    // Every thread of the CTA calls it.  (At most 1024 threads, whole warps.)
     DV_DEV static SeqRun init(const SeqAttnArgs &a, SeqSmem &sm)
     {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -128,13 +135,32 @@ struct SeqSched {
         };
         SeqRun r;
         r.W = 0;
+        auto runs = [&]() {
+            r.C = (int)min((long long)gridDim.x, max(1ll, r.W / MIN_RUN));
+            r.c = blockIdx.x;
+            r.lo = r.c < r.C ? seq_quot(r.W * r.c, r.C) : r.W;
+            r.hi = r.c < r.C ? seq_quot(r.W * (r.c + 1), r.C) : r.W;
+        };
+        if (a.B <= 32) {  // every warp for itself: no barrier between them
+            v = lane < a.B ? places(a, seq_row(a, lane, blockIdx.x == 0 && warp == 0)) * hs : 0;
+            before = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long t = __shfl_up_sync(0xffffffffu, before, o);
+                before += lane >= o ? t : 0;
+            }
+            r.W = __shfl_sync(0xffffffffu, before, 31);
+            before -= v;
+            runs();
+            const unsigned in = __ballot_sync(0xffffffffu, before <= r.lo && r.lo < before + v);
+            r.b = in ? __ffs(in) - 1 : 0;
+            r.base = __shfl_sync(0xffffffffu, before, r.b);
+            return r;
+        }
         const int step = blockDim.x;
         for (int b0 = 0; b0 < a.B; b0 += step)
             r.W += scan(b0, blockIdx.x == 0);
-        r.C = (int)min((long long)gridDim.x, max(1ll, r.W / MIN_RUN));
-        r.c = blockIdx.x;
-        r.lo = r.c < r.C ? r.W * r.c / r.C : r.W;
-        r.hi = r.c < r.C ? r.W * (r.c + 1) / r.C : r.W;
+        runs();
         long long base = 0;
         for (int b0 = 0; b0 < a.B; b0 += step) {
             const long long all = a.B <= step ? 0 : scan(b0, false);
@@ -178,7 +204,7 @@ struct SeqSched {
                 return;
             row = seq_row(a, b, false);
             const long long per = places(a, row), at = r.lo - r.base;
-            hs = (int)(at / per);
+            hs = (int)seq_quot(at, per);
             const long long rest = at - hs * per;
             // the last whole unit, or the partial one behind them, that starts by `rest`
             int lo = 0, hi = units(a) - 1;
@@ -248,7 +274,7 @@ struct SeqSched {
     // The run that place w falls to: the last c with floor(W c / C) <= w.
     DV_DEV static int run_of(const SeqRun &r, long long w)
     {
-        return (int)(((w + 1) * r.C - 1) / r.W);
+        return (int)seq_quot((w + 1) * r.C - 1, r.W);
     }
     // Record of run c's piece of a unit that starts in run c0.
     DV_DEV static int slot(int c, int c0) { return 2 * c + (c == c0); }

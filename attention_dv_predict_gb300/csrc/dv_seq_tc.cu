@@ -335,6 +335,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    if (warp == 10 && lane < 3)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v)
+                     : "memory");
     if (tid == 0) {
         auto init = [](uint64_t &b, int n) { bar_init(smem_addr(&b), n); };
         for (int i = 0; i < NST; ++i) {
