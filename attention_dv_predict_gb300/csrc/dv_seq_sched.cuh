@@ -6,7 +6,7 @@
 // where the request has that many left.  Its work is the tiles of TP cached
 // positions that its last token sees.  Token counts and lengths are known on
 // the device only, so the tiles of all units are laid end to end (request,
-// head, tokens), each unit's behind kUnitCost empty places for what a unit
+// head, tokens), each unit's behind COST empty places for what a unit
 // costs beside its tiles and two places a tile for a pair, and C CTAs take
 // equal runs of places, each the tiles that begin in its run.  A unit inside
 // one run is finished by its CTA; of a unit cut by a run's end every CTA leaves

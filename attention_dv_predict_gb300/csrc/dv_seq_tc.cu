@@ -44,7 +44,10 @@ struct SeqMaps {
     CUtensorMap q, k, v, out;
 };
 
-using TcSched = SeqSched<64, true, 6, 16>;
+// What a unit costs beside its tiles, and the shortest run, in places: swept over
+// single tokens, short and long prompts and a mix of them (a unit of 6: the mix 476
+// us, ragged prompts 374; of 12: 409 and 338; of 20: 416 and 346).
+using TcSched = SeqSched<64, true, 12, 12>;
 
 // PAGED: keys and values of a pool.  Their tiles are laid out by groups of 8 rows,
 // a group's 64-dimension halves side by side, so that one copy brings a whole page
