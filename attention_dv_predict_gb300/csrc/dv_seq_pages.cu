@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kPageThreads = 1024;
 constexpr int kPageTokens = 1024;  // tokens per CTA
+static_assert(DV_SEQ_MAX_BATCH <= kPageThreads, "a request a thread");
 
 DV_DEV int pages_of(long long n, int page) { return (int)((n + page - 1) / page); }
 

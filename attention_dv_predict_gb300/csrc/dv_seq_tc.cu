@@ -32,6 +32,11 @@
 // 2^(s - m) with m a whole number 6 below the first tile's maximum, and m moves
 // (for this row alone) when a weight would pass 2^15, near the end of binary16's
 // range, so the outputs are rarely rescaled.
+//
+// A stream's buffers: with tiles c - 2, c - 1, c, ... of a stream's own, the scores
+// of c take the place of the weights of c - 2, whose value product has been issued
+// (an entry of the ring brings values two tiles of the run behind its keys, and a
+// stream's c - 2 is at least that far behind its c).
 #include <cudaTypedefs.h>
 
 #include "dv_kv_tma.cuh"
@@ -227,6 +232,15 @@ DV_DEV float max3(float a, float b, float c)
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+// Sums of the weights as rounded, so that a row's weights add up to 1 whatever
+// their rounding: a row of one position is that position's value.
+DV_DEV void add_pair(float &a, float &b, unsigned pair)
+{
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
+        "add.rn.f32.f16 %0, x, %0;\n\tadd.rn.f32.f16 %1, y, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(pair));
 }
 template <int N>
 DV_DEV void group_sync(int bar)
@@ -771,8 +785,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             fma2(p, q, scale, -ms);
                             p = ex2(p);
                             q = ex2(q);
-                            add2(sum[i & 2], sum[(i & 2) + 1], p, q);
                             pr[i / 2] = h2(p, q);
+                            add_pair(sum[i & 2], sum[(i & 2) + 1], pr[i / 2]);
                         }
                         tm_st8(tP + c / 2, pr);
                     }

@@ -765,6 +765,8 @@ class Rope:
         gains = [t for t in (q_gain, k_gain) if t is not None]
         dev = torch.device(device) if device is not None else gains[0].device if gains else \
             torch.device("cuda", torch.cuda.current_device())
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
         if steps is None and rot_dim:
             host = (C.c_uint64 * max(1, rot_dim // 2))()
             _check("dv_rope_steps", _lib.dv_rope_steps(

@@ -758,8 +758,8 @@ int dv_qk_rope(const dv_seq_desc *desc, const dv_rope *rope, int tokens, const i
  * a NaN, makes the result non-finite (every value of it, or that dimension's).
  * Scores, sums and outputs are held in binary32.  Binary16 rows of 64 or 128
  * values run on tensor cores (tcgen05): a weight is rounded to binary16 (2^-11
- * of itself, or 2^-31 of the row's largest) before it meets its value; all other
- * arithmetic is binary32.  The order of every sum is fixed by the shapes, the
+ * of itself, or 2^-31 of the row's largest) for its value and for the sum; all
+ * other arithmetic is binary32.  The order of every sum is fixed by the shapes, the
  * lengths and the device.
  */
 int dv_prompt_attn(const dv_seq_desc *desc, int batch, int tokens, int max_tok,

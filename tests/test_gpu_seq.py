@@ -738,3 +738,150 @@ def test_two_streams_at_once(dv):
             assert dv.dv_check(c.ws) == 0
             c.out.fill_(0)
         torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ edges of the ranges
+
+
+@pytest.mark.parametrize("Hkv,G", [(1, 256), (1, 160), (1, 131), (2, 48), (1, 12)])
+def test_wide_groups(dv, Hkv, G):
+    """Query heads that fill a unit's rows alone, do not divide them, or are a prime number."""
+    for D, dtype in ((64, "f16"), (32, "f32")):
+        Seqs(dv, [5, 70], [0, 0], Hkv, G, D, dtype).check()
+        Seqs(dv, [1, 1, 3], [200, 0, 77], Hkv, G, D, dtype, 16).check(max_tok=3)
+
+
+def test_pool_beyond_32_bits(dv):
+    """Pages behind the first 2^31 elements of a pool, written by dv_qk_rope and attended."""
+    H, Hkv, D, page = 8, 8, 128, 128
+    n_pages = (1 << 31) // (Hkv * page * D) + 40
+    desc = dv.make_seq_desc(H, Hkv, D, dv.DV_F16, page, n_pages)
+    shape = (n_pages, Hkv, page, D)
+    cache = dv.PagedCache(desc, tensors={n: torch.empty(shape, dtype=torch.float16, device="cuda")
+                                         for n in ("k", "v")})
+    ws = dv.SeqWorkspace(desc)
+    T = 300
+    rng = np.random.default_rng(0)
+    qkv = rng.standard_normal((T, 3 * H, D)).astype(np.float16)
+    x = dev(qkv)
+    table = np.array([[n_pages - 1, n_pages - 30, n_pages - 7]], np.int32)
+    pos = np.arange(T, dtype=np.int32)
+    slots = table[0, pos // page] * page + pos % page
+    q = torch.zeros(T, H, D, dtype=torch.float16, device="cuda")
+    dv.dv_qk_rope(dv.Rope(D, 0), x[:, :H], x[:, H:2 * H], i32(pos), ws, q_out=q, v=x[:, 2 * H:],
+                  cache=cache, slots=i32(slots))
+    out = torch.zeros(T, H, D, dtype=torch.float16, device="cuda")
+    dv.dv_paged_attn(cache, q, i32([0, T]), i32([0]), i32(table), out, ws)
+    assert dv.dv_check(ws) == 0
+    K = qkv[:, H:2 * H].transpose(1, 0, 2)
+    V = qkv[:, 2 * H:].transpose(1, 0, 2)
+    close(out, *seq_ref.packed(qkv[:, :H], [K], [V], [0, T], [0], D ** -0.5, True))
+    one = torch.zeros(1, H, D, dtype=torch.float16, device="cuda")
+    dv.dv_paged_attn(cache, q[-1:], i32([0, 1]), i32([T - 1]), i32(table), one, ws, max_tok=1)
+    want, tol = seq_ref.packed(qkv[-1:, :H], [K], [V], [0, 1], [T - 1], D ** -0.5, True)
+    close(one, want, tol)
+
+
+def test_first_call_inside_a_capture(dv):
+    """Each operator's first call of a process may be a captured one, on a stream of its own."""
+    import subprocess
+    import sys
+
+    code = """
+import sys; sys.path.insert(0, %r); sys.path.insert(0, %r)
+import torch
+from attention_dv_predict_gb300 import dv
+from test_gpu_seq import serving, step, i32
+s = serving(dv, 2, 4, 2, 64, 16, 20, 8, 40, "f16")
+x = torch.randn(40, 8, 64, device="cuda").half()
+out = torch.zeros(40, 4, 64, dtype=torch.float16, device="cuda")
+n_tok, done = i32([30, 10]), i32([1, 0])
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    dv.dv_page_release(s["pt"], s["lens"], done, s["ws"])
+    step(dv, s, x, n_tok, out)
+    dv.dv_prompt_attn(s["desc"], x[:, :4], x[:, 4:6], x[:, 6:], s["cu"], out, s["ws"])
+g.replay()
+assert dv.dv_check(s["ws"]) == 0 and torch.isfinite(out).all() and out.abs().sum() > 0
+st = torch.cuda.Stream()
+st.wait_stream(torch.cuda.current_stream())
+want = out.clone()
+out.zero_()
+torch.cuda.synchronize()
+dv.dv_prompt_attn(s["desc"], x[:, :4], x[:, 4:6], x[:, 6:], s["cu"], out, s["ws"], stream=st)
+st.synchronize()
+assert torch.equal(out, want)
+"""
+    import os
+
+    here = os.path.dirname(os.path.abspath(__file__))
+    subprocess.run([sys.executable, "-c", code % (os.path.dirname(here), here)], check=True,
+                   timeout=300)
+
+
+def test_wrappers_refuse(dv):
+    T, H, Hkv, D, page = 8, 4, 2, 64, 16
+    desc = dv.make_seq_desc(H, Hkv, D, dv.DV_F16, page, 10)
+    cache, ws, pt = dv.PagedCache(desc), dv.SeqWorkspace(desc), dv.PageTables(desc, 2, 3)
+    x = torch.zeros(T, H + 2 * Hkv, D, dtype=torch.float16, device="cuda")
+    q, k, v = x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:]
+    out = torch.zeros(T, H, D, dtype=torch.float16, device="cuda")
+    cu, lens, pos, slots = i32([0, 4, 8]), i32([0, 0]), i32(range(T)), i32(range(T))
+    r = dv.Rope(D, D)
+
+    def prompt(**kw):
+        a = dict(desc=desc, q=q, k=k, v=v, cu=cu, out=out, ws=ws)
+        a.update(kw)
+        dv.dv_prompt_attn(**a)
+
+    def paged(**kw):
+        a = dict(cache=cache, q=q, cu=cu, lens=lens, tables=pt.tables, out=out, ws=ws)
+        a.update(kw)
+        dv.dv_paged_attn(**a)
+
+    def rope(**kw):
+        a = dict(rope=r, q=q, k=k, pos=pos, ws=ws, q_out=out, v=v, cache=cache, slots=slots)
+        a.update(kw)
+        dv.dv_qk_rope(**a)
+
+    def take(**kw):
+        a = dict(pt=pt, lens=lens, n_tok=lens, cu=cu, pos=pos, slots=slots, ws=ws)
+        a.update(kw)
+        dv.dv_page_take(**a)
+
+    prompt(), rope(), take()
+    assert dv.dv_check(ws) == 0
+    bad = [(prompt, dict(q=q.float())), (prompt, dict(q=q[:, :3])), (prompt, dict(q=q[0])),
+           (prompt, dict(k=q)), (prompt, dict(v=v.cpu())), (prompt, dict(cu=cu.long())),
+           (prompt, dict(out=out.float())), (prompt, dict(out=x[:, :H])),
+           (prompt, dict(q=x.transpose(1, 2)[:, :H, :H])), (prompt, dict(scale=0.0)),
+           (prompt, dict(max_tok=0)), (paged, dict(lens=cu)), (paged, dict(tables=pt.tables[0])),
+           (paged, dict(lens=lens.cpu())), (paged, dict(q=q[:, :, :32])),
+           (rope, dict(k=q)), (rope, dict(slots=None)), (rope, dict(cache=None)),
+           (rope, dict(pos=pos[:4])), (rope, dict(rope=dv.Rope(32, 32))),
+           (rope, dict(q_out=out[:4])), (rope, dict(k=k.float())),
+           (take, dict(cu=cu[:2])), (take, dict(slots=slots[:4])), (take, dict(lens=lens.long()))]
+    for f, kw in bad:
+        with pytest.raises((ValueError, dv.DvError)):
+            f(**kw)
+    for f in (lambda: dv.PagedCache(dv.make_seq_desc(H, Hkv, D, dv.DV_F16)),
+              lambda: dv.PageTables(dv.make_seq_desc(H, Hkv, D, dv.DV_F16), 2, 3),
+              lambda: dv.SeqWorkspace(dv.make_seq_desc(H, 3, D, dv.DV_F16)),
+              lambda: dv.PagedCache(desc, tensors={"k": cache.k}),
+              lambda: dv.PagedCache(desc, tensors={"k": cache.k, "v": cache.v.float()}),
+              lambda: dv.Rope(D, 7), lambda: dv.Rope(D, D, theta=0.5),
+              lambda: dv.Rope(D, D, q_gain=torch.ones(3, device="cuda"))):
+        with pytest.raises((ValueError, dv.DvError)):
+            f()
+    assert dv.dv_check(ws) == 0
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 32), ("f16", 128), ("f16", 64)])
+def test_one_position_is_its_value(dv, dtype, D):
+    """A first token sees itself alone: its result is its value row, to the bit."""
+    c = Seqs(dv, [1, 3, 1, 200], [0] * 4, 2, 3, D, dtype)
+    c.run()
+    first = c.cu[:4]
+    np.testing.assert_array_equal(c.out.cpu().numpy()[first],
+                                  np.repeat(c.qkv[first, c.H + c.Hkv:], 3, 1))
