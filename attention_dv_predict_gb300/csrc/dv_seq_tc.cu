@@ -751,8 +751,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     for (int i = 8; i < TP; i += 2)
                         tops[i / 2 % 4] = max3(tops[i / 2 % 4], v[i], v[i + 1]);
                     const float high = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
+                    // From 2^24 on a score rounded (m) and the product in a multiply-add may
+                    // be further apart than the weights' range: both are the former then.
+                    const bool far = fabsf(high) >= 0x1p24f && high > -INFINITY;
                     const bool need = m == -INFINITY ? high > -INFINITY : high - m > kSeqLimit;
-                    if (__any_sync(0xffffffffu, need)) {  // (a row's first tile, or rarely)
+                    float sc = scale;
+                    if (__any_sync(0xffffffffu, need || far)) {  // (a row's first tile, or rarely)
+                        if (far) {
+                            sc = 1.f;
+#pragma unroll
+                            for (int i = 0; i < TP; ++i)
+                                v[i] *= scale;
+                        }
                         const float mn = need ? floorf(high) - kSeqShift : m;
                         const float f = need ? pow2(m - mn) : 1.f;
                         m = mn;
@@ -782,7 +792,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
                             float p = v[c + i], q = v[c + i + 1];
-                            fma2(p, q, scale, -ms);
+                            fma2(p, q, sc, -ms);
                             p = ex2(p);
                             q = ex2(q);
                             pr[i / 2] = h2(p, q);

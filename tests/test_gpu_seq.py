@@ -885,3 +885,32 @@ def test_one_position_is_its_value(dv, dtype, D):
     first = c.cu[:4]
     np.testing.assert_array_equal(c.out.cpu().numpy()[first],
                                   np.repeat(c.qkv[first, c.H + c.Hkv:], 3, 1))
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 32), ("f16", 128), ("f16", 64)])
+@pytest.mark.parametrize("page", [0, 16])
+def test_scores_of_any_size(dv, dtype, D, page):
+    """Equal scores near the end of the type's squares: the plain mean of the values.
+
+    Every position's score is the same sum of the same products, so the weights are
+    equal; n of them are summed with their values in binary32 (n 2^-24 of the sum of
+    |v|, twice for the sum and the quotient), and the result is rounded once.
+    """
+    n, big = 200, 6e4 if dtype == "f16" else 1e15
+    for sign in (1, -1):
+        c = Seqs(dv, [n, 1], [0, n if page else 0], 1, 2, D, dtype, page=page)
+        c.qkv[:, :2] = big
+        c.qkv[:, 2] = sign * big
+        if page:
+            c.pk[:] = sign * big
+        c.upload()
+        got = c.run().double().cpu().numpy()
+        assert dv.dv_check(c.ws) == 0
+        half = torch.finfo(TT[dtype]).eps / 2
+        for b in range(2):
+            V = c.V[b][0].astype(np.float64)
+            for i in range(c.toks[b]):
+                m = (c.lens[b] + i if page else i) + 1
+                want, size = V[:m].mean(0), np.abs(V[:m]).mean(0)
+                tol = half * np.abs(want) + 3 * m * 2.0 ** -24 * size
+                assert (np.abs(got[c.cu[b] + i] - want) <= tol).all()
