@@ -51,7 +51,8 @@ struct SeqMaps {
 
 // What a unit costs beside its tiles, and the shortest run, in places: swept over
 // single tokens, short and long prompts and a mix of them (a unit of 6: the mix 476
-// us, ragged prompts 374; of 12: 409 and 338; of 20: 416 and 346).
+// us, ragged prompts 374; of 12: 409 and 338; of 20: 416 and 346; with sums of rounded
+// weights and outputs set aside, both later, 12 takes 415 and 359).
 using TcSched = SeqSched<64, true, 12, 12>;
 
 // PAGED: keys and values of a pool.  Their tiles are laid out by groups of 8 rows,
@@ -77,6 +78,7 @@ struct SeqTcCfg {
                          OFF_CTL = OFF_OUT + 2 * OUT;
     static constexpr int T_S = 0, T_O = 256, T_COLS = 512;  // tensor-memory columns
     static constexpr int REC = 2 * RM * D + 4 * RM;      // floats of a piece's record
+    static constexpr int ACC = RM * D + RM;              // and of what a stream has set aside
     using Sched = TcSched;
 };
 
@@ -333,6 +335,52 @@ struct Plan {
 
 constexpr float kSeqShift = 6.f;   // the first tile's largest weight is 2^6 to 2^7
 constexpr float kSeqLimit = 15.f;  // a weight above 2^15 moves the reference
+// Tensor cores cut their sums off instead of rounding them: outputs of one sign lose
+// 3e-7 of themselves a tile (measured; 6e-4 over 262144 positions).  So after this
+// many tiles a stream sets its outputs aside, where they are added in binary32: 8e-5,
+// a sixth of binary16's half step.
+constexpr int kSeqFold = 256;
+
+// Outputs of a row are added to those set aside (`first`: there are none) and start
+// from zero again, or, `back`, return with them.  Whole warps.  Not inlined: between
+// the tiles' loops its code took 3 % of long prompts' time without ever running.
+template <class C>
+__device__ __noinline__ void seq_fold(float *rec, int stream, int row, unsigned tO, float m,
+                                      bool first, bool back)
+{
+    constexpr int RM = C::RM, D = C::D;
+    float *const acc = rec + 2 * (size_t)kSeqTcCtas * C::REC + (size_t)stream * C::ACC;
+    const float was = first ? -INFINITY : ld_cg(acc + RM * D + row);
+    const float f = was == -INFINITY ? 0.f : pow2(was - m);
+    tc_fence_after();
+#pragma unroll 1
+    for (int c = 0; c < D; c += 16) {
+        float y[16];
+        unsigned z[16];
+        tm_ld16(tO + c, y);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            float4 *const at = reinterpret_cast<float4 *>(acc) + (c + i) / 4 * RM + row;
+            float4 o = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            if (!first) {
+                const float4 g = __ldcg(at);
+                o = make_float4(fmaf(g.x, f, o.x), fmaf(g.y, f, o.y), fmaf(g.z, f, o.z),
+                                fmaf(g.w, f, o.w));
+            }
+            if (!back)
+                __stcg(at, o);
+            z[i] = back ? __float_as_uint(o.x) : 0u;
+            z[i + 1] = back ? __float_as_uint(o.y) : 0u;
+            z[i + 2] = back ? __float_as_uint(o.z) : 0u;
+            z[i + 3] = back ? __float_as_uint(o.w) : 0u;
+        }
+        tm_st16(tO + c, z);
+    }
+    if (!back)
+        __stcg(acc + RM * D + row, m);
+    tm_wait_st();
+    tc_fence_before();
+}
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
@@ -824,15 +872,27 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     bar_arrive(smem_addr(&ctl.p_full[w][buf]));
                 ++tiles;
             };
+            // (at rest behind the product before, like a rescaling)
+            auto fold = [&](bool first, bool back) {
+                wait(&ctl.o_full[w][(tiles - 1) & 1], (tiles - 1) >> 1);
+                __syncwarp();
+                seq_fold<C>(a.rec, 2 * run.c + w, row, tO, m, first, back);
+            };
             // (the first tile with an edge, of this stream's)
             const int plain = min(n, pl.pair ? pl.edge : (pl.edge + 1 - w) >> 1);
             int j = 0;
 #pragma unroll 1
-            for (; j < plain; ++j)
-                tile(j, std::false_type{});
+            while (j < n) {
+                if (j > 0 && busy)
+                    fold(j == kSeqFold, false);
+                const int stop = min(n, j + kSeqFold), inner = min(plain, stop);
 #pragma unroll 1
-            for (; j < n; ++j)
-                tile(j, std::true_type{});
+                for (; j < inner; ++j)
+                    tile(j, std::false_type{});
+#pragma unroll 1
+                for (; j < stop; ++j)
+                    tile(j, std::true_type{});
+            }
             edges += pl.n - pl.edge;
 
             // ---- the piece's end; the next one is found while its last product runs
@@ -844,6 +904,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (n > 0) {
                 wait(&ctl.o_full[w][(tiles - 1) & 1], (tiles - 1) >> 1);
                 tc_fence_after();
+                if (n > kSeqFold && busy)
+                    fold(false, true);
             }
             // Results go to shared memory, laid out as a copy to the output takes them: a
             // thread writing its own row took 7000 cycles a pair.
@@ -1173,7 +1235,8 @@ cudaError_t launch_seq_tc(const SeqAttnArgs &a, int nsm, cudaStream_t st)
 
 size_t seq_tc_record_bytes(int D)
 {
-    return 2 * (size_t)kSeqTcCtas * (2 * 128 * D + 4 * 128) * 4;
+    // two pieces' records a CTA, and what its streams set aside
+    return 2 * (size_t)kSeqTcCtas * (2 * 128 * D + 4 * 128 + 128 * D + 128) * 4;
 }
 
 }  // namespace dv

@@ -759,8 +759,10 @@ int dv_qk_rope(const dv_seq_desc *desc, const dv_rope *rope, int tokens, const i
  * Scores, sums and outputs are held in binary32.  Binary16 rows of 64 or 128
  * values run on tensor cores (tcgen05): a weight is rounded to binary16 (2^-11
  * of itself, or 2^-31 of the row's largest) for its value and for the sum; all
- * other arithmetic is binary32.  The order of every sum is fixed by the shapes, the
- * lengths and the device.
+ * other arithmetic is binary32, of which tensor cores cut sums off instead of rounding
+ * them: outputs lose at most 2^-13 of the sum of their terms' sizes, at any length.  A
+ * row whose seen scores are all -infinity (infinite keys) gives 0.  The order of every
+ * sum is fixed by the shapes, the lengths and the device.
  */
 int dv_prompt_attn(const dv_seq_desc *desc, int batch, int tokens, int max_tok,
                    const dv_kv_rows *q, const dv_kv_rows *k, const dv_kv_rows *v,

@@ -914,3 +914,55 @@ def test_scores_of_any_size(dv, dtype, D, page):
                 want, size = V[:m].mean(0), np.abs(V[:m]).mean(0)
                 tol = half * np.abs(want) + 3 * m * 2.0 ** -24 * size
                 assert (np.abs(got[c.cu[b] + i] - want) <= tol).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("tok", [1, 100, 200])
+def test_long_sums_are_not_cut_off(dv, tok, D):
+    """Outputs of one sign over many tiles of one stream: no bias.
+
+    A sum of the tensor cores may be short by a step of binary32 (2^-23) for each of its
+    products of 16 positions, 4 a tile of 64, and sums 256 tiles: 2^-13 of itself at
+    most.  All else rounds, so its mean over 8 heads x D outputs and the last tokens is
+    far smaller (a rounded weight and result: 2^-11 / sqrt(outputs)).
+    """
+    H, page, n = 8192 // D, 128, 1 << 17
+    desc = dv.make_seq_desc(H, H, D, dv.DV_F16, page, n // page)
+    ws, cache = dv.SeqWorkspace(desc), dv.PagedCache(desc)
+    g = torch.Generator("cuda").manual_seed(3)
+    cache.k.normal_(generator=g)
+    cache.v.uniform_(0.5, 1, generator=g)
+    q = torch.randn(tok, H, D, device="cuda", generator=g).half()
+    out = torch.empty_like(q)
+    tables = torch.arange(n // page, device="cuda").int().view(1, -1)
+    dv.dv_paged_attn(cache, q, i32([0, tok]), i32([n - tok]), tables, out, ws)
+    assert dv.dv_check(ws) == 0
+    means = []
+    for h in range(0, H, H // 8):
+        K, V = (t[:, h].reshape(n, D).double() for t in (cache.k, cache.v))
+        want = torch.softmax(K @ q[-1, h].double() * D ** -0.5, 0) @ V
+        rel = out[-1, h].double() / want - 1
+        assert rel.abs().max() <= 2 * 2.0 ** -11 + 2.0 ** -13
+        means.append(rel.mean().item())
+    assert abs(sum(means) / 8) <= 2.0 ** -13 + 4 * 2.0 ** -11 / math.sqrt(8 * D)
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 32), ("f16", 128), ("f16", 64)])
+def test_infinite_keys(dv, dtype, D):
+    """Keys of -infinity have no weight; a row that sees nothing else gives 0."""
+    n, dead = 300, 150
+    c = Seqs(dv, [n], [0], 1, 1, D, dtype)
+    c.qkv[:, 0] = np.abs(c.qkv[:, 0]) + NP[dtype](0.01)
+    c.qkv[:dead, 1] = -np.inf
+    c.upload()
+    got = c.run().double().cpu().numpy()
+    assert dv.dv_check(c.ws) == 0
+    assert (got[:dead] == 0).all()
+    q, K, V = (c.qkv[dead:, i].astype(np.float64) for i in range(3))
+    s = q @ K.T * D ** -0.5
+    w = np.tril(np.exp(s - s.max(1, keepdims=True)))
+    w /= w.sum(1, keepdims=True)
+    half = torch.finfo(TT[dtype]).eps / 2
+    # a weight and the result rounded once each, scores of at most max|s| in binary32
+    tol = (2 * half + 2.0 ** -20 * (1 + np.abs(s).max())) * (w @ np.abs(V))
+    assert (np.abs(got[dead:, 0] - w @ V) <= tol).all()
