@@ -966,3 +966,33 @@ def test_infinite_keys(dv, dtype, D):
     # a weight and the result rounded once each, scores of at most max|s| in binary32
     tol = (2 * half + 2.0 ** -20 * (1 + np.abs(s).max())) * (w @ np.abs(V))
     assert (np.abs(got[dead:, 0] - w @ V) <= tol).all()
+
+
+@pytest.mark.parametrize("tok", [1, 100, 200])
+@pytest.mark.parametrize("rise", [25.0, -25.0, 3.0])
+def test_long_sums_with_moving_references(dv, tok, rise):
+    """Scores that rise or fall over 2^17 positions: early parts keep their weight.
+
+    Values are in 0.5 to 1, so a weight's rounding (2^-11), the result's (2^-11), the tensor
+    cores' sums (2^-13) and scores of at most 32 in binary32 (8 D steps of 2^-24 of them, of
+    which a weight's relative error is that) bound the relative error.
+    """
+    D, H, page, n = 64, 128, 128, 1 << 17
+    desc = dv.make_seq_desc(H, H, D, dv.DV_F16, page, n // page)
+    ws, cache = dv.SeqWorkspace(desc), dv.PagedCache(desc)
+    g = torch.Generator("cuda").manual_seed(4)
+    cache.k.normal_(generator=g)
+    ramp = torch.linspace(0, rise, n, device="cuda").view(n // page, 1, page)
+    cache.k[..., 0] = (ramp * D ** 0.5 / 4).half()
+    cache.v.uniform_(0.5, 1, generator=g)
+    q = torch.randn(tok, H, D, device="cuda", generator=g).half() * 0.25
+    q[..., 0] = 4
+    out = torch.empty_like(q)
+    tables = torch.arange(n // page, device="cuda").int().view(1, -1)
+    dv.dv_paged_attn(cache, q, i32([0, tok]), i32([n - tok]), tables, out, ws)
+    assert dv.dv_check(ws) == 0
+    for h in range(0, H, H // 8):
+        K, V = (t[:, h].reshape(n, D).double() for t in (cache.k, cache.v))
+        want = torch.softmax(K @ q[-1, h].double() * D ** -0.5, 0) @ V
+        rel = out[-1, h].double() / want - 1
+        assert rel.abs().max() <= 2 * 2.0 ** -11 + 2.0 ** -13 + 8 * D * 2.0 ** -24 * 32
