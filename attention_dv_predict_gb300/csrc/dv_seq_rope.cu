@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5)
 
     // sines and cosines, by the lanes; then this lane's four pairs'
     float sn[4], cs[4];
+    unsigned turns = 0;  // which of them turn
     if (a.rot) {
         for (int i = lane; i < half; i += 32) {
             float s, c;
@@ -113,9 +114,10 @@ __global__ void __launch_bounds__(kRopeThreads, 5)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int i = split ? ca + e : 4 * part + e;  // the pair, if there is one
-            const bool turns = split ? ca < half : i < half;
-            sn[e] = turns ? s_sin[warp][i] : 0.f;
-            cs[e] = turns ? s_cos[warp][i] : 1.f;
+            const bool on = split ? ca < half : i < half;
+            turns |= (unsigned)on << e;
+            sn[e] = on ? s_sin[warp][i] : 0.f;
+            cs[e] = on ? s_cos[warp][i] : 1.f;
         }
     }
     float *const row = s_row[warp] + mine * D;
@@ -182,10 +184,14 @@ __global__ void __launch_bounds__(kRopeThreads, 5)
                         y[e] *= f * g[e];
                 }
                 if (turn && !odd) {
+                    // (a choice of the result: a value that does not turn may be infinite
+                    // or NaN, and a product with a sine of zero would spread it)
                     auto rotate = [&](float &p, float &q, int e) {
                         const float r = fmaf(p, cs[e], -q * sn[e]);
-                        q = fmaf(q, cs[e], p * sn[e]);
-                        p = r;
+                        const float u = fmaf(q, cs[e], p * sn[e]);
+                        const bool on = (turns >> e) & 1;
+                        p = on ? r : p;
+                        q = on ? u : q;
                     };
                     if (a.interleaved) {
 #pragma unroll

@@ -731,7 +731,8 @@ typedef struct {
  *   q, k, v: rows (t, h) (stride_b is not used), t < tokens; v NULL: no values.
  *   pos [tokens] device: positions; a token with a negative one is skipped.
  *   x' = x / sqrt(mean(x^2) + eps) gain (DV_LAYERNORM: of x less its mean), then
- *   each pair turns by its angle: (a, b) -> (a cos - b sin, b cos + a sin).
+ *   each pair turns by its angle: (a, b) -> (a cos - b sin, b cos + a sin).  Values
+ *   behind the first rot_dim do not turn: they are kept, infinities and NaN too.
  *   q_out: rows of the queries; may be q itself (same place, type, strides).
  *   k_out: rows of the keys, or NULL; may be k.  pool, slots [tokens]: where keys
  *   and values go (NULL: nowhere); a negative slot takes nothing, one out of

@@ -996,3 +996,45 @@ def test_long_sums_with_moving_references(dv, tok, rise):
         want = torch.softmax(K @ q[-1, h].double() * D ** -0.5, 0) @ V
         rel = out[-1, h].double() / want - 1
         assert rel.abs().max() <= 2 * 2.0 ** -11 + 2.0 ** -13 + 8 * D * 2.0 ** -24 * 32
+
+
+@pytest.mark.parametrize("src", ["f32", "f16"])
+@pytest.mark.parametrize("D,rot,interleaved", [
+    (128, 64, False), (128, 64, True), (128, 96, False), (128, 8, False), (64, 48, False),
+    (64, 20, False), (64, 2, True), (32, 12, True), (16, 10, True), (8, 4, False), (8, 2, True),
+    (256, 128, False), (256, 64, True), (128, 0, False)])
+def test_values_that_do_not_turn_are_kept(dv, src, D, rot, interleaved):
+    """Infinities, NaN and -0 behind the turned part stay where and what they are, to the bit (a
+    NaN: some NaN), and the turned part does not see them."""
+    T, H, Hkv = 13, 6, 2
+    dst = "f16" if D == 256 else src
+    qkv, pos, slots, cache, ws, r, want, page = rope_case(dv, T, H, Hkv, D, rot, src, dst,
+                                                          interleaved)
+    rng = np.random.default_rng(D + rot)
+    odd = rng.choice(np.array([np.inf, -np.inf, np.nan, -0.0, 0.0, 1.5]), qkv[..., rot:].shape)
+    qkv[..., rot:] = odd
+    x = dev(qkv)
+
+    def kept(got, rows, out):
+        got, rows = got.cpu().numpy(), rows.astype(NP[out])
+        nan = np.isnan(rows)
+        assert (np.isnan(got) == nan).all()
+        whole = np.uint32 if out == "f32" else np.uint16
+        np.testing.assert_array_equal(np.where(nan, 0, np.ascontiguousarray(got).view(whole)),
+                                      np.where(nan, 0, np.ascontiguousarray(rows).view(whole)))
+
+    for out in ("f32", "f16"):
+        q_out = torch.zeros(T, H, D, dtype=TT[out], device="cuda")
+        k_out = torch.zeros(T, Hkv, D, dtype=TT[out], device="cuda")
+        dv.dv_qk_rope(r, x[:, :H], x[:, H:H + Hkv], i32(pos), ws, q_out=q_out, k_out=k_out,
+                      v=x[:, H + Hkv:], cache=cache, slots=i32(slots))
+        assert dv.dv_check(ws) == 0
+        for got, lo, w in ((q_out, 0, want[0]), (k_out, H, want[1])):
+            kept(got[..., rot:], qkv[:, lo:lo + got.shape[1], rot:], out)
+            if rot:
+                close(got[..., :rot], *(y[..., :rot] for y in rounded(w, out)))
+    stored = pool_rows(cache.k, slots, page)
+    kept(stored[..., rot:], qkv[:, H:H + Hkv, rot:], dst)
+    if rot:
+        close(stored[..., :rot], *(y[..., :rot] for y in rounded(want[1], dst)))
+    kept(pool_rows(cache.v, slots, page), qkv[:, H + Hkv:], dst)
