@@ -335,11 +335,16 @@ struct Plan {
 
 constexpr float kSeqShift = 6.f;   // the first tile's largest weight is 2^6 to 2^7
 constexpr float kSeqLimit = 15.f;  // a weight above 2^15 moves the reference
-// Tensor cores cut their sums off instead of rounding them: outputs of one sign lose
-// 3e-7 of themselves a tile (measured; 6e-4 over 262144 positions).  So after this
-// many tiles a stream sets its outputs aside, where they are added in binary32: 8e-5,
-// a sixth of binary16's half step.
-constexpr int kSeqFold = 256;
+// Tensor cores cut off what they add instead of rounding it: of the 16 products of a
+// step and the sum before them each below 2^-25 of the largest of these, and the new sum
+// below 2^-23 of itself (measured, with terms of chosen sizes).  A tile is four steps, so
+// outputs could lose 5.25 x 2^-21 of the sum of their terms' sizes a tile.  After this
+// many tiles a stream sets its outputs aside, where they are added in binary32: 1.6e-4 at
+// most, a third of binary16's half step, and 3.5e-5 in the mean over 262144 positions of one
+// sign (256 tiles: 6.4e-4, seen 2.4e-4 beside a term that outweighs the others; 9.5e-5).  It
+// costs 4 % of two prompts of 16384 and 7 % of 2048 tokens after 30000, against 256 tiles;
+// 48 tiles cost 3 % more, in decode too.
+constexpr int kSeqFold = 64;
 
 // Outputs of a row are added to those set aside (`first`: there are none) and start
 // from zero again, or, `back`, return with them.  Whole warps.  Not inlined: between

@@ -761,7 +761,7 @@ int dv_qk_rope(const dv_seq_desc *desc, const dv_rope *rope, int tokens, const i
  * values run on tensor cores (tcgen05): a weight is rounded to binary16 (2^-11
  * of itself, or 2^-31 of the row's largest) for its value and for the sum; all
  * other arithmetic is binary32, of which tensor cores cut sums off instead of rounding
- * them: outputs lose at most 2^-13 of the sum of their terms' sizes, at any length.  A
+ * them: outputs lose at most 5.25 x 2^-15 (1.6e-4) of the sum of their terms' sizes.  A
  * row whose seen scores are all -infinity (infinite keys) gives 0.  The order of every
  * sum is fixed by the shapes, the lengths and the device.
  */

@@ -1038,3 +1038,89 @@ def test_values_that_do_not_turn_are_kept(dv, src, D, rot, interleaved):
     if rot:
         close(stored[..., :rot], *(y[..., :rot] for y in rounded(want[1], dst)))
     kept(pool_rows(cache.v, slots, page), qkv[:, H + Hkv:], dst)
+
+
+# What tensor cores may cut off of a sum, of the sum of its terms' sizes: 64 tiles of 64 positions
+# between additions in binary32 are 256 products of 16 terms; each cuts its terms and the sum before
+# them (17) off below 2^-25 of the largest, and the new sum below 2^-23 of itself.
+CUT = 256 * (17 * 2.0 ** -25 + 2.0 ** -23)
+
+
+def shared_cache(dv, B, tok, N, D, seed):
+    """B requests of one query head over the same N cached positions (whole units of attention,
+    at least one for every CTA), their descriptor and what the calls take beside queries."""
+    page = 128
+    desc = dv.make_seq_desc(1, 1, D, dv.DV_F16, page, N // page)
+    cache = dv.PagedCache(desc)
+    tables = i32(range(N // page))[None].expand(B, -1).contiguous()
+    args = i32(range(0, B * tok + 1, tok)), i32([N - tok] * B), tables
+    out = torch.zeros(B * tok, 1, D, dtype=torch.float16, device="cuda")
+    return cache, args, out, torch.Generator("cuda").manual_seed(seed)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("tok,B", [(1, 304), (40, 304), (200, 152)])
+def test_small_terms_beside_large_ones(dv, tok, B, D):
+    """A term that outweighs 16384 others 2^25 times, and its opposite behind them: what is left is
+    the others' sum.
+
+    Weights are powers of two (exact in binary16); the sum loses CUT of the terms' sizes; binary32
+    adds the tiles' sums of weights (2^-24 each, at most 512) and forms the quotient; the result
+    is rounded once (2^-11, or 2^-25)."""
+    pair = tok > 128
+    nt = 256 if pair else 512  # 256 tiles a stream
+    N = nt * 64
+    cache, args, out, gen = shared_cache(dv, B, tok, N, D, D + tok)
+    K, V = torch.zeros(N, D, device="cuda"), torch.zeros(N, D, device="cuda")
+    K[:, 0] = -25.0
+    for d, v in enumerate((1 - 2.0 ** -10, 1.0, 0.75, 0.5)):
+        V[:, d::4] = v
+    # (the two streams of a unit of up to 128 rows have every other tile each)
+    for p, sign in ((0, 1.0), ((nt - 6) * 64 + 5, -1.0)):
+        for at in ([p] if pair else [p, p + 64]):
+            K[at, 0], V[at] = 0.0, sign
+    cache.k.copy_(K.view(cache.k.shape))
+    cache.v.copy_(V.view(cache.v.shape))
+    q = torch.zeros(B * tok, 1, D, dtype=torch.float16, device="cuda")
+    q[:, 0, 0] = 1
+    ws = dv.SeqWorkspace(cache.desc)
+    dv.dv_paged_attn(cache, q, *args, out, ws, max_tok=tok, scale=math.log(2))
+    assert dv.dv_check(ws) == 0
+    w = torch.exp2(K[:, 0].double())
+    seen = torch.arange(N, device="cuda") <= torch.arange(N - tok, N, device="cuda")[:, None]
+    p = w * seen
+    p /= p.sum(1, keepdim=True)
+    want, size = p @ V.double(), p @ V.double().abs()
+    tol = CUT * size + want.abs() * (2.0 ** -11 + 514 * 2.0 ** -24) + 2.0 ** -25
+    for b in range(B):
+        close(out[b * tok:(b + 1) * tok, 0], want.cpu().numpy(), tol.cpu().numpy())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("tok,B", [(1, 304), (200, 152)])
+def test_long_sums_of_whole_units(dv, tok, B, D):
+    """Positive values over 262144 positions, no unit cut: 2048 tiles (a pair: 4096) of a stream.
+
+    Each output: CUT, 2^-11 for the weights' rounding and 2^-11 for the result's, and binary32: a
+    score's error, at most (D + 16) 2^-23 of its products' sizes (as in seq_ref, twice in a weight),
+    and at most 4096 + 64 additions of 2^-24.  The mean: roundings are of either sign, so the mean of
+    them over 4096 outputs and more is under 4 x 2^-11 / 64, and what is left is within CUT.  Sums
+    that are never set aside lose 6e-4 in the mean, three times what is allowed."""
+    N = 1 << 18
+    cache, args, out, gen = shared_cache(dv, B, tok, N, D, 7 * D + tok)
+    cache.k.normal_(generator=gen)
+    cache.v.uniform_(0.5, 1, generator=gen)
+    q = torch.randn(B * tok, 1, D, generator=gen, device="cuda").half()
+    ws = dv.SeqWorkspace(cache.desc)
+    dv.dv_paged_attn(cache, q, *args, out, ws, max_tok=tok)
+    assert dv.dv_check(ws) == 0
+    K, V = cache.k.view(N, D).double(), cache.v.view(N, D).double()
+    rows = torch.arange(0, B * tok, max(1, B * tok // 64), device="cuda")[:64]
+    s = q[rows, 0].double() @ K.T * D ** -0.5
+    big = (q[rows, 0].double().abs() @ K.abs().T).amax(1, keepdim=True) * D ** -0.5
+    s.masked_fill_(torch.arange(N, device="cuda") > (N - tok + rows % tok)[:, None], -math.inf)
+    want = torch.softmax(s, 1) @ V
+    r = out[rows, 0].double() / want - 1
+    tol = CUT + 2 * 2.0 ** -11 + 2 * (D + 16) * 2.0 ** -23 * big + 4160 * 2.0 ** -24
+    assert (r.abs() <= tol).all(), (r.abs().max().item(), tol.min().item())
+    assert r.mean().abs() <= CUT + 4 * 2.0 ** -11 / 64, r.mean().item()
