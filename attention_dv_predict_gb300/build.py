@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libdv.so")
 SOURCES = ["dv_abi.cu", "dv_rowdot.cu", "dv_colacc.cu", "dv_colacc_mma.cu", "dv_attn.cu",
            "dv_select.cu", "dv_stream.cu", "dv_mlp.cu", "dv_kv_abi.cu", "dv_kv_write.cu",
            "dv_kv_topk.cu", "dv_kv_attn.cu", "dv_kv_mma.cu", "dv_kv_tc.cu", "dv_seq_abi.cu",
-           "dv_seq_pages.cu", "dv_seq_rope.cu", "dv_seq_attn.cu",
+           "dv_seq_pages.cu", "dv_rope_steps.cpp", "dv_seq_rope.cu", "dv_seq_attn.cu",
            "dv_seq_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -139,11 +139,6 @@ dv_status attn_launch(SeqAttnArgs &a, void *stream)
     return cuda_status(on_tc(a.f16, a.D) ? launch_seq_tc(a, nsm, st) : launch_seq_attn(a, nsm, st));
 }
 
-double dim_of_turns(double turns, int rot, double theta, double orig)
-{
-    return rot * std::log(orig / (turns * 2 * 3.14159265358979323846)) / (2 * std::log(theta));
-}
-
 }  // namespace
 
 namespace dv {
@@ -247,47 +242,6 @@ int dv_page_take(const dv_seq_desc *desc, int batch, const int32_t *lens, const 
     a.cnt = at<int>(ws, kSeqPageCnt);
     a.status = at<int>(ws, 0);
     return cuda_status(launch_page_take(a, static_cast<cudaStream_t>(stream)));
-}
-
-int dv_rope_steps(int rot_dim, double theta, int scaling, double factor, double orig_len,
-                  double low, double high, uint64_t *steps)
-{
-    const double tau = 2 * 3.14159265358979323846;
-    if (rot_dim < 2 || rot_dim % 2 || rot_dim > 256 || !(theta > 1) || !std::isfinite(theta) ||
-        !steps || scaling < DV_ROPE_NONE || scaling > DV_ROPE_RAMP_INDEX)
-        return DV_ERR_INVALID_ARG;
-    if (scaling != DV_ROPE_NONE && (!(factor >= 1) || !std::isfinite(factor)))
-        return DV_ERR_INVALID_ARG;
-    const bool ramp = scaling == DV_ROPE_RAMP || scaling == DV_ROPE_RAMP_INDEX;
-    if (ramp && (!(orig_len > 0) || !std::isfinite(orig_len) || !(low < high) || !(low > 0) ||
-                 !std::isfinite(high)))
-        return DV_ERR_INVALID_ARG;
-    if (scaling == DV_ROPE_BASE) {
-        if (rot_dim == 2)
-            return DV_ERR_INVALID_ARG;
-        theta *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
-    }
-    double i0 = 0, i1 = 0;
-    if (scaling == DV_ROPE_RAMP_INDEX) {
-        i0 = std::fmax(std::floor(dim_of_turns(high, rot_dim, theta, orig_len)), 0);
-        i1 = std::fmin(std::ceil(dim_of_turns(low, rot_dim, theta, orig_len)), rot_dim - 1);
-        if (i0 == i1)
-            i1 += 0.001;
-    }
-    for (int i = 0; i < rot_dim / 2; ++i) {
-        double f = std::pow(theta, -2.0 * i / rot_dim), w = 1;
-        if (scaling == DV_ROPE_RAMP)
-            w = (orig_len * f / tau - low) / (high - low);
-        if (scaling == DV_ROPE_RAMP_INDEX)
-            w = 1 - (i - i0) / (i1 - i0);
-        w = std::fmin(std::fmax(w, 0), 1);
-        if (scaling == DV_ROPE_LINEAR)
-            f /= factor;
-        else if (ramp)
-            f *= w + (1 - w) / factor;
-        steps[i] = (uint64_t)std::llrint(std::ldexp(f / tau, 64));
-    }
-    return DV_OK;
 }
 
 int dv_qk_rope(const dv_seq_desc *desc, const dv_rope *rope, int tokens, const int32_t *pos,

@@ -696,10 +696,11 @@ int dv_page_take(const dv_seq_desc *desc, int batch, const int32_t *lens, const 
  *   DV_ROPE_RAMP    f_i (w + (1 - w) / factor), w rising from 0 to 1 as the
  *                   turns over the trained length, orig_len f_i / 2 pi, rise
  *                   from low to high
- *   DV_ROPE_RAMP_INDEX  the same with w falling from 1 to 0 as i rises from
- *                   floor(dim(high)) to ceil(dim(low)) (held within 0 ..
- *                   rot_dim - 1), dim(r) = rot_dim ln(orig_len / 2 pi r) / (2 ln
- *                   theta): the pair that makes r turns */
+ *   DV_ROPE_RAMP_INDEX  the same with w = 1 - (i - a) / (b - a) held within 0 .. 1:
+ *                   falling over the pairs a = max(floor(dim(high)), 0) to b =
+ *                   min(ceil(dim(low)), rot_dim - 1) (b + 0.001 where they are
+ *                   equal), dim(r) = rot_dim ln(orig_len / 2 pi r) / (2 ln theta):
+ *                   the pair that makes r turns */
 typedef enum {
     DV_ROPE_NONE = 0,
     DV_ROPE_LINEAR = 1,
@@ -709,9 +710,11 @@ typedef enum {
 } dv_rope_scaling;
 
 /* The angles as the kernel takes them, turns per position in units of 2^-64:
- * steps (HOST) [rot_dim / 2], to be copied to the device once.  An angle is the
- * product with the position modulo 2^64, so it is as exact at position 2^30 as
- * at the first.  theta > 1, 1 <= factor, orig_len, low < high where used. */
+ * steps (HOST) [rot_dim / 2], to be copied to the device once.  A step is the exact
+ * angle of these parameters rounded to the nearest unit, and a kernel's angle its
+ * product with the position modulo 2^64: off by at most half a unit a position,
+ * 2^-35 of a turn at position 2^30.  theta > 1, 1 <= factor, orig_len, low < high
+ * where used. */
 int dv_rope_steps(int rot_dim, double theta, int scaling, double factor, double orig_len,
                   double low, double high, uint64_t *steps);
 
@@ -737,8 +740,9 @@ typedef struct {
  *   k_out: rows of the keys, or NULL; may be k.  pool, slots [tokens]: where keys
  *   and values go (NULL: nowhere); a negative slot takes nothing, one out of
  *   range neither (recorded).  v goes to the pool alone, as it is.
- * Outputs otherwise overlap nothing.  Arithmetic is binary32, angles are exact
- * to 2^-31 of a turn; a row is rounded once, when it is stored.
+ * Outputs otherwise overlap nothing.  Arithmetic is binary32; an angle is that of
+ * its step to 2^-33 of a turn at any position, a sine or cosine within 2^-22 of the
+ * angle's; a row is rounded once, when it is stored.
  */
 int dv_qk_rope(const dv_seq_desc *desc, const dv_rope *rope, int tokens, const int32_t *pos,
                const dv_kv_rows *q, const dv_kv_rows *k, const dv_kv_rows *v,

@@ -183,3 +183,58 @@ def test_the_plain_forms_on_small_cases():
     got, _ = seq_ref.attend(np.zeros((2, 2)), np.ones((3, 2)), np.arange(6.0).reshape(3, 2), [0, 1],
                             1.0, False)
     np.testing.assert_allclose(got, [[0, 1], [1, 2]])
+
+
+@pytest.mark.parametrize("rot", [2, 4, 6, 64, 96, 128, 256])
+@pytest.mark.parametrize("scaling", ["none", "linear", "base", "ramp", "ramp_index"])
+@pytest.mark.parametrize("theta,factor,orig,low,high", [
+    (10000.0, 8.0, 4096.0, 1.0, 32.0), (500000.0, 3.7, 8192.0, 1.0, 4.0),
+    (1000003.7, 1.0, 131072.0, 0.3, 1.1), (1.7e308, 1e300, 1e6, 1e-3, 64.0),
+    (1.0000001, 40.0, 10000.0, 1.0, 32.0)])
+def test_rope_steps_are_rounded_from_the_exact_angle(dv, rot, scaling, theta, factor, orig, low,
+                                                     high):
+    """Half a unit of 2^-64 turns (and 2^-20 of one for binary128's own roundings: 113 bits of a
+    number below 2^62 are 2^-51 of a unit, some hundred times): 80 digits decide."""
+    import decimal
+
+    if scaling == "base" and rot == 2:
+        pytest.skip("refused: no other pair to stretch")
+    host = (C.c_uint64 * (rot // 2))()
+    assert dv._lib.dv_rope_steps(rot, theta, dv.DV_ROPE_SCALING[scaling], factor, orig, low, high,
+                                 host) == 0
+    with decimal.localcontext() as ctx:
+        ctx.prec = 80
+        X = decimal.Decimal
+
+        def arctan_inverse(n):
+            total = term = X(1) / n
+            k = 1
+            while abs(term) > X(10) ** -85:
+                term = -term / (n * n)
+                k += 2
+                total += term / k
+            return total
+
+        pi = 4 * (4 * arctan_inverse(5) - arctan_inverse(239))  # (Machin)
+        th, fa, og, lo, hi = (X(v) for v in (theta, factor, orig, low, high))
+        log = th.ln()
+        if scaling == "base":
+            log += fa.ln() * rot / (rot - 2)
+        for i in range(rot // 2):
+            f = (-2 * i * log / rot).exp()
+            w = X(1)
+            if scaling == "ramp":
+                w = (og * f / (2 * pi) - lo) / (hi - lo)
+            if scaling == "ramp_index":
+                a, b = (rot * (og / (2 * pi * r)).ln() / (2 * log) for r in (hi, lo))
+                a = max(a.to_integral_value(decimal.ROUND_FLOOR), X(0))
+                b = min(b.to_integral_value(decimal.ROUND_CEILING), X(rot - 1))
+                b += X(0.001) if a == b else 0
+                w = 1 - (i - a) / (b - a)
+            w = min(max(w, X(0)), X(1))
+            if scaling == "linear":
+                f /= fa
+            elif scaling.startswith("ramp"):
+                f *= w + (1 - w) / fa
+            off = abs(X(host[i]) - f / (2 * pi) * 2 ** 64)
+            assert off <= X(0.5) + X(2) ** -20, (i, off)
