@@ -1124,3 +1124,80 @@ def test_long_sums_of_whole_units(dv, tok, B, D):
     tol = CUT + 2 * 2.0 ** -11 + 2 * (D + 16) * 2.0 ** -23 * big + 4160 * 2.0 ** -24
     assert (r.abs() <= tol).all(), (r.abs().max().item(), tol.min().item())
     assert r.mean().abs() <= CUT + 4 * 2.0 ** -11 / 64, r.mean().item()
+
+
+@pytest.mark.parametrize("args", [([300, 1, 129], [4000, 9000, 0], 2, 4, 128, "f16", 16),
+                                  ([1] * 12, list(range(0, 6000, 500)), 2, 2, 64, "f16", 32),
+                                  ([100, 7], [900, 0], 2, 2, 32, "f32", 16),
+                                  ([700, 1, 90], [0] * 3, 1, 5, 128, "f16")])
+def test_a_request_alone(dv, args):
+    """A request's rows alone in a call and in a batch: each within the bound of seq_ref, so at most
+    twice that apart (other requests move cuts between CTAs, and with max_tok the grouping)."""
+    c = Seqs(dv, *args)
+    got = c.run().double().cpu().numpy()
+    assert dv.dv_check(c.ws) == 0
+    want, tol = c.want()
+    cu, lens, tables = c.cu, c.lens, getattr(c, "tables", None)
+    x = c.x
+    for b in range(len(cu) - 1):
+        n = int(cu[b + 1] - cu[b])
+        rows = slice(cu[b], cu[b + 1])
+        c.x = x[cu[b]:cu[b + 1]].contiguous()
+        c.d_cu = i32([0, n])
+        if c.page:
+            c.d_lens, c.d_tables = i32(lens[b:b + 1]), i32(tables[b:b + 1])
+        for max_tok in (None, n):
+            out = torch.zeros(n, c.H, c.D, dtype=c.out.dtype, device="cuda")
+            c.run(max_tok=max_tok, out=out)
+            assert dv.dv_check(c.ws) == 0
+            close(out, want[rows], tol[rows])
+            close(out, got[rows], 2 * tol[rows])
+
+
+@pytest.mark.parametrize("dtype,D", [("f16", 128), ("f16", 64), ("f32", 32)])
+@pytest.mark.parametrize("G", [5, 10, 11])
+def test_groups_that_fill_no_unit(dv, G, D, dtype):
+    """Mixed steps whose query heads a KV head leave much of a unit's rows empty: tight, loose and
+    default bounds on the tokens, which choose other groups."""
+    toks, lens = [1, 40, 1, 0, 1, 150, 1], [700, 30, 0, 9, 65, 128, 2000]
+    c = Seqs(dv, toks, lens, 2, G, D, dtype, 16)
+    for max_tok in (150, None):
+        c.check(max_tok=max_tok)
+    Seqs(dv, [1] * 20, list(range(0, 1000, 50)), 1, G, D, dtype, 16).check()
+
+
+@pytest.mark.parametrize("dtype,D,tok,N", [
+    ("f16", 64, 1, (1 << 30) - 77), ("f16", 128, 200, (1 << 30) - 77), ("f16", 128, 40, 1 << 30),
+    ("f32", 32, 1, (1 << 26) - 9)])
+def test_longest_requests(dv, dtype, D, tok, N):
+    """A block table of up to 2^30 positions (61 pages over and over): a position's weight times
+    how often it is seen.
+
+    Bounds: scores as in seq_ref; binary16: CUT, and 2^-11 each for the weights and the result;
+    additions in binary32 of 2^-24 each: of a CTA's tiles (152 CTAs; 64 more within a tile and where
+    pieces meet) or, on CUDA cores, of its positions (608 CTAs), in numerator and denominator."""
+    page, P = 128, 61
+    desc = dv.make_seq_desc(1, 1, D, dv.DV_F16 if dtype == "f16" else dv.DV_F32, page, P)
+    cache, ws = dv.PagedCache(desc), dv.SeqWorkspace(desc)
+    g = torch.Generator("cuda").manual_seed(D + tok)
+    cache.k.normal_(generator=g)
+    cache.v.uniform_(0.5, 1, generator=g)
+    tables = (torch.arange(seq_ref.pages(N, page), device="cuda") % P).int()[None].contiguous()
+    q = torch.randn(tok, 1, D, generator=g, device="cuda").to(TT[dtype])
+    out = torch.zeros_like(q)
+    dv.dv_paged_attn(cache, q, i32([0, tok]), i32([N - tok]), tables, out, ws, max_tok=tok)
+    assert dv.dv_check(ws) == 0
+    K, V = (t.view(-1, D).double() for t in (cache.k, cache.v))
+    s = q[:, 0].double() @ K.T * D ** -0.5
+    big = (q[:, 0].double().abs() @ K.abs().T).amax(1, keepdim=True) * D ** -0.5
+    n = torch.arange(N - tok + 1, N + 1, device="cuda")[:, None]
+    times = n // (P * page) + (torch.arange(P * page, device="cuda") < n % (P * page))
+    w = torch.exp(s - s.amax(1, keepdim=True)) * times
+    want = w @ V / w.sum(1, keepdim=True)
+    tol = 2 * (D + 16) * 2.0 ** -23 * big
+    if dtype == "f16":
+        tol = tol + CUT + 2 * 2.0 ** -11 + (N / 64 / 152 + 64) * 2.0 ** -24
+    else:
+        tol = tol + 2 * (N / 608 + 1024) * 2.0 ** -24
+    r = (out[:, 0].double() / want - 1).abs()
+    assert (r <= tol).all(), (r.max().item(), tol.min().item())
