@@ -70,7 +70,7 @@ struct SeqAttnArgs {
     int *status;
 };
 
-// Largest number of KV-head groups' query rows in `rows` rows (dv_seq_abi.cu).
+// Sets group, tlog and sub for units of `rows` query rows (dv_seq_abi.cu).
 void seq_group(SeqAttnArgs &a, int rows);
 
 cudaError_t launch_page_release(const SeqReleaseArgs &a, cudaStream_t st);

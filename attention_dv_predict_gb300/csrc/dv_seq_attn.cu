@@ -243,15 +243,15 @@ cudaError_t launch_gen(SeqAttnArgs a, int nsm, cudaStream_t st)
 template <typename T>
 cudaError_t launch_type(const SeqAttnArgs &a, int nsm, cudaStream_t st)
 {
+    constexpr bool HALF = sizeof(T) == 2;  // (64 and 128 of them are the tensor cores')
     switch (a.D) {
     case 8: return launch_gen<T, 8>(a, nsm, st);
     case 16: return launch_gen<T, 16>(a, nsm, st);
     case 32: return launch_gen<T, 32>(a, nsm, st);
-    case 64: return launch_gen<T, 64>(a, nsm, st);
-    case 128: return launch_gen<T, 128>(a, nsm, st);
-    case 256:
-        if constexpr (sizeof(T) == 2)
-            return launch_gen<T, 256>(a, nsm, st);
+    case HALF ? 256 : 64: return launch_gen<T, HALF ? 256 : 64>(a, nsm, st);
+    case 128:
+        if constexpr (!HALF)
+            return launch_gen<T, 128>(a, nsm, st);
     default: return cudaErrorInvalidValue;
     }
 }

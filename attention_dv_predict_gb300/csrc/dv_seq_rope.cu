@@ -254,8 +254,8 @@ template <bool SRC16, int D>
 cudaError_t launch_rope_d(const SeqRopeArgs &a, cudaStream_t st)
 {
     constexpr int RPW = 32 / (D / 8), NW = kRopeThreads / 32;
-    // Runs of 32 rows, shorter ones where that leaves fewer than 32 warps an SM; the
-    // fewest rows are one of every lane group.
+    // Runs of 32 rows, shorter ones where that leaves fewer than 152 x 32 warps (an SM
+    // holds 20 at a time); the fewest rows are one of every lane group.
     int per = 32 / RPW * RPW, q_runs, runs;
     for (;; per -= RPW) {
         q_runs = (a.H + per - 1) / per;

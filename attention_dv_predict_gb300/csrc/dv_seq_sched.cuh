@@ -71,7 +71,7 @@ template <int TP_, bool PAIR_, int COST_, int MIN_RUN_>
 struct SeqSched {
     static constexpr int TP = TP_, COST = COST_, MIN_RUN = MIN_RUN_;
     static constexpr bool PAIR = PAIR_;
-    static constexpr int TPLOG = TP == 128 ? 7 : 6;
+    static constexpr int TPLOG = 6;
     static_assert(TP == 1 << TPLOG && MIN_RUN >= 4, "a run holds a tile's start");
 
     DV_DEV static int tiles(int len, int e) { return (int)(((long long)len + e + TP - 1) >> TPLOG); }
