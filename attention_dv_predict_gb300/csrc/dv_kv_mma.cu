@@ -216,8 +216,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
         for (int i = 0; i < NT; ++i)
             o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         float m = -INFINITY, l = 0.f;  // reference point, sum
-        // Tensor cores cut their sums off instead of rounding them: every step
-        // takes up to 2^-23 of a value, always towards zero.  So the values of
+        // Tensor cores cut their terms and sums off instead of rounding them: every
+        // step takes up to 5.25 x 2^-23 of a value, always towards zero.  So the values of
         // FLUSH tiles at a time are added here in binary32 (in local memory,
         // on purpose: as registers they would cost a CTA per SM).
         volatile float acc[NT * 2 + 1];  // values; sum

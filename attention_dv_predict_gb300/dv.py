@@ -890,7 +890,8 @@ def dv_prompt_attn(desc: SeqDesc, q: torch.Tensor, k: torch.Tensor, v: torch.Ten
                    max_tok: Optional[int] = None, scale: Optional[float] = None, stream=None):
     """Causal attention of packed prompts: q, out [T, H, D], k, v [T, Hkv, D], cu [B + 1] (int32).
 
-    max_tok: the most tokens of a request (T by default); scale: head_dim ** -0.5 by default."""
+    max_tok: the most tokens of a request (T by default; the kernel is chosen by it, so a tight
+    bound is faster); scale: head_dim ** -0.5 by default."""
     st = _seq_dev(ws, stream)
     T, B = _kv_dim("q", q, 3, 0), _kv_dim("cu", cu, 1, 0) - 1
     shape, kv = (T, desc.n_heads, desc.head_dim), (T, desc.n_kv_heads, desc.head_dim)
@@ -906,7 +907,8 @@ def dv_paged_attn(cache: PagedCache, q: torch.Tensor, cu: torch.Tensor, lens: to
                   max_tok: Optional[int] = None, scale: Optional[float] = None, stream=None):
     """Causal attention of new tokens q [T, H, D] over their requests' pages, into out [T, H, D].
 
-    cu [B + 1], lens [B], tables [B, max_pages] int32; max_tok, scale as dv_prompt_attn's."""
+    cu [B + 1], lens [B], tables [B, max_pages] int32; max_tok, scale as dv_prompt_attn's (decode
+    wants max_tok=1: the default may take several times as long)."""
     d = cache.desc
     st = _seq_dev(ws, stream, cache)
     T, B, P = _kv_dim("q", q, 3, 0), _kv_dim("cu", cu, 1, 0) - 1, _kv_dim("tables", tables, 2, 1)
