@@ -4,8 +4,8 @@
 // A kernel multiplies a step by positions up to 2^31, so a step is worth no more
 // than its last bits: in binary64 the fastest pairs would be off by some hundred
 // units (2^-25 of a turn at position 2^30).  Everything is held in binary128
-// (113 bits) and rounded once.  g++ computes binary128 in software on both
-// machines, so the steps are the same on both.
+// (113 bits) and rounded once.  g++ computes binary128 in software on x86 and on Arm
+// (where it is long double), so the steps are the same on both.
 #include <cmath>
 
 #include "dv.h"
