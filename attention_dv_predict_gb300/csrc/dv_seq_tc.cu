@@ -34,7 +34,7 @@
 // range, so the outputs are rarely rescaled.
 //
 // A weight is one binary16 number (2^-11 of itself), rounded as the result is: both
-// together leave 2.6e-4 to 2.9e-4 of the results against 64 bits, the result's own
+// together leave 2.6e-4 to 3e-4 of the results against 64 bits, the result's own
 // rounding alone 2.1e-4.  Two parts, as the operators with binary32 results have, would
 // be a second value product, 256 cycles more beside the 640 of a stream's tile.
 //
